@@ -80,7 +80,8 @@ typedef enum mla_status {
   MLA_ERR_BAD_POSITION = 7,    /* a position outside [0, max_pos) was seen (and clamped)  */
   MLA_ERR_NO_MEMORY = 8,       /* workspace allocation failed in create                   */
   MLA_ERR_WRONG_MODE = 9,      /* run of one quant mode on a handle made for the other    */
-  MLA_ERR_BAD_SLOT = 10        /* a paged-cache slot past the cache was seen (row dropped)*/
+  MLA_ERR_BAD_SLOT = 10,       /* a paged-cache slot past the cache was seen (row dropped)*/
+  MLA_ERR_BAD_LENGTH = 11      /* a sequence length or offset out of range was seen       */
 } mla_status;
 
 typedef enum mla_dtype { MLA_F16 = 0, MLA_BF16 = 1 } mla_dtype;
@@ -351,6 +352,154 @@ mla_status mla_kv_prolog_run_noalloc(const mla_prolog_config* cfg, int b, int s,
                                      const float* cos_table, const float* sin_table,
                                      void* k_nope, void* value, void* k_pe,
                                      unsigned int* device_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention on the prolog's outputs.  Three operators that share a handle
+ * (mla_attn): the append of new tokens to a paged latent cache, the
+ * attention of new tokens over that cache (decode, multi-token decode and
+ * chunks, in the form that absorbs kv_b_proj into query and output
+ * projections), and the attention over whole prompts on the up-projected
+ * k_nope / value / k_pe of mla_kv_prolog_run.
+ *
+ * The conventions at the top of this file hold (device pointers 16-byte
+ * aligned, nothing allocated or synchronised by a call, faults that the
+ * device detects recorded and read by mla_attn_status).  Rows may be strided:
+ * strides are in elements, multiples of 8, at least the row's width (a
+ * stride along a dimension of size 1 is not read); a row itself is
+ * contiguous.  The calls run on the device that was current in create.
+ * One handle holds one workspace: calls of it on two streams (or in two
+ * graphs that run at the same time) need a handle each; mla_latent_append
+ * and mla_attn_prompt_run use only its status word and may overlap.  */
+typedef struct mla_attn_config {
+  int num_heads;    /* H query heads, 1 .. 1024                                        */
+  int num_kv_heads; /* heads of k_nope / value in mla_attn_prompt_run; divides H; 0: H */
+  int kv_lora_rank; /* must be 512                                                     */
+  int rope_dim;     /* must be 64                                                      */
+  int nope_dim;     /* must be 128                                                     */
+  int v_dim;        /* must be 128                                                     */
+  int dtype;        /* mla_dtype of queries, keys, values, caches and outputs          */
+  float eps;        /* RMSNorm epsilon of mla_latent_append                            */
+  float scale;      /* softmax scale; 0 selects 1 / sqrt(nope_dim + rope_dim)          */
+  int max_tokens;   /* largest T (or b*s) of any call                                  */
+  int max_pos;      /* rows of the cos/sin tables                                      */
+  unsigned long long spin_budget_ns; /* device wait limit; 0 selects 1 s               */
+} mla_attn_config;
+
+typedef struct mla_attn_s mla_attn;
+
+/* Validate `cfg`, allocate the workspace (partial results of the split
+ * paged attention, status word) on the current device, return a handle in
+ * *out.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (dimensions other
+ * than above, num_heads % num_kv_heads != 0, num_heads * max_tokens >=
+ * 2^30), MLA_ERR_NO_MEMORY, MLA_ERR_CUDA. */
+mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out);
+mla_status mla_attn_destroy(mla_attn* h);
+
+/* Synchronise `stream`, read and clear the handle's device status word:
+ * MLA_OK, MLA_ERR_BAD_POSITION, MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_BAD_SLOT or
+ * MLA_ERR_BAD_LENGTH (in that order of precedence). */
+mla_status mla_attn_status(mla_attn* h, cudaStream_t stream);
+
+/* Number of kernels the last call on this handle enqueued (-1: null handle). */
+int mla_attn_last_launches(mla_attn* h);
+
+/* Append T token rows to a paged latent cache, rotating positions on the way.
+ *   compressed_kv [T, 512]   dtype   first 512 columns of kv_a_proj's rows
+ *   k_pe          [T, 64]    dtype   its last 64 columns
+ *   q_pe          [T, H, 64] dtype   position part of the queries, or NULL
+ *   positions     [T] int32; cos_table, sin_table [max_pos, 64] f32
+ *   gamma_kv      [512] dtype
+ *   slot_mapping  [T] int32: row t goes to cache row slot_mapping[t] (block *
+ *                 page_size + offset); negative: not stored (padding); at or
+ *                 past num_blocks * page_size: not stored, MLA_ERR_BAD_SLOT.
+ *                 The slots of a call are distinct (rows that share one
+ *                 leave a mixture there).
+ *   latent_cache  [num_blocks * page_size rows, 512], row stride given
+ *   kpe_cache     [num_blocks * page_size rows, 64],  row stride given
+ *                 (both may be views of one [num_blocks, page_size, 576] cache)
+ *   q_pe_out      [T, H, 64] dtype, may be q_pe itself (same strides)
+ * Stored: latent = compressed_kv / sqrt(mean(compressed_kv^2) + eps) *
+ * gamma_kv and k_pe rotated as in step 6 above, fp32 arithmetic, rounded
+ * once; q_pe_out = q_pe rotated the same way (every row, stored or not).
+ * gamma_kv NULL stores the compressed rows as they are; cos_table and
+ * sin_table both NULL store k_pe as it is (then positions may be NULL and
+ * q_pe must be) -- together: a plain scatter of mla_kv_prolog_run_latent's
+ * rows.  Cache rows that no slot names keep their contents.  Positions
+ * outside [0, max_pos) are clamped and reported (MLA_ERR_BAD_POSITION).
+ * Errors: MLA_ERR_INVALID_ARG (also num_blocks * page_size > INT_MAX, bad
+ * strides), MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+mla_status mla_latent_append(mla_attn* h, int T, const void* compressed_kv, int ckv_stride,
+                             const void* k_pe, int k_pe_stride, const void* q_pe,
+                             int q_pe_token_stride, int q_pe_head_stride, const int32_t* positions,
+                             const void* gamma_kv, const float* cos_table, const float* sin_table,
+                             const int32_t* slot_mapping, int page_size, int num_blocks,
+                             void* latent_cache, int latent_row_stride, void* kpe_cache,
+                             int kpe_row_stride, void* q_pe_out, int q_pe_out_token_stride,
+                             int q_pe_out_head_stride, cudaStream_t stream);
+
+/* Attention of the newest tokens of num_seqs sequences over their paged
+ * latent cache.  Per token row t and head h the query is [q_latent | q_pe]
+ * (q_latent = q_nope absorbed through the k_nope half of kv_b_proj), a
+ * cached token's key is [latent | k_pe] and its value is latent:
+ *   q_latent [T, H, 512], q_pe [T, H, 64]  dtype (strided)
+ *   cu_q     [num_seqs + 1] int32: sequence i owns token rows cu_q[i] ..
+ *            cu_q[i+1] - 1 (its n newest tokens, oldest first); NULL: every
+ *            sequence owns T / num_seqs rows (T = num_seqs: plain decode)
+ *   kv_lens  [num_seqs] int32: cached tokens L of the sequence, the n newest
+ *            included (already appended)
+ *   block_table [num_seqs, table_stride] int32: block of cache rows
+ *            j * page_size .. of the sequence at [i, j]; entries past
+ *            ceil(L / page_size) are not read
+ *   latent_cache, kpe_cache as for mla_latent_append
+ *   out      [T, H, 512] dtype, dense;  lse [T, H] f32, dense, or NULL
+ * Row i of n sees the cached tokens j <= L - n + i: out = sum_j p_j latent_j
+ * with p = softmax(scale * q . key), lse = ln sum_j exp(scale * q . key_j).
+ * A row that sees none (L < n) gets zeros and -infinity.  Token rows of no
+ * sequence are left as they were; cache rows past L are not used (they may
+ * hold anything, NaN included).  Scores, maxima, sums and outputs are
+ * accumulated in fp32; the softmax weights are rounded to dtype for their
+ * product with the latents.  Results do not depend on timing.
+ * Two launches.  A block index outside [0, num_blocks) reads as a block of
+ * zeros and is reported (MLA_ERR_BAD_SLOT); a length below 0 or past
+ * table_stride * page_size and offsets outside [0, T] are clamped and
+ * reported (MLA_ERR_BAD_LENGTH).  Errors: MLA_ERR_INVALID_ARG (also T %
+ * num_seqs != 0 without cu_q), MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED,
+ * MLA_ERR_CUDA. */
+mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_latent,
+                              int q_latent_token_stride, int q_latent_head_stride, const void* q_pe,
+                              int q_pe_token_stride, int q_pe_head_stride, const int32_t* cu_q,
+                              const int32_t* kv_lens, const int32_t* block_table, int table_stride,
+                              const void* latent_cache, int latent_row_stride, const void* kpe_cache,
+                              int kpe_row_stride, int page_size, int num_blocks, void* out,
+                              float* lse, cudaStream_t stream);
+
+/* Attention over whole prompts in the up-projected form, on the outputs of
+ * mla_kv_prolog_run (or mla_prolog_w8a8_run):
+ *   q_nope [b, H, s, 128], q_pe [b, H, s, 64]   dtype (q_pe rotated)
+ *   k_nope [b, KH, s, 128], value [b, KH, s, 128], k_pe [b, 1, s, 64]  dtype;
+ *            KH = num_kv_heads, query head h uses key head h / (H / KH)
+ *   out    [b, H, s, 128] dtype;  lse [b, H, s] f32, dense, or NULL
+ * Strides are given per dimension, so token-major tensors serve as well.
+ *   cu_seqlens [num_seqs + 1] int32: packed sequences, sequence i being
+ *            tokens cu_seqlens[i] .. cu_seqlens[i+1] - 1 of the s tokens
+ *            (b = 1); NULL: b sequences of s tokens (num_seqs is not read).
+ * Token i of a sequence sees the tokens j <= i of it (causal = 1) or all of
+ * them (causal = 0): out = sum_j p_j value_j, p = softmax(scale *
+ * (q_nope . k_nope_j + q_pe . k_pe_j)), lse as above.  Tokens of no sequence
+ * are neither read nor written.  Arithmetic as for mla_attn_paged_run; values
+ * must be finite within a sequence.  Offsets outside [0, s] or decreasing
+ * are clamped and reported (MLA_ERR_BAD_LENGTH).  Errors as above; cu_seqlens
+ * with b > 1 is MLA_ERR_INVALID_ARG. */
+mla_status mla_attn_prompt_run(mla_attn* h, int b, int s, const int32_t* cu_seqlens, int num_seqs,
+                               int causal, const void* q_nope, int q_nope_batch_stride,
+                               int q_nope_head_stride, int q_nope_token_stride, const void* q_pe,
+                               int q_pe_batch_stride, int q_pe_head_stride, int q_pe_token_stride,
+                               const void* k_nope, int k_nope_batch_stride, int k_nope_head_stride,
+                               int k_nope_token_stride, const void* k_pe, int k_pe_batch_stride,
+                               int k_pe_token_stride, const void* value, int value_batch_stride,
+                               int value_head_stride, int value_token_stride, void* out,
+                               int out_batch_stride, int out_head_stride, int out_token_stride,
+                               float* lse, cudaStream_t stream);
 
 /* Text of a status code (static storage), the text of the last CUDA error
  * seen by this library on the calling thread, and the ABI version. */

@@ -18,10 +18,11 @@ MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
                 3: "MLA_ERR_TOO_MANY_TOKENS", 4: "MLA_ERR_MISALIGNED", 5: "MLA_ERR_CUDA",
                 6: "MLA_ERR_DEVICE_TIMEOUT", 7: "MLA_ERR_BAD_POSITION", 8: "MLA_ERR_NO_MEMORY",
-                9: "MLA_ERR_WRONG_MODE", 10: "MLA_ERR_BAD_SLOT"}
+                9: "MLA_ERR_WRONG_MODE", 10: "MLA_ERR_BAD_SLOT", 11: "MLA_ERR_BAD_LENGTH"}
 PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_DECODE_GRID = 0, 1, 2, 3
 MLA_F16, MLA_BF16 = 0, 1
 QUANT_NONE, QUANT_W8A8 = 0, 1
+_INT_MAX = 0x7fffffff
 
 EXPORTED = ["mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
             "mla_kv_prolog_status", "mla_kv_prolog_destroy", "mla_kv_prolog_set_path",
@@ -30,7 +31,8 @@ EXPORTED = ["mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
             "mla_last_cuda_error", "mla_abi_version", "mla_kv_prolog_run_noalloc",
             "mla_kv_prolog_prepare_weights", "mla_kv_prolog_run_latent", "mla_kv_prolog_run_paged",
             "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold", "mla_prolog_w8a8_capture",
-            "mla_kv_prolog_last_cluster_launches"]
+            "mla_kv_prolog_last_cluster_launches", "mla_attn_create", "mla_attn_destroy", "mla_attn_status",
+            "mla_attn_last_launches", "mla_latent_append", "mla_attn_paged_run", "mla_attn_prompt_run"]
 
 
 class MLAError(RuntimeError):
@@ -46,6 +48,14 @@ class Config(ctypes.Structure):
                 ("eps", ctypes.c_float), ("max_tokens", ctypes.c_int), ("max_pos", ctypes.c_int),
                 ("quant", ctypes.c_int), ("q_lora_rank", ctypes.c_int),
                 ("spin_budget_ns", ctypes.c_ulonglong)]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("kv_lora_rank", ctypes.c_int), ("rope_dim", ctypes.c_int),
+                ("nope_dim", ctypes.c_int), ("v_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("max_tokens", ctypes.c_int),
+                ("max_pos", ctypes.c_int), ("spin_budget_ns", ctypes.c_ulonglong)]
 
 
 _lib = None
@@ -85,13 +95,22 @@ def load(path: str | None = None):
     L.mla_kv_prolog_prepare_weights.argtypes = [H, P, P, P]
     L.mla_kv_prolog_auto_threshold.argtypes = [H]
     L.mla_prolog_w8a8_capture.argtypes = [H, P, P, P]
+    L.mla_attn_create.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(ctypes.c_void_p)]
+    L.mla_attn_destroy.argtypes = [H]
+    L.mla_attn_status.argtypes = [H, P]
+    L.mla_attn_last_launches.argtypes = [H]
+    L.mla_latent_append.argtypes = [H, I, P, I, P, I, P, I, I] + [P] * 5 + [I, I, P, I, P, I, P, I, I, P]
+    L.mla_attn_paged_run.argtypes = [H, I, I, P, I, I, P, I, I, P, P, P, I, P, I, P, I, I, I, P, P, P]
+    L.mla_attn_prompt_run.argtypes = [H, I, I, P, I, I] + [P, I, I, I] * 3 + [P, I, I] + [P, I, I, I] * 2 + [P, P]
     for fn in ("mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
                "mla_kv_prolog_status", "mla_kv_prolog_destroy", "mla_kv_prolog_set_path",
                "mla_kv_prolog_last_launches", "mla_kv_prolog_last_path", "mla_w8a8_quant_rows",
                "mla_w8a8_gemm_s32", "mla_prolog_w8a8_operands", "mla_abi_version",
                "mla_kv_prolog_run_noalloc", "mla_kv_prolog_prepare_weights", "mla_kv_prolog_run_latent",
                "mla_kv_prolog_run_paged", "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold",
-               "mla_prolog_w8a8_capture", "mla_kv_prolog_last_cluster_launches"):
+               "mla_prolog_w8a8_capture", "mla_kv_prolog_last_cluster_launches", "mla_attn_create",
+               "mla_attn_destroy", "mla_attn_status", "mla_attn_last_launches", "mla_latent_append",
+               "mla_attn_paged_run", "mla_attn_prompt_run"):
         getattr(L, fn).restype = ctypes.c_int
     L.mla_status_string.argtypes = [ctypes.c_int]
     L.mla_status_string.restype = ctypes.c_char_p
@@ -388,6 +407,193 @@ class MLAProlog:
             mla_kv_prolog_run(self.h, self.cfg, b, s, d["hidden"], d["positions"], d["W_kva"],
                               d["gamma_kv"], d["W_kvb"], d["cos"], d["sin"], out["k_nope"],
                               out["value"], out["k_pe"], stream)
+        return out
+
+
+# ------------------------------------------------------------------ attention
+def mla_attn_create(cfg: dict, max_tokens: int, num_kv_heads: int | None = None, scale: float | None = None,
+                    spin_budget_ns: int = 0) -> ctypes.c_void_p:
+    c = AttnConfig(cfg["num_heads"], num_kv_heads or 0, cfg["kv_lora_rank"], cfg["rope_dim"], cfg["nope_dim"],
+                   cfg["v_dim"], MLA_F16 if cfg["dtype"] == "fp16" else MLA_BF16, cfg["eps"], scale or 0.0,
+                   max_tokens, cfg["max_pos"], spin_budget_ns)
+    h = ctypes.c_void_p()
+    _check(load().mla_attn_create(ctypes.byref(c), ctypes.byref(h)), "mla_attn_create")
+    return h
+
+
+def mla_attn_destroy(h):
+    _check(load().mla_attn_destroy(h), "mla_attn_destroy")
+
+
+def mla_attn_status(h, stream=None) -> int:
+    """Raw status code (0 = ok, 6 = timeout, 7 = bad position, 10 = bad slot, 11 = bad length)."""
+    return load().mla_attn_status(h, _stream(stream))
+
+
+class MLAAttention:
+    """Attention on the prolog's outputs: latent cache append, paged latent
+    attention, prompt attention (one library handle, one workspace).
+
+    Tensors may be strided in every dimension but the last; shapes, types
+    and devices are checked here, strides and alignment in the library.
+    scale None: 1 / sqrt(nope_dim + rope_dim)."""
+
+    def __init__(self, cfg: dict, max_tokens: int, num_kv_heads: int | None = None, scale: float | None = None,
+                 spin_budget_ns: int = 0):
+        self.cfg = cfg
+        self.max_tokens = max_tokens
+        self.dtype = _tdt(cfg)
+        self.heads = cfg["num_heads"]
+        self.kv_heads = num_kv_heads or cfg["num_heads"]
+        self.h = None
+        self.h = mla_attn_create(cfg, max_tokens, num_kv_heads, scale, spin_budget_ns)
+        self.device = torch.cuda.current_device()
+
+    def close(self):
+        if self.h is not None:
+            mla_attn_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def last_launches(self) -> int:
+        return load().mla_attn_last_launches(self.h)
+
+    def status(self, stream=None) -> int:
+        return mla_attn_status(self.h, stream)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _rows(self, t, shape, name):
+        """Address and element strides of a tensor of the handle's dtype whose last dimension is contiguous."""
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
+            raise TypeError(f"{name} must be a tensor on CUDA device {self.device}")
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        if max(st) > _INT_MAX:  # (the stride of a dimension of size 1 does not matter)
+            st = tuple(x if k > 1 else shape[-1] for x, k in zip(st, shape))
+            if max(st) > _INT_MAX:
+                raise ValueError(f"{name}: strides must be below 2^31 elements")
+        return t.data_ptr(), st
+
+    def _flat(self, t, dtype, shape, name):
+        """Address of a contiguous tensor."""
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
+            raise TypeError(f"{name} must be a tensor on CUDA device {self.device}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _cache(self, t, width, name):
+        """Address, row stride, blocks and page size of a cache [num_blocks, page_size, width]."""
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must have shape [num_blocks, page_size, {width}]")
+        nb, page, _ = t.shape
+        ptr, st = self._rows(t, (nb, page, width), name)
+        row = st[1] if page > 1 else st[0]
+        if nb > 1 and page > 1 and st[0] != page * row:
+            raise ValueError(f"{name}: rows must be evenly spaced")
+        # (a single row has no stride of its own)
+        return ptr, (row if nb * page > 1 else max(width, row)), nb, page
+
+    def alloc_latent_caches(self, num_blocks: int, page_size: int):
+        """latent_cache [num_blocks, page_size, 512] and kpe_cache [num_blocks, page_size, 64]."""
+        c, dev = self.cfg, torch.device("cuda", self.device)
+        return dict(latent_cache=torch.empty(num_blocks, page_size, c["kv_lora_rank"], dtype=self.dtype, device=dev),
+                    kpe_cache=torch.empty(num_blocks, page_size, c["rope_dim"], dtype=self.dtype, device=dev))
+
+    def append_latent(self, compressed_kv, k_pe, positions, gamma_kv, cos, sin, slot_mapping, latent_cache, kpe_cache,
+                      q_pe=None, q_pe_out=None, stream=None):
+        """RMSNorm compressed_kv [T, 512] (gamma_kv None: as it is), rotate k_pe [T, 64] (cos, sin None: as it is)
+        and store both at slot_mapping in the paged caches; rotate q_pe [T, H, 64] into q_pe_out (None: in place).
+        Returns q_pe_out."""
+        T = compressed_kv.shape[0]
+        f32, i32, rank, rope = torch.float32, torch.int32, self.cfg["kv_lora_rank"], self.cfg["rope_dim"]
+        ckv, ckv_st = self._rows(compressed_kv, (T, rank), "compressed_kv")
+        kp, kp_st = self._rows(k_pe, (T, rope), "k_pe")
+        lc, lc_row, nb, page = self._cache(latent_cache, rank, "latent_cache")
+        kc, kc_row, nb2, page2 = self._cache(kpe_cache, rope, "kpe_cache")
+        if nb2 != nb or page2 != page:
+            raise ValueError("latent_cache and kpe_cache must have the same blocks")
+        table = (self.cfg["max_pos"], rope)
+        qp = qo = None
+        q0 = q1 = o0 = o1 = 0
+        if q_pe is not None:
+            if q_pe_out is None:
+                q_pe_out = q_pe
+            shape = (T, self.heads, rope)
+            qp, (q0, q1, _) = self._rows(q_pe, shape, "q_pe")
+            qo, (o0, o1, _) = self._rows(q_pe_out, shape, "q_pe_out")
+        _check(load().mla_latent_append(
+            self.h, T, ckv, ckv_st[0], kp, kp_st[0], qp, q0, q1,
+            None if positions is None else self._flat(positions, i32, (T,), "positions"),
+            None if gamma_kv is None else self._flat(gamma_kv, self.dtype, (rank,), "gamma_kv"),
+            None if cos is None else self._flat(cos, f32, table, "cos"),
+            None if sin is None else self._flat(sin, f32, table, "sin"),
+            self._flat(slot_mapping, i32, (T,), "slot_mapping"), page, nb, lc, lc_row, kc, kc_row, qo, o0, o1,
+            self._stream(stream)), "mla_latent_append")
+        return q_pe_out
+
+    def run_paged(self, q_latent, q_pe, kv_lens, block_table, latent_cache, kpe_cache, out, cu_q=None, lse=None,
+                  stream=None):
+        """Attention of the newest tokens over the paged latent cache: q_latent [T, H, 512], q_pe [T, H, 64],
+        kv_lens [n], block_table [n, blocks], cu_q [n + 1] or None (T / n tokens each) -> out [T, H, 512] and
+        lse [T, H] (float32, optional)."""
+        T, H, i32 = q_latent.shape[0], self.heads, torch.int32
+        rank, rope = self.cfg["kv_lora_rank"], self.cfg["rope_dim"]
+        ql, (ql0, ql1, _) = self._rows(q_latent, (T, H, rank), "q_latent")
+        qp, (qp0, qp1, _) = self._rows(q_pe, (T, H, rope), "q_pe")
+        lc, lc_row, nb, page = self._cache(latent_cache, rank, "latent_cache")
+        kc, kc_row, nb2, page2 = self._cache(kpe_cache, rope, "kpe_cache")
+        if nb2 != nb or page2 != page:
+            raise ValueError("latent_cache and kpe_cache must have the same blocks")
+        n = kv_lens.shape[0]
+        _check(load().mla_attn_paged_run(
+            self.h, n, T, ql, ql0, ql1, qp, qp0, qp1,
+            None if cu_q is None else self._flat(cu_q, i32, (n + 1,), "cu_q"),
+            self._flat(kv_lens, i32, (n,), "kv_lens"),
+            self._flat(block_table, i32, (n, block_table.shape[-1]), "block_table"), block_table.shape[-1],
+            lc, lc_row, kc, kc_row, page, nb, self._flat(out, self.dtype, (T, H, rank), "out"),
+            None if lse is None else self._flat(lse, torch.float32, (T, H), "lse"), self._stream(stream)),
+            "mla_attn_paged_run")
+        return out
+
+    def run_prompt(self, q_nope, q_pe, k_nope, k_pe, value, out, cu_seqlens=None, causal=True, lse=None, stream=None):
+        """Attention over whole prompts: q_nope [b, H, s, 128], q_pe [b, H, s, 64], k_nope and value
+        [b, KH, s, 128], k_pe [b, 1, s, 64] -> out [b, H, s, 128] and lse [b, H, s] (float32, optional).
+        cu_seqlens [n + 1]: packed sequences along the s tokens (b = 1)."""
+        b, H, s, d = q_nope.shape
+        c, KH = self.cfg, self.kv_heads
+        rope, vd = c["rope_dim"], c["v_dim"]
+        qn, (a0, a1, a2, _) = self._rows(q_nope, (b, self.heads, s, c["nope_dim"]), "q_nope")
+        qp, (b0, b1, b2, _) = self._rows(q_pe, (b, H, s, rope), "q_pe")
+        kn, (c0, c1, c2, _) = self._rows(k_nope, (b, KH, s, c["nope_dim"]), "k_nope")
+        kp, (d0, _, d2, _) = self._rows(k_pe, (b, 1, s, rope), "k_pe")
+        va, (e0, e1, e2, _) = self._rows(value, (b, KH, s, vd), "value")
+        ou, (f0, f1, f2, _) = self._rows(out, (b, H, s, vd), "out")
+        n = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        _check(load().mla_attn_prompt_run(
+            self.h, b, s, None if cu_seqlens is None else self._flat(cu_seqlens, torch.int32, (n + 1,), "cu_seqlens"),
+            n, 1 if causal else 0, qn, a0, a1, a2, qp, b0, b1, b2, kn, c0, c1, c2, kp, d0, d2, va, e0, e1, e2,
+            ou, f0, f1, f2, None if lse is None else self._flat(lse, torch.float32, (b, H, s), "lse"),
+            self._stream(stream)), "mla_attn_prompt_run")
         return out
 
 

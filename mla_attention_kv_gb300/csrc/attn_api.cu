@@ -1,0 +1,274 @@
+// attn_api.cu -- the attention part of the C ABI (include/mla_prolog.h):
+// handle, argument checks, workspace and kernel dispatch of the latent cache
+// append, the paged latent attention and the prompt attention.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <new>
+
+#include "../../include/mla_prolog.h"
+#include "attn.h"
+
+using namespace mla;
+
+struct mla_attn_s {
+  mla_attn_config cfg;
+  int device;
+  int num_sms;
+  int last_launches;
+  float scale_log2;
+  unsigned long long budget_ns;
+  void* ws;
+  unsigned* status;
+  float* part_o;
+  float* part_ml;
+};
+
+namespace {
+
+mla_status fail(cudaError_t e, const char* what) {
+  char text[256];
+  snprintf(text, sizeof(text), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
+  set_error_text(text);
+  return MLA_ERR_CUDA;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A stride between rows of `width` elements: whole 16-byte units, rows not
+// overlapping (the stride of a dimension of size 1 is not read).
+bool stride_ok(int stride, int width, bool used) { return !used || (stride >= width && stride % 8 == 0); }
+
+// Makes the handle's device current for the length of a call.
+struct DeviceGuard {
+  int before = -1;
+  cudaError_t err;
+  explicit DeviceGuard(int device) {
+    err = cudaGetDevice(&before);
+    if (err == cudaSuccess && before != device)
+      err = cudaSetDevice(device);
+    else
+      before = -1;
+  }
+  ~DeviceGuard() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
+  if (!cfg || !out) return MLA_ERR_INVALID_ARG;
+  *out = nullptr;
+  const mla_attn_config& c = *cfg;
+  if (c.num_heads <= 0 || c.num_kv_heads < 0 || c.max_tokens <= 0 || c.max_pos <= 0 || !(c.eps >= 0.0f) ||
+      !(c.scale >= 0.0f) || isinf(c.scale) || (c.dtype != MLA_F16 && c.dtype != MLA_BF16))
+    return MLA_ERR_INVALID_ARG;
+  const int kvh = c.num_kv_heads ? c.num_kv_heads : c.num_heads;
+  if (c.kv_lora_rank != kRank || c.rope_dim != kRope || c.nope_dim != kNope || c.v_dim != kV ||
+      c.num_heads % kvh != 0 || c.num_heads > 1024 || (long long)c.num_heads * c.max_tokens > 0x7fffffffLL / 2)
+    return MLA_ERR_UNSUPPORTED;
+  mla_attn_s* h = new (std::nothrow) mla_attn_s();
+  if (!h) return MLA_ERR_NO_MEMORY;
+  memset(h, 0, sizeof(*h));
+  h->cfg = c;
+  h->cfg.num_kv_heads = kvh;
+  h->budget_ns = c.spin_budget_ns ? c.spin_budget_ns : 1000000000ull;
+  h->scale_log2 = (c.scale > 0.0f ? c.scale : 1.0f / sqrtf((float)(kNope + kRope))) * kLog2e;
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+  if (e != cudaSuccess) {
+    delete h;
+    return fail(e, "device query");
+  }
+  // workspace: [status, 256 bytes] | two partial results per worker
+  const size_t rows = (size_t)h->num_sms * 2 * kPagedMmaRows;
+  const size_t ml_off = 256, o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+  e = cudaMalloc(&h->ws, o_off + rows * kRank * sizeof(float));
+  if (e != cudaSuccess) {
+    delete h;
+    fail(e, "cudaMalloc workspace");
+    return MLA_ERR_NO_MEMORY;
+  }
+  e = cudaMemset(h->ws, 0, 256);
+  if (e != cudaSuccess) {
+    cudaFree(h->ws);
+    delete h;
+    return fail(e, "cudaMemset workspace");
+  }
+  unsigned char* base = static_cast<unsigned char*>(h->ws);
+  h->status = reinterpret_cast<unsigned*>(base);
+  h->part_ml = reinterpret_cast<float*>(base + ml_off);
+  h->part_o = reinterpret_cast<float*>(base + o_off);
+  *out = h;
+  return MLA_OK;
+}
+
+mla_status mla_attn_destroy(mla_attn* h) {
+  if (!h) return MLA_ERR_INVALID_ARG;
+  cudaError_t e = cudaFree(h->ws);
+  delete h;
+  return e == cudaSuccess ? MLA_OK : fail(e, "cudaFree workspace");
+}
+
+mla_status mla_attn_status(mla_attn* h, cudaStream_t stream) {
+  if (!h) return MLA_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return fail(e, "cudaStreamSynchronize");
+  unsigned st = 0;
+  e = cudaMemcpy(&st, h->status, sizeof(unsigned), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return fail(e, "read status");
+  if (st) {
+    e = cudaMemset(h->status, 0, 256);
+    if (e != cudaSuccess) return fail(e, "clear status");
+  }
+  if (st & kStatusBadPosition) return MLA_ERR_BAD_POSITION;
+  if (st & kStatusTimeout) return MLA_ERR_DEVICE_TIMEOUT;
+  if (st & kStatusBadSlot) return MLA_ERR_BAD_SLOT;
+  if (st & kStatusBadLength) return MLA_ERR_BAD_LENGTH;
+  return MLA_OK;
+}
+
+int mla_attn_last_launches(mla_attn* h) { return h ? h->last_launches : -1; }
+
+mla_status mla_latent_append(mla_attn* h, int T, const void* compressed_kv, int ckv_stride, const void* k_pe,
+                             int k_pe_stride, const void* q_pe, int q_pe_token_stride, int q_pe_head_stride,
+                             const int32_t* positions, const void* gamma_kv, const float* cos_table,
+                             const float* sin_table, const int32_t* slot_mapping, int page_size, int num_blocks,
+                             void* latent_cache, int latent_row_stride, void* kpe_cache, int kpe_row_stride,
+                             void* q_pe_out, int q_pe_out_token_stride, int q_pe_out_head_stride,
+                             cudaStream_t stream) {
+  if (!h || T < 0 || page_size <= 0 || num_blocks <= 0 || (long long)page_size * num_blocks > 0x7fffffffLL)
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  if (T == 0) return MLA_OK;
+  if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  const int H = h->cfg.num_heads;
+  if (!compressed_kv || !k_pe || !slot_mapping || !latent_cache || !kpe_cache || (!cos_table != !sin_table) ||
+      (cos_table && !positions) || (q_pe && (!cos_table || !q_pe_out)))
+    return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(ckv_stride, kRank, T > 1) || !stride_ok(k_pe_stride, kRope, T > 1) ||
+      !stride_ok(latent_row_stride, kRank, true) || !stride_ok(kpe_row_stride, kRope, true))
+    return MLA_ERR_INVALID_ARG;
+  if (q_pe && (!stride_ok(q_pe_token_stride, kRope, T > 1) || !stride_ok(q_pe_head_stride, kRope, H > 1) ||
+               !stride_ok(q_pe_out_token_stride, kRope, T > 1) || !stride_ok(q_pe_out_head_stride, kRope, H > 1)))
+    return MLA_ERR_INVALID_ARG;
+  if (q_pe == q_pe_out && q_pe &&
+      (q_pe_token_stride != q_pe_out_token_stride || q_pe_head_stride != q_pe_out_head_stride))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {compressed_kv, k_pe, slot_mapping, latent_cache, kpe_cache, gamma_kv, cos_table, sin_table,
+                        positions, q_pe, q_pe ? q_pe_out : nullptr};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  AppendParams p = {};
+  p.ckv = compressed_kv; p.kpe = k_pe; p.qpe = q_pe; p.positions = positions; p.gamma = gamma_kv;
+  p.cos_t = cos_table; p.sin_t = sin_table; p.slots = slot_mapping; p.latent_cache = latent_cache;
+  p.kpe_cache = kpe_cache; p.qpe_out = q_pe_out; p.status = h->status; p.ckv_stride = ckv_stride;
+  p.kpe_stride = k_pe_stride; p.q_ts = q_pe_token_stride; p.q_hs = q_pe_head_stride; p.lat_rs = latent_row_stride;
+  p.kpe_rs = kpe_row_stride; p.qo_ts = q_pe_out_token_stride; p.qo_hs = q_pe_out_head_stride; p.T = T; p.heads = H;
+  p.nslots = page_size * num_blocks; p.max_pos = h->cfg.max_pos; p.eps = h->cfg.eps;
+  cudaError_t e = append_launch(h->cfg.dtype == MLA_BF16, p, stream);
+  if (e != cudaSuccess) return fail(e, "append launch");
+  h->last_launches = 1;
+  return MLA_OK;
+}
+
+mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_latent, int q_latent_token_stride,
+                              int q_latent_head_stride, const void* q_pe, int q_pe_token_stride,
+                              int q_pe_head_stride, const int32_t* cu_q, const int32_t* kv_lens,
+                              const int32_t* block_table, int table_stride, const void* latent_cache,
+                              int latent_row_stride, const void* kpe_cache, int kpe_row_stride, int page_size,
+                              int num_blocks, void* out, float* lse, cudaStream_t stream) {
+  if (!h || num_seqs < 0 || T < 0 || page_size <= 0 || num_blocks <= 0 || table_stride < 0 ||
+      (long long)page_size * num_blocks > 0x7fffffffLL)
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  if (num_seqs == 0 || T == 0) return MLA_OK;
+  if (!cu_q && T % num_seqs != 0) return MLA_ERR_INVALID_ARG;
+  if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  const int H = h->cfg.num_heads;
+  if (!q_latent || !q_pe || !kv_lens || !block_table || !latent_cache || !kpe_cache || !out) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(q_latent_token_stride, kRank, T > 1) || !stride_ok(q_latent_head_stride, kRank, H > 1) ||
+      !stride_ok(q_pe_token_stride, kRope, T > 1) || !stride_ok(q_pe_head_stride, kRope, H > 1) ||
+      !stride_ok(latent_row_stride, kRank, true) || !stride_ok(kpe_row_stride, kRope, true))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q_latent, q_pe, cu_q, kv_lens, block_table, latent_cache, kpe_cache, out, lse};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  const bool bf16 = h->cfg.dtype == MLA_BF16;
+  PagedParams p = {};
+  p.q_lat = q_latent; p.q_pe = q_pe; p.cu_q = cu_q; p.kv_lens = kv_lens; p.table = block_table; p.latent = latent_cache;
+  p.kpe = kpe_cache; p.out = out; p.lse = lse; p.part_o = h->part_o; p.part_ml = h->part_ml; p.status = h->status;
+  p.ql_ts = q_latent_token_stride; p.ql_hs = q_latent_head_stride; p.qp_ts = q_pe_token_stride;
+  p.qp_hs = q_pe_head_stride; p.table_stride = table_stride; p.lat_rs = latent_row_stride; p.kpe_rs = kpe_row_stride;
+  p.page = page_size; p.nblocks = num_blocks; p.nseq = num_seqs; p.T = T; p.heads = H;
+  p.n_uniform = cu_q ? 0 : T / num_seqs; p.workers = h->num_sms; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
+  // (with ragged chunks the host knows only the average)
+  const long long rows_per_seq = (long long)(T / num_seqs > 0 ? T / num_seqs : 1) * H;
+  const int rows = rows_per_seq <= 16 ? 16 : kPagedMmaRows;
+  cudaError_t e = paged_mma_launch(bf16, p, rows, stream);
+  if (e != cudaSuccess) return fail(e, "paged attention launch");
+  e = paged_combine_launch(bf16, p, rows, stream);
+  if (e != cudaSuccess) return fail(e, "paged attention combine launch");
+  h->last_launches = 2;
+  return MLA_OK;
+}
+
+mla_status mla_attn_prompt_run(mla_attn* h, int b, int s, const int32_t* cu_seqlens, int num_seqs, int causal,
+                               const void* q_nope, int q_nope_batch_stride, int q_nope_head_stride,
+                               int q_nope_token_stride, const void* q_pe, int q_pe_batch_stride,
+                               int q_pe_head_stride, int q_pe_token_stride, const void* k_nope,
+                               int k_nope_batch_stride, int k_nope_head_stride, int k_nope_token_stride,
+                               const void* k_pe, int k_pe_batch_stride, int k_pe_token_stride, const void* value,
+                               int value_batch_stride, int value_head_stride, int value_token_stride, void* out,
+                               int out_batch_stride, int out_head_stride, int out_token_stride, float* lse,
+                               cudaStream_t stream) {
+  if (!h || b < 0 || s < 0 || (causal != 0 && causal != 1) || (cu_seqlens && (num_seqs < 0 || b > 1)))
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  const long long T = (long long)b * s;
+  if (T == 0 || (cu_seqlens && num_seqs == 0)) return MLA_OK;
+  if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  if (!q_nope || !q_pe || !k_nope || !k_pe || !value || !out) return MLA_ERR_INVALID_ARG;
+  const int H = h->cfg.num_heads, KH = h->cfg.num_kv_heads;
+  PromptParams p = {};
+  p.q_nope = {q_nope, q_nope_batch_stride, q_nope_head_stride, q_nope_token_stride};
+  p.q_pe = {q_pe, q_pe_batch_stride, q_pe_head_stride, q_pe_token_stride};
+  p.k_nope = {k_nope, k_nope_batch_stride, k_nope_head_stride, k_nope_token_stride};
+  p.k_pe = {k_pe, k_pe_batch_stride, 0, k_pe_token_stride};
+  p.value = {value, value_batch_stride, value_head_stride, value_token_stride};
+  p.out = {out, out_batch_stride, out_head_stride, out_token_stride};
+  const struct { PromptTensor* t; int width, heads; } all[] = {
+      {&p.q_nope, kNope, H}, {&p.q_pe, kRope, H}, {&p.k_nope, kNope, KH}, {&p.k_pe, kRope, 1}, {&p.value, kV, KH}, {&p.out, kV, H}};
+  for (const auto& x : all)
+    if (!stride_ok(x.t->sb, x.width, b > 1) || !stride_ok(x.t->sh, x.width, x.heads > 1) || !stride_ok(x.t->st, x.width, s > 1))
+      return MLA_ERR_INVALID_ARG;
+  for (const auto& x : all) {
+    if (!aligned16(x.t->ptr)) return MLA_ERR_MISALIGNED;
+    if (b == 1) x.t->sb = x.width;
+    if (x.heads == 1) x.t->sh = x.width;
+    if (s == 1) x.t->st = x.width;
+  }
+  if (!aligned16(cu_seqlens) || !aligned16(lse)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  p.lse = lse; p.cu = cu_seqlens; p.status = h->status; p.b = b; p.s = s; p.nseq = cu_seqlens ? num_seqs : b;
+  p.heads = H; p.kv_heads = KH; p.causal = causal; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
+  cudaError_t e = prompt_mma_launch(h->cfg.dtype == MLA_BF16, p, stream);
+  if (e != cudaSuccess) return fail(e, "prompt attention launch");
+  h->last_launches = 1;
+  return MLA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,380 @@
+// paged_mma.cu -- attention of new tokens over the paged latent cache, for
+// items of 16 or 32 query rows, on mma.sync; and the kernel that joins
+// partial results.
+//
+// Per query row r (a token and a head; q = [q_latent | q_pe], 576 wide) and
+// cached token k (row [latent | k_pe], the latent also being the value):
+//   s_k = scale * q . key_k,  out = sum_k softmax(s)_k * latent_k.
+// One pass over the keys with a running maximum m and sum l per row:
+//   m' = max(m, max s),  l' = l * 2^(m - m') + sum 2^(s - m'),
+//   o' = o * 2^(m - m') + sum 2^(s - m') * latent       (s in log2 units)
+// The 2^(s - m') are rounded to the I/O dtype (the operand type of the
+// product with the latents); l sums them before that rounding, in fp32.
+//
+// With at most 32 rows an item reads 1152 bytes per key for at most
+// 2 * 32 * 1088 FLOPs, well under the ratio at which the tensor cores
+// matter, so the kernel is built around the key stream: one CTA per SM, two
+// stages of 64 keys (74 KB each) filled by 16-byte cp.async (any page size;
+// a page may end anywhere in a tile), each key row used from shared memory
+// twice (as key and as value).
+#include "attn.h"
+#include "common.cuh"
+#include "paged_plan.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPmThreads = 256;
+constexpr int kPitch = kQkDim * 2 + 16;  // bytes per key / query row in shared memory: 73 16-byte units
+constexpr int kStageBytes = kKeyTile * kPitch;
+constexpr int kSPitch = kKeyTile + 4;    // floats
+constexpr int kPPitch = kKeyTile + 8;    // 16-bit values
+
+template <int MT>
+struct PmSmem {
+  static constexpr int R = 16 * MT;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + R * kPitch;
+  static constexpr int kS = kK + 2 * kStageBytes;
+  static constexpr int kP = kS + 2 * R * kSPitch * 4;
+  static constexpr int kRow = kP + R * kPPitch * 2;  // alpha [R], then 1 / l [R]
+  static constexpr int kPlan = (kRow + 2 * R * 4 + 15) & ~15;
+  static constexpr int kBytes = kPlan + (int)sizeof(PlanShared);
+};
+
+// Row index (block * page + offset) of key k of sequence s in the cache, or
+// -1 where it has none.
+__device__ __forceinline__ int cache_row(const PagedParams& p, int s, int k, int keys) {
+  if (k >= keys) return -1;
+  const int pg = k / p.page;
+  const int blk = p.table[(size_t)s * p.table_stride + pg];
+  if (blk < 0 || blk >= p.nblocks) {
+    atomicOr(p.status, kStatusBadSlot);
+    return -1;
+  }
+  return blk * p.page + (k - pg * p.page);
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedParams p) {
+  using E = Elem<T>;
+  using S = PmSmem<MT>;
+  constexpr int R = S::R;
+  constexpr int TPR = kPmThreads / R;        // softmax threads per row
+  constexpr int KPT = kKeyTile / TPR;        // keys per softmax thread
+  extern __shared__ __align__(16) unsigned char smem[];
+  const uint32_t sb = smem_u32(smem);
+  PlanShared* plan = reinterpret_cast<PlanShared*>(smem + S::kPlan);
+  float* sS = reinterpret_cast<float*>(smem + S::kS);
+  float* sAlpha = reinterpret_cast<float*>(smem + S::kRow);
+  float* sInv = sAlpha + R;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = p.heads;
+
+  const long long total = plan_total(p, plan, R, blockIdx.x == 0);
+  if (total == 0) return;
+  const int W = plan_workers(total, p.workers);
+  const int w = blockIdx.x;
+  if (w >= W) return;
+  const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
+  if (x0 >= x1) return;
+
+  PlanCursor c;
+  c.seek(p, plan, R, x0);
+  for (bool more = true; more && c.lo < x1; more = c.next(p, R)) {
+    const Seq q = c.q;
+    const int row0 = c.j * R;  // first row of the item within its sequence
+    const int live = min(R, q.n * H - row0);
+    const int keys = q.keys_of_item(c.j, R, H);
+    const int tiles = (keys + kKeyTile - 1) / kKeyTile;
+    const long long a = x0 > c.lo ? x0 : c.lo, b = x1 < c.hi ? x1 : c.hi;
+    const int t0 = c.tile_at(a, tiles), t1 = c.tile_at(b, tiles);
+    const bool whole = c.lo >= x0 && c.hi <= x1;
+    const int s = c.s;
+
+    // ---- key tiles: warp w loads rows 8w .. 8w+7 of a stage
+    auto rows_of = [&](int tile) {  // lanes 0-7 hold their rows' cache rows
+      return lane < 8 ? cache_row(p, s, tile * kKeyTile + warp * 8 + lane, keys) : -1;
+    };
+    auto load = [&](int tile, int rows) {
+      const uint32_t st = sb + S::kK + (tile & 1) * kStageBytes + warp * 8 * kPitch;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int row = __shfl_sync(~0u, rows, r);
+        const T* src = static_cast<const T*>(p.latent) + (size_t)max(row, 0) * p.lat_rs;
+        const uint32_t d = st + r * kPitch;
+        cp_async16(d + lane * 16, src + lane * 8, row < 0 ? 0 : 16);
+        cp_async16(d + 512 + lane * 16, src + 256 + lane * 8, row < 0 ? 0 : 16);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; r += 4) {
+        const int row = __shfl_sync(~0u, rows, r + (lane >> 3));
+        const T* src = static_cast<const T*>(p.kpe) + (size_t)max(row, 0) * p.kpe_rs;
+        cp_async16(st + (r + (lane >> 3)) * kPitch + 1024 + (lane & 7) * 16, src + (lane & 7) * 8, row < 0 ? 0 : 16);
+      }
+    };
+    __syncthreads();  // the previous item's stages and queries are read
+    // ---- queries (rows past the end are zero), together with the first tile
+    for (int r = warp; r < R; r += kPmThreads / 32) {
+      const int tok = (row0 + r) / H, hd = (row0 + r) - tok * H;
+      const bool ok = r < live;
+      const T* ql = static_cast<const T*>(p.q_lat) + (ok ? (size_t)(q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs : 0);
+      const T* qp = static_cast<const T*>(p.q_pe) + (ok ? (size_t)(q.begin + tok) * p.qp_ts + (size_t)hd * p.qp_hs : 0);
+      const uint32_t d = sb + S::kQ + r * kPitch;
+      cp_async16(d + lane * 16, ql + lane * 8, ok ? 16 : 0);
+      cp_async16(d + 512 + lane * 16, ql + 256 + lane * 8, ok ? 16 : 0);
+      if (lane < 8) cp_async16(d + 1024 + lane * 16, qp + lane * 8, ok ? 16 : 0);
+    }
+    if (t0 < t1) load(t0, rows_of(t0));
+    cp_async_commit();
+    if (t0 + 1 < t1) load(t0 + 1, rows_of(t0 + 1));
+    cp_async_commit();
+
+    float acc[MT][8][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    const int srow = tid / TPR, sk0 = tid % TPR;  // softmax: row, first key (keys sk0 + TPR * i)
+    const int limit = srow < live ? q.keys_of_row(row0 + srow, H) : 0;
+    float m_run = -INFINITY, l_run = 0.f;
+
+    for (int tile = t0; tile < t1; ++tile) {
+      int rows_next = tile + 2 < t1 ? rows_of(tile + 2) : -1;
+      cp_async_wait<1>();
+      __syncthreads();
+      const uint32_t st = sb + S::kK + (tile & 1) * kStageBytes;
+      {  // scores: warp = (16 keys kg, half kh of the 576 columns)
+        const int kg = warp & 3, kh = warp >> 2;
+        float sc[MT][2][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[m][n][i] = 0.f;
+        const uint32_t kaddr = st + (kg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kPitch + kh * 576 + ((lane >> 3) & 1) * 16;
+        const uint32_t qaddr = sb + S::kQ + (lane & 15) * kPitch + kh * 576 + (lane >> 4) * 16;
+#pragma unroll 6
+        for (int k = 0; k < 18; ++k) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(kaddr + k * 32, b0, b1, b2, b3);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t af[4];
+            ldsm_x4(qaddr + m * 16 * kPitch + k * 32, af[0], af[1], af[2], af[3]);
+            mma16816<E::kBf16>(sc[m][0], af, b0, b1);
+            mma16816<E::kBf16>(sc[m][1], af, b2, b3);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float* d = sS + (kh * R + m * 16 + (lane >> 2)) * kSPitch + kg * 16 + n * 8 + (lane & 3) * 2;
+            *reinterpret_cast<float2*>(d) = make_float2(sc[m][n][0], sc[m][n][1]);
+            *reinterpret_cast<float2*>(d + 8 * kSPitch) = make_float2(sc[m][n][2], sc[m][n][3]);
+          }
+      }
+      __syncthreads();
+      {  // softmax of the tile
+        float v[KPT], mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+          const int k = sk0 + i * TPR;
+          const float x = sS[srow * kSPitch + k] + sS[(R + srow) * kSPitch + k];
+          v[i] = tile * kKeyTile + k < limit ? x * p.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, v[i]);
+        }
+#pragma unroll
+        for (int d = TPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+        const float m_new = fmaxf(m_run, mx);
+        const float mu = m_new == -INFINITY ? 0.f : m_new;  // (a row with no key so far)
+        const float alpha = exp2f(m_run - mu);
+        float ls = 0.f;
+        T* prow = reinterpret_cast<T*>(smem + S::kP) + srow * kPPitch;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+          const float e = exp2f(v[i] - mu);
+          ls += e;
+          prow[sk0 + i * TPR] = E::from_f(e);
+        }
+        l_run = l_run * alpha + ls;
+        m_run = m_new;
+        if (sk0 == 0) sAlpha[srow] = alpha;
+      }
+      __syncthreads();
+      {  // output: warp = 64 latent columns
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float a0 = sAlpha[m * 16 + (lane >> 2)], a1 = sAlpha[m * 16 + (lane >> 2) + 8];
+          if (__any_sync(~0u, a0 != 1.f || a1 != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              acc[m][n][0] *= a0;
+              acc[m][n][1] *= a0;
+              acc[m][n][2] *= a1;
+              acc[m][n][3] *= a1;
+            }
+          }
+        }
+        const uint32_t paddr = sb + S::kP + (lane & 15) * (kPPitch * 2) + (lane >> 4) * 16;
+        const uint32_t vaddr = st + (lane & 15) * kPitch + warp * 128 + (lane >> 4) * 16;
+#pragma unroll
+        for (int k = 0; k < kKeyTile / 16; ++k) {
+          uint32_t af[MT][4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            ldsm_x4(paddr + m * 16 * kPPitch * 2 + k * 32, af[m][0], af[m][1], af[m][2], af[m][3]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_trans(vaddr + k * 16 * kPitch + n * 32, b0, b1, b2, b3);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma16816<E::kBf16>(acc[m][2 * n], af[m], b0, b1);
+              mma16816<E::kBf16>(acc[m][2 * n + 1], af[m], b2, b3);
+            }
+          }
+        }
+      }
+      __syncthreads();  // the stage is free
+      if (tile + 2 < t1) load(tile + 2, rows_next);
+      cp_async_commit();
+    }
+    cp_async_wait<0>();
+
+    // ---- results
+    float l_all = l_run;
+#pragma unroll
+    for (int d = TPR / 2; d; d >>= 1) l_all += __shfl_xor_sync(~0u, l_all, d);
+    if (whole) {
+      if (sk0 == 0) {
+        sInv[srow] = l_all == 0.f ? 0.f : 1.f / l_all;
+        if (p.lse && srow < live)
+          p.lse[(size_t)q.begin * H + row0 + srow] = l_all == 0.f ? -INFINITY : (m_run + log2f(l_all)) * kLn2;
+      }
+      __syncthreads();
+      T* out = static_cast<T*>(p.out) + ((size_t)q.begin * H + row0) * kRank;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int r = m * 16 + (lane >> 2) + hf * 8;
+          const float iv = sInv[r];
+          if (r < live) {
+            uint32_t* o = reinterpret_cast<uint32_t*>(out + (size_t)r * kRank + warp * 64) + (lane & 3);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) o[n * 4] = E::pack(acc[m][n][2 * hf] * iv, acc[m][n][2 * hf + 1] * iv);
+          }
+        }
+    } else {
+      const size_t slot = (size_t)w * 2 + (c.lo < x0 ? 0 : 1);
+      if (sk0 == 0) {
+        float* ml = p.part_ml + (slot * R + srow) * 2;
+        ml[0] = m_run;
+        ml[1] = l_all;
+      }
+      if (t0 < t1) {
+        float* po = p.part_o + slot * R * kRank;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int r = m * 16 + (lane >> 2) + hf * 8;
+            float2* o = reinterpret_cast<float2*>(po + (size_t)r * kRank + warp * 64) + (lane & 3);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) o[n * 4] = make_float2(acc[m][n][2 * hf], acc[m][n][2 * hf + 1]);
+          }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine
+// Block (v, y): the item that holds the beginning of worker v's range, if it
+// began in worker v - 1's range; rows 8y .. 8y + 7 of it, one warp per row.  With weights u_i = 2^(m_i - m):
+//   l = sum u_i l_i,  out = sum u_i o_i / l,  lse = (m + log2 l) * ln 2.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p, int R) {
+  using E = Elem<T>;
+  __shared__ PlanShared plan;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long total = plan_total(p, &plan, R, false);
+  if (total == 0) return;
+  const int W = plan_workers(total, p.workers);
+  const int v = blockIdx.x + 1;
+  if (v >= W) return;
+  const long long x = plan_worker_begin(total, v, W);
+  if (x >= total) return;
+  PlanCursor c;
+  c.seek(p, &plan, R, x);
+  if (c.lo == x) return;                                   // no item is cut here
+  const int w1 = plan_worker_of(c.lo, total, W), w2 = plan_worker_of(c.hi - 1, total, W);
+  if (v != w1 + 1) return;                                 // (every range is at least kMinRange long)
+  const int r = blockIdx.y * 8 + warp;
+  if (r >= R || c.j * R + r >= c.q.n * p.heads) return;
+  float m = -INFINITY;
+  for (int u = w1; u <= w2; ++u) {
+    const size_t slot = (size_t)u * 2 + (u == w1 ? 1 : 0);
+    const float* ml = p.part_ml + (slot * R + r) * 2;
+    if (ml[1] != 0.f) m = fmaxf(m, ml[0]);
+  }
+  float l = 0.f, o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+  for (int u = w1; u <= w2; ++u) {
+    const size_t slot = (size_t)u * 2 + (u == w1 ? 1 : 0);
+    const float* ml = p.part_ml + (slot * R + r) * 2;
+    if (ml[1] == 0.f) continue;  // no key in this piece
+    const float f = exp2f(ml[0] - m);
+    l += f * ml[1];
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + (slot * R + r) * kRank);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = po[i * 32 + lane];
+      o[4 * i] += f * a.x;
+      o[4 * i + 1] += f * a.y;
+      o[4 * i + 2] += f * a.z;
+      o[4 * i + 3] += f * a.w;
+    }
+  }
+  const float iv = l == 0.f ? 0.f : 1.f / l;
+  const size_t row = (size_t)c.q.begin * p.heads + c.j * R + r;
+  uint2* d = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * kRank);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    d[i * 32 + lane] = make_uint2(E::pack(o[4 * i] * iv, o[4 * i + 1] * iv), E::pack(o[4 * i + 2] * iv, o[4 * i + 3] * iv));
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <typename T, int MT>
+cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PmSmem<MT>::kBytes);
+  if (e != cudaSuccess) return e;
+  paged_mma_kernel<T, MT><<<p.workers, kPmThreads, PmSmem<MT>::kBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream) {
+  if (rows == 16)
+    return bf16 ? launch_mma<__nv_bfloat16, 1>(p, stream) : launch_mma<__half, 1>(p, stream);
+  return bf16 ? launch_mma<__nv_bfloat16, 2>(p, stream) : launch_mma<__half, 2>(p, stream);
+}
+
+cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream) {
+  if (p.workers < 2) return cudaSuccess;
+  const dim3 grid(p.workers - 1, (rows + 7) / 8);
+  if (bf16)
+    paged_combine_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p, rows);
+  else
+    paged_combine_kernel<__half><<<grid, 256, 0, stream>>>(p, rows);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,199 @@
+// paged_plan.cuh -- how the paged attention kernels share their work.
+//
+// A work item is (sequence, block of R consecutive query rows); a query row
+// is a (token, head) pair, row = token * H + head.  Its keys are taken in
+// tiles of kKeyTile.  The lengths live on the device, so the split is made
+// there: every item gets a width in a common cost space (about its number of
+// key tiles, plus a constant for what an item costs by itself), the widths
+// of all items are laid end to end, and worker w of W takes the cost range
+// [total * w / W, total * (w + 1) / W).  A range may begin and end inside an
+// item; such items are computed in pieces whose results (unnormalised
+// output, maximum, sum) go to the workspace and are joined in a fixed order
+// by the combine kernel, so results do not depend on timing.  The joining
+// kernel derives the same split again from the same lengths.
+//
+// The cumulative cost inside a sequence is the closed form
+//   F(j) = j * first + (last - first) * j^2 / (2 * items),
+// first / last being the widths of its first and last item (the causal limit
+// grows along the chunk): exact for one item, an even slope for many.  A
+// position x inside item j is mapped to the key tile
+// (x - F(j)) * tiles / width, by both neighbours alike.
+#pragma once
+#include <stdint.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace mla {
+
+constexpr int kKeyTile = 64;
+// Width of an item beyond its key tiles (loading its queries, storing its
+// result), in key tiles.
+constexpr int kItemCost = 1;
+constexpr int kPlanThreadsMax = 512;
+
+struct PlanShared {
+  int threads;
+  long long base[kPlanThreadsMax + 1];  // cost before each thread's strip of sequences
+  long long warp_sum[kPlanThreadsMax / 32];
+};
+
+struct Seq {
+  int begin;  // first token row
+  int n;      // new tokens
+  int L;      // cached tokens (the new ones included)
+  int items;
+  int first, last;  // widths of the first and last item
+
+  __host__ __device__ __forceinline__ int keys_of_row(int row_in_seq, int H) const {
+    const int t = row_in_seq / H;
+    const int k = L - n + t + 1;
+    return k < 0 ? 0 : (k > L ? L : k);
+  }
+  // keys of item j: those of its last row
+  __host__ __device__ __forceinline__ int keys_of_item(int j, int R, int H) const {
+    const long long last_row = (long long)(j + 1) * R - 1;
+    const long long rows = (long long)n * H;
+    return keys_of_row((int)(last_row < rows ? last_row : rows - 1), H);
+  }
+  __host__ __device__ __forceinline__ long long cum(int j) const {
+    // (the divisor of a sequence without items only has to be nonzero)
+    return (long long)j * first + (long long)(last - first) * j * j / (2 * (long long)(items > 0 ? items : 1));
+  }
+};
+
+// Sequence s of the call.  Lengths out of range are clamped and, where
+// `report`, recorded.
+__host__ __device__ __forceinline__ Seq plan_seq(const PagedParams& p, int s, int R, bool report) {
+  Seq q;
+  bool bad = false;
+  if (p.cu_q) {
+    int a = p.cu_q[s], b = p.cu_q[s + 1];
+    if (a < 0 || a > p.T) { bad = true; a = a < 0 ? 0 : p.T; }
+    if (b < a || b > p.T) { bad = true; b = b < a ? a : p.T; }
+    q.begin = a;
+    q.n = b - a;
+  } else {
+    q.begin = s * p.n_uniform;
+    q.n = p.n_uniform;
+  }
+  const long long cap = (long long)p.table_stride * p.page;
+  int L = p.kv_lens[s];
+  if (L < 0) { bad = true; L = 0; }
+  if (L > cap) { bad = true; L = (int)cap; }
+  q.L = L;
+  const long long rows = (long long)q.n * p.heads;
+  q.items = (int)((rows + R - 1) / R);
+  q.first = q.last = kItemCost;
+  if (q.items > 0) {
+    q.first += (q.keys_of_item(0, R, p.heads) + kKeyTile - 1) / kKeyTile;
+    q.last += (q.keys_of_item(q.items - 1, R, p.heads) + kKeyTile - 1) / kKeyTile;
+  }
+#ifdef __CUDA_ARCH__
+  if (report && bad) atomicOr(p.status, kStatusBadLength);
+#endif
+  return q;
+}
+
+// Cost of all sequences; ps->base[i] = cost before thread i's strip.  All
+// threads of the block (a multiple of 32, at most kPlanThreadsMax).
+__device__ __forceinline__ long long plan_total(const PagedParams& p, PlanShared* ps, int R, bool report) {
+  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int strip = (p.nseq + nt - 1) / nt;
+  long long mine = 0;
+  for (int i = 0; i < strip; ++i) {
+    const int s = tid * strip + i;
+    if (s < p.nseq) {
+      const Seq q = plan_seq(p, s, R, report);
+      mine += q.cum(q.items);
+    }
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) ps->warp_sum[warp] = inc;
+  __syncthreads();
+  long long before = 0;
+  for (int w = 0; w < warp; ++w) before += ps->warp_sum[w];
+  ps->base[tid] = before + inc - mine;
+  if (tid == nt - 1) {
+    ps->base[nt] = before + inc;
+    ps->threads = nt;
+  }
+  __syncthreads();
+  return ps->base[nt];
+}
+
+// Workers that take part: a range is not worth less than kMinRange.
+constexpr int kMinRange = 2;
+__host__ __device__ __forceinline__ int plan_workers(long long total, int W) {
+  const long long w = total / kMinRange;
+  return w < 1 ? 1 : (w < W ? (int)w : W);
+}
+__host__ __device__ __forceinline__ long long plan_worker_begin(long long total, int w, int W) { return total * w / W; }
+// The worker whose range holds position x.
+__host__ __device__ __forceinline__ int plan_worker_of(long long x, long long total, int W) {
+  return (int)(((x + 1) * W - 1) / total);
+}
+
+// A place in the list of items: sequence, item, and the item's cost range.
+struct PlanCursor {
+  int s;
+  Seq q;
+  long long seq_base;
+  int j;
+  long long lo, hi;
+
+  __host__ __device__ __forceinline__ void set_item(int jj) {
+    j = jj;
+    lo = seq_base + q.cum(jj);
+    hi = seq_base + q.cum(jj + 1);
+  }
+  // The item that holds position x (0 <= x < total).
+  __host__ __device__ __forceinline__ void seek(const PagedParams& p, const PlanShared* ps, int R, long long x) {
+    const int nt = ps->threads;
+    const int strip = (p.nseq + nt - 1) / nt;
+    int a = 0, b = nt;  // last strip with base <= x
+    while (b - a > 1) {
+      const int m = (a + b) / 2;
+      if (ps->base[m] <= x) a = m; else b = m;
+    }
+    s = a * strip;
+    seq_base = ps->base[a];
+    q = plan_seq(p, s, R, false);
+    while (seq_base + q.cum(q.items) <= x) {
+      seq_base += q.cum(q.items);
+      ++s;
+      q = plan_seq(p, s, R, false);
+    }
+    int l = 0, h = q.items;
+    while (h - l > 1) {
+      const int m = (l + h) / 2;
+      if (seq_base + q.cum(m) <= x) l = m; else h = m;
+    }
+    set_item(l);
+  }
+  // The next item; false past the last one.
+  __host__ __device__ __forceinline__ bool next(const PagedParams& p, int R) {
+    if (j + 1 < q.items) {
+      set_item(j + 1);
+      return true;
+    }
+    do {
+      seq_base += q.cum(q.items);
+      if (++s >= p.nseq) return false;
+      q = plan_seq(p, s, R, false);
+    } while (q.items == 0);
+    set_item(0);
+    return true;
+  }
+  // Key tile that position x of this item (lo <= x <= hi) stands for.
+  __host__ __device__ __forceinline__ int tile_at(long long x, int tiles) const {
+    return (int)((x - lo) * tiles / (hi - lo));
+  }
+};
+
+}  // namespace mla
