@@ -1,6 +1,7 @@
 // attn.h -- parameters and launchers of the attention operators (latent
 // cache append, paged latent attention, prompt attention).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -72,6 +73,16 @@ struct PromptParams {
   float scale_log2;
   unsigned long long budget_ns;
 };
-cudaError_t prompt_mma_launch(bool bf16, const PromptParams& p, cudaStream_t stream);
+// Tensor maps of the last call of the tcgen05 kernel and what they were made
+// from (a map is a function of address, sizes and strides alone).
+struct PromptMaps {
+  struct Key {
+    PromptTensor t[5];
+    int b, s, heads, kv_heads;
+  } key;
+  bool valid;
+  CUtensorMap map[5];  // q_nope, q_pe, k_nope, k_pe, value
+};
+cudaError_t prompt_tc_launch(bool bf16, const PromptParams& p, PromptMaps* maps, cudaStream_t stream);
 
 }  // namespace mla

@@ -25,6 +25,7 @@ struct mla_attn_s {
   unsigned* status;
   float* part_o;
   float* part_ml;
+  PromptMaps prompt_maps;
 };
 
 namespace {
@@ -265,7 +266,7 @@ mla_status mla_attn_prompt_run(mla_attn* h, int b, int s, const int32_t* cu_seql
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
   p.lse = lse; p.cu = cu_seqlens; p.status = h->status; p.b = b; p.s = s; p.nseq = cu_seqlens ? num_seqs : b;
   p.heads = H; p.kv_heads = KH; p.causal = causal; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
-  cudaError_t e = prompt_mma_launch(h->cfg.dtype == MLA_BF16, p, stream);
+  cudaError_t e = prompt_tc_launch(h->cfg.dtype == MLA_BF16, p, &h->prompt_maps, stream);
   if (e != cudaSuccess) return fail(e, "prompt attention launch");
   h->last_launches = 1;
   return MLA_OK;

@@ -1,0 +1,74 @@
+// attn_tc.cuh -- helpers shared by the tcgen05 attention kernels: bounded
+// waits, TMEM stores of 32 columns, packed fp32 arithmetic, 2^x.
+#pragma once
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace mla {
+
+// Bounded mbarrier wait shared by all roles of a CTA; gives up on the time
+// budget or when another role has already given up.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                        unsigned long long budget, unsigned* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t n = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if (((++n) & 63) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > budget) {
+        *abort = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x (results below the normal range become 0).
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Scale `COLS` (a multiple of 16) fp32 TMEM columns of this thread's lane.
+template <int COLS>
+__device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t v[32];
+    tc::ld32(taddr + c, v);
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+    tc::st16(taddr + c, v);
+    tc::st16(taddr + c + 16, v + 16);
+  }
+}
+
+}  // namespace mla

@@ -51,4 +51,19 @@ bool encode_tmap_3d_colblocks(CUtensorMap* map, CUtensorMapDataType dtype, const
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_4d_rows(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t width,
+                         uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3,
+                         uint32_t box1) {
+  auto fn = get_encode();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {width, d1, d2, d3};
+  cuuint64_t strides[3] = {s1 * 2, s2 * 2, s3 * 2};
+  cuuint32_t box[4] = {64, box1, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, dtype, 4, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mla

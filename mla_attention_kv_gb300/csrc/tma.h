@@ -26,7 +26,22 @@ bool encode_tmap_3d_colblocks(CUtensorMap* map, CUtensorMapDataType dtype, const
                               uint32_t box_rows, uint32_t box_blocks, uint32_t elem_bytes,
                               CUtensorMapSwizzle swizzle);
 
+// Encode a 4-D map of rows of `width` 16-bit elements (dims {width, d1, d2,
+// d3}, element strides s1 .. s3, each a multiple of 8), box {64, box1, 1, 1},
+// 128-byte swizzle.
+bool encode_tmap_4d_rows(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t width,
+                         uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3,
+                         uint32_t box1);
+
 #ifdef __CUDACC__
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 // Tiled 2-D load of one box into shared memory; completion is counted in
 // bytes on `bar`.  c_inner * element size must be a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c_inner,
