@@ -56,6 +56,25 @@ struct PagedParams {
 // mma.sync kernel: items of 16 or 32 query rows.
 constexpr int kPagedMmaRows = 32;
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
+// tcgen05 kernel: items of 128 query rows, two CTAs per worker; pages whose
+// size is a multiple of 8.
+constexpr int kPagedTcRows = 128;
+struct PagedMaps {  // tensor maps of the last call's caches and what they were made from
+  struct Key {
+    const void* lat;
+    const void* kpe;
+    int lat_rs, kpe_rs, rows, box;
+  } key;
+  bool valid;
+  CUtensorMap lat, kpe;
+};
+// Cache rows per TMA box: the largest power of two that divides the page, at
+// most a key tile; below 8 the 128-byte swizzle pattern would not fit.
+inline int paged_tc_box(int page) {
+  const int b = page & -page;
+  return b > 64 ? 64 : b;
+}
+cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream);
 // Joins the partial results of items split over workers.
 cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
 

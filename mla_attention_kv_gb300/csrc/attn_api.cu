@@ -25,6 +25,7 @@ struct mla_attn_s {
   unsigned* status;
   float* part_o;
   float* part_ml;
+  PagedMaps paged_maps;
   PromptMaps prompt_maps;
 };
 
@@ -88,7 +89,8 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     return fail(e, "device query");
   }
   // workspace: [status, 256 bytes] | two partial results per worker
-  const size_t rows = (size_t)h->num_sms * 2 * kPagedMmaRows;
+  const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedTcRows;
+  const size_t rows = rows_mma > rows_tc ? rows_mma : rows_tc;
   const size_t ml_off = 256, o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
   e = cudaMalloc(&h->ws, o_off + rows * kRank * sizeof(float));
   if (e != cudaSuccess) {
@@ -217,8 +219,10 @@ mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_la
   p.n_uniform = cu_q ? 0 : T / num_seqs; p.workers = h->num_sms; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   // (with ragged chunks the host knows only the average)
   const long long rows_per_seq = (long long)(T / num_seqs > 0 ? T / num_seqs : 1) * H;
-  const int rows = rows_per_seq <= 16 ? 16 : kPagedMmaRows;
-  cudaError_t e = paged_mma_launch(bf16, p, rows, stream);
+  const bool tc = rows_per_seq > kPagedMmaRows && paged_tc_box(page_size) >= 8;
+  const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
+  if (tc) p.workers = h->num_sms / 2;
+  cudaError_t e = tc ? paged_tc_launch(bf16, p, &h->paged_maps, stream) : paged_mma_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention launch");
   e = paged_combine_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention combine launch");

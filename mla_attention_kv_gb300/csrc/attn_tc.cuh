@@ -26,6 +26,12 @@ __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile 
   return true;
 }
 
+// The same for a whole warp: all lanes get one answer.
+__device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             unsigned long long budget, unsigned* status) {
+  return __all_sync(~0u, at_wait(bar, parity, abort, budget, status));
+}
+
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));

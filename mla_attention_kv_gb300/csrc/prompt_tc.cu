@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
     const uint64_t dv0 = tc::sdesc_sw128(sbase, kPtSlotBytes, 1024);  // MN-major: values
     bool ok = true;
     auto wait = [&](uint64_t* b, uint32_t par) {
-      if (ok && !at_wait(bar(b), par, abort, p.budget_ns, p.status)) ok = false;
-      ok = __all_sync(~0u, ok);
+      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
       return ok;
     };
     auto slot_full = [&](uint32_t u) { return wait(&sh->full[u % kPtSlots], (u / kPtSlots) & 1); };
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
     const float scale = p.scale_log2;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      if (!at_wait(bar(&sh->sfull[w]), i & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+      if (!at_wait_warp(bar(&sh->sfull[w]), i & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
       tc::fence_after_sync();
       uint32_t s[128];
 #pragma unroll
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
       f2_unpack(sum[1], b0, b1);
       l += (a0 + a1) + (b0 + b1);
     }
-    if (ok && n > 0 && at_wait(bar(&sh->ofull[w]), 0, abort, p.budget_ns, p.status)) {
+    if (ok && n > 0 && at_wait_warp(bar(&sh->ofull[w]), 0, abort, p.budget_ns, p.status)) {
       tc::fence_after_sync();
       const bool live = w * kPtTile + r < rows;
       const float iv = l == 0.f ? 0.f : 1.f / l;
