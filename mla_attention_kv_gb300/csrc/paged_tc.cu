@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
     for (uint32_t u = uv > kVTiles ? uv - kVTiles : 0; u < uv; ++u)
       mbar_wait_bounded(bar(&sh->vfull[u % kVTiles]), (u / kVTiles) & 1, drain_budget(p.budget_ns));
   } else if (warp == 5) {
-    // ============================================================ MMA (whole warp; lane 0 issues)
+    // ============================================================ MMA (whole warp; an elected lane issues)
     const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 64, false, false);
     const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 256, false, true);
     const uint64_t dk = tc::sdesc_sw128(sbase, 16, 1024);
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
       for (int j = 0; j < 5; ++j, ++un) {
         const uint32_t s = un % kNSlots;
         if (!wait(&sh->nfull[s], (un / kNSlots) & 1)) return;
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint64_t bd = dk + ((kUtN + s * kBlk) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
       }
       const uint32_t s = g_qk % kVTiles;
       if (!wait(&sh->vfull[s], (g_qk / kVTiles) & 1)) return;
-      if (lane == 0) {
+      if (tc::elect_one()) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint64_t ad = dk + ((kUtQ + j * 16384) >> 4), bd = dk + ((kUtV + (s * 4 + j) * kBlk) >> 4);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
         if (t == t0 && item > 0 && !wait(&sh->ofree, (item - 1) & 1)) break;
         if (!wait(&sh->pfull, g_pv & 1)) break;
         tc::fence_after_sync();
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint64_t bd = dv + ((kUtV + s * 4 * kBlk) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) tc::mma_f16_ts(tmem, tmem + kTmP + k * 8, bd + k * 128, id_pv, t > t0 || k > 0);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
       }
       ++item;
     }
-    if (lane == 0) {  // every MMA issued so far has completed before TMEM is released
+    if (tc::elect_one()) {  // every MMA issued so far has completed before TMEM is released
       tc::commit(bar(&sh->done));
       mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));
     }

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
         if ((w ? n1 : n0) > 0) mbar_wait_bounded(bar(&sh->qfull[w]), 0, drain_budget(p.budget_ns));
     }
   } else if (warp == 9) {
-    // ============================================================ MMA (whole warp; lane 0 issues)
+    // ============================================================ MMA (whole warp; an elected lane issues)
     const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 128, false, false);
     const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 128, false, true);
     const uint32_t id_pv64 = tc::idesc_f16(E::kBf16, 128, 64, false, true);
@@ -161,18 +161,18 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
       for (int c = 0; c < 3; ++c) {
         const uint32_t u = 5 * i + c;
         if (!slot_full(u)) return;
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint64_t ad = dk0 + ((w * kPtQBytes + c * 16384) >> 4);
           const uint64_t bd = dk0 + ((kPtRing + (u % kPtSlots) * kPtSlotBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) tc::mma_f16(tmem + w * 128, ad + 2 * k, bd + 2 * k, id_qk, c > 0 || k > 0);
         }
       }
-      if (lane == 0) tc::commit(bar(&sh->sfull[w]));
+      if (tc::elect_one()) tc::commit(bar(&sh->sfull[w]));
       __syncwarp();
     };
     auto release = [&](uint32_t u, int n) {
-      if (lane == 0)
+      if (tc::elect_one())
         for (int c = 0; c < n; ++c) tc::commit(bar(&sh->empty[(u + c) % kPtSlots]));
       __syncwarp();
     };
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
       }
       if (!wait(&sh->pfull[w], i & 1)) return;
       tc::fence_after_sync();
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t s0 = u % kPtSlots, s1 = (u + 1) % kPtSlots;
         const uint64_t b0 = dv0 + ((kPtRing + s0 * kPtSlotBytes) >> 4), b1 = dv0 + ((kPtRing + s1 * kPtSlotBytes) >> 4);
         const uint32_t o = tmem + 256 + w * 128, pa = tmem + w * 128;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
       if (ok && i + 1 < nt) release(5 * (i + 1), 3);
     }
     // every MMA issued so far has completed before TMEM is released
-    if (lane == 0) {
+    if (tc::elect_one()) {
       tc::commit(bar(&sh->done));
       mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));
     }

@@ -65,6 +65,15 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool a
 }
 
 // ---------------------------------------------------------------- MMA
+// True in one lane of a converged warp, the same one every time.  An MMA
+// issued under this predicate costs the issuing warp little; under a
+// comparison with the lane index every tcgen05.mma takes at least 93 cycles,
+// because its operands are not known to be uniform across the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // D[tmem] (+)= A[smem desc] * B[smem desc]; issued by one thread.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, bool accumulate) {
