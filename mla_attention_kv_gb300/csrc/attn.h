@@ -96,11 +96,11 @@ struct PromptParams {
 // from (a map is a function of address, sizes and strides alone).
 struct PromptMaps {
   struct Key {
-    PromptTensor t[5];
-    int b, s, heads, kv_heads;
+    PromptTensor t[3];
+    int b, s, kv_heads;
   } key;
   bool valid;
-  CUtensorMap map[5];  // q_nope, q_pe, k_nope, k_pe, value
+  CUtensorMap map[3];  // k_nope, k_pe, value
 };
 cudaError_t prompt_tc_launch(bool bf16, const PromptParams& p, PromptMaps* maps, cudaStream_t stream);
 

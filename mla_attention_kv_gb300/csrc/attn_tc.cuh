@@ -6,26 +6,31 @@
 
 namespace mla {
 
+// A value that is the same in every lane, made known as such to the compiler:
+// the operands of tcgen05 and TMA instructions are uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(~0u, v); }
+
 // Bounded mbarrier wait shared by all roles of a CTA; gives up on the time
 // budget or when another role has already given up.
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                         unsigned long long budget, unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t n = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if (((++n) & 63) == 0) {
+  // (the timer is read only after some tries: reading it costs about as much as a wait usually takes)
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63) == 0) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > budget) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > budget) {
         *abort = 1;
         atomicOr(status, kStatusTimeout);
         return false;
       }
     }
   }
-  return true;
 }
-
 // The same for a whole warp: all lanes get one answer.
 __device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
                                              unsigned long long budget, unsigned* status) {

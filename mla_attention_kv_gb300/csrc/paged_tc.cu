@@ -19,8 +19,9 @@
 // Keys: a tile is nine blocks of 64 keys x 64 columns (8 KB, 128-byte
 // swizzle) by TMA, in boxes of the largest power of two that divides the
 // page (8 to 64 rows).  Five blocks serve the scores alone and are released
-// as soon as their MMAs are done (ring of eight); the four of this CTA's
-// output half are the B operand of both products (ring of three tiles).
+// as soon as their MMAs are done (one stage); the four of this CTA's output
+// half are the B operand of both products (three stages).  Tiles are
+// requested into L2 four tiles ahead of their copies.
 // MMA order: scores of tile i + 1, then output of tile i, so the softmax of
 // a tile runs under the scores of the next.
 //
@@ -41,19 +42,21 @@ namespace {
 constexpr int kUtThreads = 192;
 constexpr int kUtRows = kPagedTcRows;  // 128
 constexpr uint32_t kBlk = 8192;        // 64 keys x 64 columns
-constexpr int kNSlots = 8, kVTiles = 3;
+constexpr int kNTiles = 1, kVTiles = 3;  // stages of the two rings
+constexpr int kAhead = 4;                // key tiles requested into L2 ahead of their copies
+constexpr uint32_t kNBytes = 5 * kBlk, kVBytes = 4 * kBlk;
 constexpr uint32_t kUtQ = 0;                              // 4 chunks of [128 x 64]
 constexpr uint32_t kUtV = kUtQ + 4 * 16384;               // [kVTiles][4] blocks
-constexpr uint32_t kUtN = kUtV + kVTiles * 4 * kBlk;      // [kNSlots] blocks
-constexpr uint32_t kUtBar = kUtN + kNSlots * kBlk;        // 229376
+constexpr uint32_t kUtN = kUtV + kVTiles * kVBytes;       // [kNTiles][5] blocks
+constexpr uint32_t kUtBar = kUtN + kNTiles * kNBytes;
 constexpr uint32_t kUtSmem = kUtBar + 512 + 1024;
 static_assert(kUtSmem <= 232448, "shared memory of one CTA");
-static_assert(sizeof(PlanShared) <= kNSlots * kBlk, "the plan is made in the key ring before any copy");
+static_assert(sizeof(PlanShared) <= kNTiles * kNBytes, "the plan is made in the key ring before any copy");
 constexpr uint32_t kTmS = 256, kTmP = 320, kTmQ = 352;
 constexpr float kRescale = 8.0f;
 
 struct UtShared {
-  uint64_t nfull[kNSlots], nempty[kNSlots];
+  uint64_t nfull[kNTiles], nempty[kNTiles];
   uint64_t vfull[kVTiles], vempty[kVTiles];
   uint64_t qready, sfull, sfree, pfull, pvdone, ofree, done;
   uint32_t tmem;
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   UtShared* sh = reinterpret_cast<UtShared*>(smem + kUtBar);
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int H = p.heads;
   volatile int* abort = &sh->abort;
   auto bar = [](uint64_t* b) { return smem_u32(b); };
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
   first.seek(p, plan, kUtRows, x0);
 
   if (tid == 0) {
-    for (int i = 0; i < kNSlots; ++i) {
+    for (int i = 0; i < kNTiles; ++i) {
       mbar_init(bar(&sh->nfull[i]), 1);
       mbar_init(bar(&sh->nempty[i]), 1);
     }
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = uniform(sh->tmem);
 
   // the key tiles [t0, t1) of an item that fall to this worker
   auto span = [&](const PlanCursor& c, int* t0, int* t1) {
@@ -152,118 +155,112 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
         }
         return blk * p.page + (k - pg * p.page);
       };
+      // (both CTAs copy every row; each requests its own half of the columns)
+      auto request = [&](int r) {
+        if (r < 0 || r >= zero_row) return;
+        for (int j = 0; j < 4; ++j) tma_prefetch_2d(&a.lat, (half * 4 + j) * 64, r);
+        if (half) tma_prefetch_2d(&a.kpe, 0, r);
+      };
       int row = t0 < t1 ? rows_of(t0) : -1;
+      for (int t = t0 + 1; t < t0 + kAhead; ++t) request(rows_of(t));
+      int far = rows_of(t0 + kAhead);
       for (int t = t0; t < t1 && ok; ++t) {
+        request(far);
+        far = rows_of(t + 1 + kAhead);
         const int next = rows_of(t + 1);
         const uint32_t boxes = __popc(__ballot_sync(~0u, row >= 0));
-        for (int j = 0; j < 5; ++j, ++un) {
-          const uint32_t s = un % kNSlots;
-          if (!wait(&sh->nempty[s], ((un / kNSlots) & 1) ^ 1)) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(&sh->nfull[s]), boxes * box * 128);
-          __syncwarp();
-          if (row >= 0) {
-            const uint32_t d = sbase + kUtN + s * kBlk + lane * box * 128;
-            if (j < 4) tma_load_2d(d, &a.lat, ((half ^ 1) * 4 + j) * 64, row, bar(&sh->nfull[s]));
-            else tma_load_2d(d, &a.kpe, 0, row, bar(&sh->nfull[s]));
-          }
+        const uint32_t n = un % kNTiles;
+        if (!wait(&sh->nempty[n], ((un / kNTiles) & 1) ^ 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(&sh->nfull[n]), boxes * box * 640);
+        __syncwarp();
+        if (row >= 0) {
+          const uint32_t d = sbase + kUtN + n * kNBytes + lane * box * 128;
+          for (int j = 0; j < 4; ++j) tma_load_2d(d + j * kBlk, &a.lat, ((half ^ 1) * 4 + j) * 64, row, bar(&sh->nfull[n]));
+          tma_load_2d(d + 4 * kBlk, &a.kpe, 0, row, bar(&sh->nfull[n]));
         }
-        if (!ok) break;
+        ++un;
         const uint32_t s = uv % kVTiles;
         if (!wait(&sh->vempty[s], ((uv / kVTiles) & 1) ^ 1)) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(&sh->vfull[s]), boxes * box * 512);
         __syncwarp();
         if (row >= 0)
           for (int j = 0; j < 4; ++j)
-            tma_load_2d(sbase + kUtV + (s * 4 + j) * kBlk + lane * box * 128, &a.lat, (half * 4 + j) * 64, row, bar(&sh->vfull[s]));
+            tma_load_2d(sbase + kUtV + s * kVBytes + j * kBlk + lane * box * 128, &a.lat, (half * 4 + j) * 64, row, bar(&sh->vfull[s]));
         ++uv;
         row = next;
       }
     }
     // every issued copy has landed before the CTA may exit
     __syncwarp();
-    for (uint32_t u = un > kNSlots ? un - kNSlots : 0; u < un; ++u)
-      mbar_wait_bounded(bar(&sh->nfull[u % kNSlots]), (u / kNSlots) & 1, drain_budget(p.budget_ns));
+    for (uint32_t u = un > kNTiles ? un - kNTiles : 0; u < un; ++u)
+      mbar_wait_bounded(bar(&sh->nfull[u % kNTiles]), (u / kNTiles) & 1, drain_budget(p.budget_ns));
     for (uint32_t u = uv > kVTiles ? uv - kVTiles : 0; u < uv; ++u)
       mbar_wait_bounded(bar(&sh->vfull[u % kVTiles]), (u / kVTiles) & 1, drain_budget(p.budget_ns));
   } else if (warp == 5) {
-    // ============================================================ MMA (whole warp; an elected lane issues)
-    const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 64, false, false);
-    const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 256, false, true);
-    const uint64_t dk = tc::sdesc_sw128(sbase, 16, 1024);
-    const uint64_t dv = tc::sdesc_sw128(sbase, kBlk, 1024);
-    bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t par) {
-      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
-      return ok;
-    };
-    uint32_t un = 0, g_qk = 0, g_pv = 0, item = 0;
-    auto qk = [&]() {  // scores of tile g_qk
-      if (!wait(&sh->sfree, (g_qk & 1) ^ 1)) return;
-      tc::fence_after_sync();
-      for (int j = 0; j < 5; ++j, ++un) {
-        const uint32_t s = un % kNSlots;
-        if (!wait(&sh->nfull[s], (un / kNSlots) & 1)) return;
-        if (tc::elect_one()) {
-          const uint64_t bd = dk + ((kUtN + s * kBlk) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_f16_ts(tmem + kTmS, tmem + kTmQ + j * 32 + k * 8, bd + 2 * k, id_qk, j > 0 || k > 0);
-          tc::commit(bar(&sh->nempty[s]));
-        }
-        __syncwarp();
-      }
-      const uint32_t s = g_qk % kVTiles;
-      if (!wait(&sh->vfull[s], (g_qk / kVTiles) & 1)) return;
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t ad = dk + ((kUtQ + j * 16384) >> 4), bd = dk + ((kUtV + (s * 4 + j) * kBlk) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tc::mma_f16(tmem + kTmS, ad + 2 * k, bd + 2 * k, id_qk, true);
-        }
-        tc::commit(bar(&sh->sfull));
-      }
-      __syncwarp();
-      ++g_qk;
-    };
-    PlanCursor c = first;
-    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kUtRows)) {
-      int t0, t1;
-      const int keys = span(c, &t0, &t1);
-      if (t0 >= t1) continue;
-      if (!wait(&sh->qready, item & 1)) break;
-      tc::fence_after_sync();
-      qk();
-      for (int t = t0; t < t1 && ok; ++t) {
-        if (t + 1 < t1) qk();
-        if (!ok) break;
-        // output of tile t
-        const uint32_t s = g_pv % kVTiles;
-        const int valid = keys - t * kKeyTile;
-        if (valid < kKeyTile) {  // latents past the keys: whole 128-byte rows, so the swizzle does not matter
-          for (int x = lane; x < (kKeyTile - valid) * 32; x += 32) {
-            const int r = valid + x / 32, q = x % 32;
-            *reinterpret_cast<uint4*>(smem + kUtV + (s * 4 + (q >> 3)) * kBlk + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (t == t0 && item > 0 && !wait(&sh->ofree, (item - 1) & 1)) break;
-        if (!wait(&sh->pfull, g_pv & 1)) break;
+    // ============================================================ MMA (one thread)
+    if (tc::elect_one()) {
+      const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 64, false, false);
+      const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 256, false, true);
+      const uint64_t dn = tc::sdesc_sw128(sbase + kUtN, 16, 1024), dq = tc::sdesc_sw128(sbase + kUtQ, 16, 1024);
+      const uint64_t dvk = tc::sdesc_sw128(sbase + kUtV, 16, 1024), dv = tc::sdesc_sw128(sbase + kUtV, kBlk, 1024);
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        ok = ok && at_wait(bar(b), par, abort, p.budget_ns, p.status);
+        return ok;
+      };
+      uint32_t ns = 0, np = 0, ks = 0, kp = 0, vs = 0;  // stages (and phases) of the rings
+      uint32_t g_qk = 0, g_pv = 0, item = 0;
+      auto qk = [&]() {  // scores of tile g_qk
+        if (!wait(&sh->sfree, (g_qk & 1) ^ 1) || !wait(&sh->nfull[ns], np)) return;
         tc::fence_after_sync();
-        if (tc::elect_one()) {
-          const uint64_t bd = dv + ((kUtV + s * 4 * kBlk) >> 4);
+        const uint64_t bn = dn + ns * (kNBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc::mma_f16_ts(tmem, tmem + kTmP + k * 8, bd + k * 128, id_pv, t > t0 || k > 0);
-          tc::commit(bar(&sh->vempty[s]));
-          tc::commit(bar(&sh->pvdone));
+        for (int k = 0; k < 20; ++k)
+          tc::mma_f16_ts(tmem + kTmS, tmem + kTmQ + k * 8, bn + (k >> 2) * (kBlk >> 4) + 2 * (k & 3), id_qk, k > 0);
+        tc::commit(bar(&sh->nempty[ns]));
+        if (++ns == kNTiles) {
+          ns = 0;
+          np ^= 1;
         }
-        __syncwarp();
-        ++g_pv;
+        if (!wait(&sh->vfull[ks], kp)) return;
+        const uint64_t bv = dvk + ks * (kVBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          tc::mma_f16(tmem + kTmS, dq + (k >> 2) * (16384 >> 4) + 2 * (k & 3), bv + (k >> 2) * (kBlk >> 4) + 2 * (k & 3), id_qk, true);
+        tc::commit(bar(&sh->sfull));
+        if (++ks == kVTiles) {
+          ks = 0;
+          kp ^= 1;
+        }
+        ++g_qk;
+      };
+      PlanCursor c = first;
+      for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kUtRows)) {
+        int t0, t1;
+        span(c, &t0, &t1);
+        if (t0 >= t1) continue;
+        if (!wait(&sh->qready, item & 1)) break;
+        tc::fence_after_sync();
+        qk();
+        for (int t = t0; t < t1 && ok; ++t) {
+          if (t + 1 < t1) qk();
+          if (!ok) break;
+          // output of tile t
+          if (t == t0 && item > 0 && !wait(&sh->ofree, (item - 1) & 1)) break;
+          if (!wait(&sh->pfull, g_pv & 1)) break;
+          tc::fence_after_sync();
+          const uint64_t bd = dv + vs * (kVBytes >> 4);
+          tc::mma_f16_ts(tmem, tmem + kTmP, bd, id_pv, t > t0);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) tc::mma_f16_ts(tmem, tmem + kTmP + k * 8, bd + k * 128, id_pv, true);
+          tc::commit(bar(&sh->vempty[vs]));
+          tc::commit(bar(&sh->pvdone));
+          if (++vs == kVTiles) vs = 0;
+          ++g_pv;
+        }
+        ++item;
       }
-      ++item;
-    }
-    if (tc::elect_one()) {  // every MMA issued so far has completed before TMEM is released
+      // every MMA issued so far has completed before TMEM is released
       tc::commit(bar(&sh->done));
       mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));
     }
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
     }
     for (bool more = true; more && c.lo < x1 && ok;) {
       int t0, t1;
-      span(c, &t0, &t1);
+      const int keys = span(c, &t0, &t1);
       const int row = c.j * kUtRows + r;
       const bool live = row < c.q.n * H;
       const int limit0 = live ? c.q.keys_of_row(row, H) : 0;
@@ -378,6 +375,14 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
         tc::st16(tmem + lanes + kTmP + 16, pk + 16);
         tc::wait_st();
         tc::fence_before_sync();
+        const int valid = keys - t * kKeyTile;
+        if (valid < kKeyTile) {
+          // latents past the keys: whole 128-byte rows, so the swizzle does not matter (the scores of this tile,
+          // which read them too, are done)
+          for (int x = tid; x < (kKeyTile - valid) * 32; x += 128)
+            *reinterpret_cast<uint4*>(smem + kUtV + (g % kVTiles) * kVBytes + ((x >> 3) & 3) * kBlk + (valid + x / 32) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+        }
         arrive(&sh->pfull);
       }
       if (!ok) break;

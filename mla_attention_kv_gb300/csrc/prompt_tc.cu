@@ -9,27 +9,33 @@
 // for their product with the values (the operand type of the MMA), the sum
 // takes them before that.
 //
-// One CTA per 256 query rows of a head, as two tiles of 128 that share every
-// key tile (128 keys) and take turns on the tensor core: while one tile's
-// scores are in the softmax warps the other tile's MMAs run.  Per pair of
-// 128 x 128 tiles the MMA needs 2 * (768 + 512) cycles (QK: 12 steps of
-// K = 16, PV: 8), the softmax one exponential per score.
+// A cluster of two CTAs takes 256 query rows of a head, each CTA 128 of them;
+// both need the same keys and values, so each loads half of every stage and
+// multicasts it to both (L2 would have to deliver 55 bytes per cycle and SM
+// otherwise).
 //
-// Tensor memory (512 columns): S0, S1 (128 each, fp32 scores; the rounded
-// weights overwrite the first 64 columns of theirs and are the A operand of
-// the PV MMA), O0, O1 (128 each).  Shared memory: the queries (96 KB) and a
-// ring of eight 16 KB slots; a key tile is three slots (64 columns each, 128
-// bytes a row, 128-byte swizzle), its values two.
+// Tensor memory: scores S0, S1 (128 columns each, by the parity of the key
+// tile; the rounded weights overwrite the first 64 columns of theirs and are
+// the A operand of the second product), output (128), queries (96). With both
+// A operands in tensor memory an MMA of 128 x 128 x 16 takes 74 cycles
+// (measured; 107 with A in shared memory, 64 by the peak rate), so a tile of
+// 128 keys takes 12 * 74 + 8 * 74 = 1480 cycles, and all of shared memory is
+// a ring of thirteen 16 KB slots for keys (three slots of 64 columns, 128
+// bytes a row, 128-byte swizzle) and values (two).
+//
+// MMA order: scores of tile i + 1, then output of tile i, so the softmax of
+// a tile runs under the scores of the next and the output of the previous.
 //
 // The output is rescaled only when a row's maximum has grown by more than 2^8
 // since the last time (weights are then at most 2^8: the sums stay exact to
 // fp32 and 2^8 * 128 keys is far inside fp16's range): rare after the first
 // tiles.
 //
-// Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a thread owns a row), 8 TMA,
-// 9 MMA.  Value rows past the sequence's end (tokens of no or another
-// sequence, which may hold anything) are zeroed in shared memory by warp 9
-// before the MMA reads them; scores of such keys are masked.
+// Warps: 0-7 queries, softmax, results (a row belongs to two threads, 64 keys
+// of a tile each: warps q and q + 4), 8 TMA, 9 MMA.  Value rows past the
+// sequence's end (tokens of no or another sequence, which may hold anything)
+// are zeroed in shared memory by the softmax warps before the MMA reads them;
+// scores of such keys are masked.
 #include <string.h>
 
 #include "attn.h"
@@ -41,67 +47,76 @@ namespace mla {
 namespace {
 
 constexpr int kPtThreads = 320;
-constexpr int kPtRows = 256;   // query rows per CTA
-constexpr int kPtTile = 128;   // query rows per MMA tile, keys per tile
-constexpr int kPtSlots = 8;
-constexpr uint32_t kPtSlotBytes = 16384;
-constexpr uint32_t kPtQBytes = 3 * 16384;  // one tile's queries
-constexpr uint32_t kPtRing = 2 * kPtQBytes;
-constexpr uint32_t kPtBar = kPtRing + kPtSlots * kPtSlotBytes;
-constexpr uint32_t kPtSmem = kPtBar + 512 + 1024;  // + alignment slack
+constexpr int kPtTile = 128;   // query rows per CTA, keys per tile
+constexpr int kPtRows = 256;   // query rows per cluster
+constexpr int kKStages = 3, kVStages = 2;
+constexpr uint32_t kBlock = 16384;  // 128 keys x 64 columns
+constexpr uint32_t kKBytes = 3 * kBlock, kVBytes = 2 * kBlock;
+constexpr uint32_t kPtV = kKStages * kKBytes;
+constexpr uint32_t kPtBar = kPtV + kVStages * kVBytes;
+constexpr uint32_t kPtSmem = kPtBar + 4096 + 1024;  // + alignment slack
 static_assert(kPtSmem <= 232448, "shared memory of one CTA");
+constexpr uint32_t kTmO = 256, kTmQ = 384;  // tensor memory columns; S0 at 0, S1 at 128
 constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that rescales the output
 
 struct PtShared {
-  uint64_t full[kPtSlots], empty[kPtSlots];
-  uint64_t qfull[2], sfull[2], pfull[2], ofull[2];
-  uint64_t done;
+  uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
+  uint64_t sfull[2], pfull[2];
+  uint64_t qready, pvdone, done, pair[4];
+  float row[2][2][128];  // exchange between the two threads of a row: [tile parity][half][row]
   PromptPlanShared plan;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(PtShared) <= 512, "barrier block");
+static_assert(sizeof(PtShared) <= 4096, "barrier block");
 
 struct PtArgs {
-  CUtensorMap qn, qp, kn, kp, v;
+  CUtensorMap kn, kp, v;
   PromptParams p;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_constant__ PtArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ PtArgs a) {
   using E = Elem<T>;
   const PromptParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   PtShared* sh = reinterpret_cast<PtShared*>(smem + kPtBar);
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   volatile int* abort = &sh->abort;
   auto bar = [](uint64_t* b) { return smem_u32(b); };
+  const int rank = blockIdx.x & 1;  // (clusters are pairs of neighbours along x)
 
   PromptPlace pl;
-  if (!prompt_place(p, &sh->plan, blockIdx.x, kPtRows, &pl, blockIdx.x == 0 && blockIdx.y == 0)) return;
+  if (!prompt_place(p, &sh->plan, blockIdx.x >> 1, kPtRows, &pl, blockIdx.x == 0 && blockIdx.y == 0)) return;
   const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-  // key tiles of the two query tiles (tile 1 may have no rows)
-  const int rows = min(kPtRows, pl.len - pl.row0);
+  // key tiles of the two CTAs (the second may have no rows)
   auto tiles_of = [&](int w) {
-    if (w * kPtTile >= rows) return 0;
-    const int end = p.causal ? min(pl.len, pl.row0 + (w + 1) * kPtTile) : pl.len;
+    const int r0 = pl.row0 + w * kPtTile;
+    if (r0 >= pl.len) return 0;
+    const int end = p.causal ? min(pl.len, r0 + kPtTile) : pl.len;
     return (end + kPtTile - 1) / kPtTile;
   };
-  const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
+  const int n = uniform(tiles_of(rank)), nt = uniform(max(tiles_of(0), tiles_of(1)));
 
   if (tid == 0) {
-    for (int i = 0; i < kPtSlots; ++i) {
-      mbar_init(bar(&sh->full[i]), 1);
-      mbar_init(bar(&sh->empty[i]), 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(bar(&sh->kfull[i]), 1);
+      mbar_init(bar(&sh->kempty[i]), 2);  // the MMA warps of both CTAs
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(bar(&sh->vfull[i]), 1);
+      mbar_init(bar(&sh->vempty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&sh->qfull[i]), 1);
       mbar_init(bar(&sh->sfull[i]), 1);
-      mbar_init(bar(&sh->pfull[i]), 4);
-      mbar_init(bar(&sh->ofull[i]), 1);
+      mbar_init(bar(&sh->pfull[i]), 8);
     }
+    mbar_init(bar(&sh->qready), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(&sh->pair[i]), 2);
+    mbar_init(bar(&sh->pvdone), 1);
     mbar_init(bar(&sh->done), 1);
     sh->abort = 0;
     fence_mbar_init();
@@ -109,167 +124,185 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
   if (warp == 9) tc::tmem_alloc(smem_u32(&sh->tmem), 512);
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers are initialised before any copy or commit reaches them
   tc::fence_after_sync();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = uniform(sh->tmem);
 
   if (warp == 8) {
     // ============================================================ TMA
-    if (lane == 0) {
-      for (int w = 0; w < 2; ++w) {
-        if ((w ? n1 : n0) == 0) continue;
-        const uint32_t q = sbase + w * kPtQBytes, b = bar(&sh->qfull[w]);
-        const int tok = pl.begin + pl.row0 + w * kPtTile;
-        mbar_arrive_expect_tx(b, kPtQBytes);
-        tma_load_4d(q, &a.qn, 0, tok, h, pl.batch, b);
-        tma_load_4d(q + 16384, &a.qn, 64, tok, h, pl.batch, b);
-        tma_load_4d(q + 32768, &a.qp, 0, tok, h, pl.batch, b);
-      }
-      uint32_t u = 0;
-      bool ok = true;
-      for (int i = 0; i < nt && ok; ++i) {
-        const int tok = pl.begin + i * kPtTile;
-        for (int c = 0; c < 5; ++c, ++u) {
-          const uint32_t s = u % kPtSlots;
-          if (!at_wait(bar(&sh->empty[s]), ((u / kPtSlots) & 1) ^ 1, abort, p.budget_ns, p.status)) { ok = false; break; }
-          const uint32_t d = sbase + kPtRing + s * kPtSlotBytes, b = bar(&sh->full[s]);
-          mbar_arrive_expect_tx(b, kPtSlotBytes);
-          if (c < 2) tma_load_4d(d, &a.kn, c * 64, tok, hk, pl.batch, b);
-          else if (c == 2) tma_load_4d(d, &a.kp, 0, tok, 0, pl.batch, b);
-          else tma_load_4d(d, &a.v, (c - 3) * 64, tok, hk, pl.batch, b);
-        }
-      }
-      // every issued copy has landed before the CTA may exit
-      for (uint32_t v = u > kPtSlots ? u - kPtSlots : 0; v < u; ++v)
-        mbar_wait_bounded(bar(&sh->full[v % kPtSlots]), (v / kPtSlots) & 1, drain_budget(p.budget_ns));
-      for (int w = 0; w < 2; ++w)
-        if ((w ? n1 : n0) > 0) mbar_wait_bounded(bar(&sh->qfull[w]), 0, drain_budget(p.budget_ns));
-    }
-  } else if (warp == 9) {
-    // ============================================================ MMA (whole warp; an elected lane issues)
-    const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 128, false, false);
-    const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 128, false, true);
-    const uint32_t id_pv64 = tc::idesc_f16(E::kBf16, 128, 64, false, true);
-    const uint64_t dk0 = tc::sdesc_sw128(sbase, 16, 1024);            // K-major: queries, keys
-    const uint64_t dv0 = tc::sdesc_sw128(sbase, kPtSlotBytes, 1024);  // MN-major: values
-    bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t par) {
-      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
-      return ok;
-    };
-    auto slot_full = [&](uint32_t u) { return wait(&sh->full[u % kPtSlots], (u / kPtSlots) & 1); };
-    auto qk = [&](int w, int i) {  // S_w = Q_w K_i^T
-      for (int c = 0; c < 3; ++c) {
-        const uint32_t u = 5 * i + c;
-        if (!slot_full(u)) return;
-        if (tc::elect_one()) {
-          const uint64_t ad = dk0 + ((w * kPtQBytes + c * 16384) >> 4);
-          const uint64_t bd = dk0 + ((kPtRing + (u % kPtSlots) * kPtSlotBytes) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tc::mma_f16(tmem + w * 128, ad + 2 * k, bd + 2 * k, id_qk, c > 0 || k > 0);
-        }
-      }
-      if (tc::elect_one()) tc::commit(bar(&sh->sfull[w]));
-      __syncwarp();
-    };
-    auto release = [&](uint32_t u, int n) {
-      if (tc::elect_one())
-        for (int c = 0; c < n; ++c) tc::commit(bar(&sh->empty[(u + c) % kPtSlots]));
-      __syncwarp();
-    };
-    bool zeroed = false;
-    auto pv = [&](int w, int i, bool last) {  // O_w += P_w V_i
-      const uint32_t u = 5 * i + 3;
-      if (!slot_full(u) || !slot_full(u + 1)) return;
-      const int valid = pl.len - i * kPtTile;
-      if (valid < kPtTile && !zeroed) {
-        // rows past the sequence's end: whole 128-byte rows, so the swizzle does not matter
-        for (int x = lane; x < (kPtTile - valid) * 16; x += 32) {
-          const int r = valid + x / 16, c = x % 16;
-          const uint32_t sl = (u + (c >> 3)) % kPtSlots;
-          *reinterpret_cast<uint4*>(smem + kPtRing + sl * kPtSlotBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        zeroed = true;
-      }
-      if (!wait(&sh->pfull[w], i & 1)) return;
-      tc::fence_after_sync();
-      if (tc::elect_one()) {
-        const uint32_t s0 = u % kPtSlots, s1 = (u + 1) % kPtSlots;
-        const uint64_t b0 = dv0 + ((kPtRing + s0 * kPtSlotBytes) >> 4), b1 = dv0 + ((kPtRing + s1 * kPtSlotBytes) >> 4);
-        const uint32_t o = tmem + 256 + w * 128, pa = tmem + w * 128;
-        if (s1 == s0 + 1) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) tc::mma_f16_ts(o, pa + k * 8, b0 + k * 128, id_pv, i > 0 || k > 0);
-        } else {  // the pair wraps around the ring
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            tc::mma_f16_ts(o, pa + k * 8, b0 + k * 128, id_pv64, i > 0 || k > 0);
-            tc::mma_f16_ts(o + 64, pa + k * 8, b1 + k * 128, id_pv64, i > 0 || k > 0);
-          }
-        }
-        if (last) tc::commit(bar(&sh->ofull[w]));
-      }
-      __syncwarp();
-    };
-    if (n0 > 0 && wait(&sh->qfull[0], 0)) qk(0, 0);
-    if (n1 > 0 && ok && wait(&sh->qfull[1], 0)) qk(1, 0);
-    if (ok) release(0, 3);
-    for (int i = 0; i < nt && ok; ++i) {
-      if (i < n0) pv(0, i, i == n0 - 1);
-      if (ok && i + 1 < n0) qk(0, i + 1);
-      if (ok && i < n1) pv(1, i, i == n1 - 1);
-      if (!ok) break;
-      release(5 * i + 3, 2);
-      if (i + 1 < n1) qk(1, i + 1);
-      if (ok && i + 1 < nt) release(5 * (i + 1), 3);
-    }
-    // every MMA issued so far has completed before TMEM is released
     if (tc::elect_one()) {
+      int nk = 0, nv = 0;  // stages filled
+      bool ok = true;
+      // this CTA's 64 rows of every block go to both CTAs
+      auto keys = [&](int i) {
+        const uint32_t s = i % kKStages, b = bar(&sh->kfull[s]), d = sbase + s * kKBytes + rank * (kBlock / 2);
+        ok = ok && at_wait(bar(&sh->kempty[s]), ((i / kKStages) & 1) ^ 1, abort, p.budget_ns, p.status);
+        if (!ok) return;
+        const int tok = pl.begin + i * kPtTile + rank * 64;
+        mbar_arrive_expect_tx(b, kKBytes);
+        tma_load_4d_multicast(d, &a.kn, 0, tok, hk, pl.batch, b, 3);
+        tma_load_4d_multicast(d + kBlock, &a.kn, 64, tok, hk, pl.batch, b, 3);
+        tma_load_4d_multicast(d + 2 * kBlock, &a.kp, 0, tok, 0, pl.batch, b, 3);
+        ++nk;
+      };
+      auto values = [&](int i) {
+        const uint32_t s = i % kVStages, b = bar(&sh->vfull[s]), d = sbase + kPtV + s * kVBytes + rank * (kBlock / 2);
+        ok = ok && at_wait(bar(&sh->vempty[s]), ((i / kVStages) & 1) ^ 1, abort, p.budget_ns, p.status);
+        if (!ok) return;
+        const int tok = pl.begin + i * kPtTile + rank * 64;
+        mbar_arrive_expect_tx(b, kVBytes);
+        tma_load_4d_multicast(d, &a.v, 0, tok, hk, pl.batch, b, 3);
+        tma_load_4d_multicast(d + kBlock, &a.v, 64, tok, hk, pl.batch, b, 3);
+        ++nv;
+      };
+      keys(0);
+      for (int i = 0; i < nt && ok; ++i) {
+        if (i + 1 < nt) keys(i + 1);
+        values(i);
+      }
+      // every copy into this CTA, and every release of a stage by the peer, has landed before the cluster may exit
+      const uint64_t t0 = globaltimer_ns();
+      auto drain = [&](uint64_t* b, int use, int stages) {
+        const uint64_t spent = globaltimer_ns() - t0, limit = drain_budget(p.budget_ns);
+        mbar_wait_bounded(bar(b + use % stages), (use / stages) & 1, spent < limit ? limit - spent : 0);
+      };
+      for (int v = max(0, nk - kKStages); v < nk; ++v) {
+        drain(sh->kfull, v, kKStages);
+        drain(sh->kempty, v, kKStages);
+      }
+      for (int v = max(0, nv - kVStages); v < nv; ++v) {
+        drain(sh->vfull, v, kVStages);
+        drain(sh->vempty, v, kVStages);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ============================================================ MMA (one thread)
+    if (tc::elect_one()) {
+      const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 128, false, false);
+      const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 128, false, true);
+      const uint64_t dk = tc::sdesc_sw128(sbase, 16, 1024);             // K-major: keys
+      const uint64_t dv = tc::sdesc_sw128(sbase + kPtV, kBlock, 1024);  // MN-major: values
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        ok = ok && at_wait(bar(b), par, abort, p.budget_ns, p.status);
+        return ok;
+      };
+      uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stage and phase of the rings
+      auto qk = [&](int i) {  // S = Q K_i^T (past this CTA's last tile: release the stage only)
+        if (!wait(&sh->kfull[ks], kp)) return;
+        if (i < n) {
+          const uint64_t bd = dk + ks * (kKBytes >> 4);
+          const uint32_t d = tmem + (i & 1) * 128;
+#pragma unroll
+          for (int k = 0; k < 12; ++k)
+            tc::mma_f16_ts(d, tmem + kTmQ + k * 8, bd + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), id_qk, k > 0);
+          tc::commit(bar(&sh->sfull[i & 1]));
+        }
+        tc::commit_multicast(bar(&sh->kempty[ks]), 3);
+        if (++ks == kKStages) {
+          ks = 0;
+          kp ^= 1;
+        }
+      };
+      auto pv = [&](int i) {  // O += P V_i
+        if (!wait(&sh->vfull[vs], vp)) return;
+        if (i < n) {
+          if (!wait(&sh->pfull[i & 1], (i >> 1) & 1)) return;
+          tc::fence_after_sync();
+          const uint64_t bd = dv + vs * (kVBytes >> 4);
+          const uint32_t pa = tmem + (i & 1) * 128;
+          tc::mma_f16_ts(tmem + kTmO, pa, bd, id_pv, i > 0);
+#pragma unroll
+          for (int k = 1; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, true);
+          tc::commit(bar(&sh->pvdone));
+        }
+        tc::commit_multicast(bar(&sh->vempty[vs]), 3);
+        if (++vs == kVStages) {
+          vs = 0;
+          vp ^= 1;
+        }
+      };
+      if (n > 0 && wait(&sh->qready, 0)) tc::fence_after_sync();
+      if (ok) qk(0);
+      for (int i = 0; i < nt && ok; ++i) {
+        if (i + 1 < nt) qk(i + 1);
+        if (ok) pv(i);
+      }
+      // every MMA issued so far has completed before TMEM is released
       tc::commit(bar(&sh->done));
       mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));
     }
     __syncwarp();
-  } else {
-    // ============================================================ softmax
-    const int w = warp >> 2;
-    const int n = w ? n1 : n0;
-    const int r = (warp & 3) * 32 + lane;
-    const int qi = pl.row0 + w * kPtTile + r;  // query's token in its sequence
-    const uint32_t ts = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t to = ts - w * 128 + 256 + w * 128;
+  } else if (n > 0) {
+    // ============================================================ queries, softmax, results
+    const int q = warp & 3, hf = warp >> 2;
+    const int r = q * 32 + lane;
+    const int qi = pl.row0 + rank * kPtTile + r;  // query's token in its sequence
+    const bool live = qi < pl.len;
+    const int tok = pl.begin + (live ? qi : 0);
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    {  // queries: q_nope by one thread of the row, q_pe by the other
+      const PromptTensor& t = hf ? p.q_pe : p.q_nope;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(t.ptr) + (size_t)pl.batch * t.sb + (size_t)h * t.sh + (size_t)tok * t.st);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (c && hf) break;
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = live ? src[c * 8 + i] : make_uint4(0, 0, 0, 0);
+        const uint32_t d = tl + kTmQ + hf * 64 + c * 32;
+        tc::st16(d, reinterpret_cast<const uint32_t*>(v));
+        tc::st16(d + 16, reinterpret_cast<const uint32_t*>(v + 4));
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh->qready));
+    }
     float m = -INFINITY;  // maximum the weights are relative to (raw score units)
-    float l = 0.f;
+    float l = 0.f;        // sum over this thread's keys
     const float scale = p.scale_log2;
     bool ok = true;
+    auto meet = [&](int k) {  // k-th meeting of the two warps of these rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh->pair[q]));
+      return at_wait_warp(bar(&sh->pair[q]), k & 1, abort, p.budget_ns, p.status);
+    };
     for (int i = 0; i < n; ++i) {
-      if (!at_wait_warp(bar(&sh->sfull[w]), i & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+      const uint32_t ts = tl + (i & 1) * 128;
+      if (!at_wait_warp(bar(&sh->sfull[i & 1]), (i >> 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
       tc::fence_after_sync();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) tc::ld32(ts + c, s + c);
+      uint32_t s[64];
+      tc::ld32(ts + hf * 64, s);
+      tc::ld32(ts + hf * 64 + 32, s + 32);
       tc::wait_ld();
-      // keys this row sees in this tile
-      const int limit = (p.causal ? min(qi + 1, pl.len) : pl.len) - i * kPtTile;
-      if (__any_sync(~0u, limit < kPtTile)) {
+      // keys this row sees among this thread's 64
+      const int limit = (p.causal ? min(qi + 1, pl.len) : pl.len) - i * kPtTile - hf * 64;
+      if (__any_sync(~0u, limit < 64)) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
+        for (int k = 0; k < 64; ++k)
           if (k >= limit) s[k] = 0xff800000u;
       }
       float mx[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
 #pragma unroll
-      for (int k = 4; k < 128; k += 4)
+      for (int k = 4; k < 64; k += 4)
 #pragma unroll
         for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[k + j]));
-      const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      sh->row[i & 1][hf][r] = tile_max;
+      // both threads of a row have their scores in registers and their maxima in place
+      if (!meet(i)) { ok = false; break; }
+      tile_max = fmaxf(tile_max, sh->row[i & 1][hf ^ 1][r]);
       if (__any_sync(~0u, (tile_max - m) * scale > kRescale)) {
-        // (the MMA that filled S was issued after the last one that wrote O: O is at rest)
         const float m_new = fmaxf(m, tile_max);
         const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * scale);
         if (i > 0) {
-          tmem_scale<128>(to, f);
+          if (!at_wait_warp(bar(&sh->pvdone), (i - 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+          tc::fence_after_sync();
+          tmem_scale<64>(tl + kTmO + hf * 64, f);
           tc::wait_st();
         }
         l *= f;
@@ -279,7 +312,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
       const uint64_t sc2 = f2_pack(scale, scale), ng2 = f2_pack(-mu * scale, -mu * scale);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -292,74 +325,88 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_tc_kernel(const __grid_c
           sum[k & 1] = f2_add(sum[k & 1], f2_pack(x0, x1));
           pk[k] = E::pack(x0, x1);
         }
-        tc::st16(ts + c * 16, pk);
+        tc::st16(ts + hf * 32 + c * 16, pk);
       }
       tc::wait_st();
       tc::fence_before_sync();
+      const int valid = pl.len - i * kPtTile;
+      if (valid < kPtTile) {
+        // value rows past the sequence's end: whole 128-byte rows, so the swizzle does not matter
+        const uint32_t vs = i % kVStages;
+        if (!at_wait_warp(bar(&sh->vfull[vs]), (i / kVStages) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+        for (int x = tid; x < (kPtTile - valid) * 16; x += 256)
+          *reinterpret_cast<uint4*>(smem + kPtV + vs * kVBytes + ((x >> 3) & 1) * kBlock + (valid + x / 16) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(&sh->pfull[w]));
+      if (lane == 0) mbar_arrive(bar(&sh->pfull[i & 1]));
       float a0, a1, b0, b1;
       f2_unpack(sum[0], a0, a1);
       f2_unpack(sum[1], b0, b1);
       l += (a0 + a1) + (b0 + b1);
     }
-    if (ok && n > 0 && at_wait_warp(bar(&sh->ofull[w]), 0, abort, p.budget_ns, p.status)) {
+    sh->row[n & 1][hf][r] = l;
+    // (phases of pvdone are awaited in order: a parity tells neighbours apart only, and the scores of tile
+    // n - 1 say no more than that the output of tile n - 3 is done)
+    ok = ok && meet(n) && (n < 2 || at_wait_warp(bar(&sh->pvdone), n & 1, abort, p.budget_ns, p.status)) &&
+         at_wait_warp(bar(&sh->pvdone), (n - 1) & 1, abort, p.budget_ns, p.status);
+    if (ok) {
       tc::fence_after_sync();
-      const bool live = w * kPtTile + r < rows;
+      l = sh->row[n & 1][0][r] + sh->row[n & 1][1][r];
       const float iv = l == 0.f ? 0.f : 1.f / l;
-      const int tok = pl.begin + qi;
-      T* out = static_cast<T*>(const_cast<void*>(p.out.ptr)) + (size_t)pl.batch * p.out.sb + (size_t)h * p.out.sh + (size_t)(live ? tok : 0) * p.out.st;
+      T* out = static_cast<T*>(const_cast<void*>(p.out.ptr)) + (size_t)pl.batch * p.out.sb + (size_t)h * p.out.sh + (size_t)tok * p.out.st + hf * 64;
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < 64; c += 32) {
         uint32_t o[32];
-        tc::ld32(to + c, o);
+        tc::ld32(tl + kTmO + hf * 64 + c, o);
         tc::wait_ld();
         if (live) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
-            uint32_t q[4];
+            uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              q[j] = E::pack(__uint_as_float(o[k + 2 * j]) * iv, __uint_as_float(o[k + 2 * j + 1]) * iv);
-            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(q[0], q[1], q[2], q[3]);
+              w[j] = E::pack(__uint_as_float(o[k + 2 * j]) * iv, __uint_as_float(o[k + 2 * j + 1]) * iv);
+            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
-      if (live && p.lse)
+      if (live && hf == 0 && p.lse)
         p.lse[((size_t)pl.batch * p.heads + h) * p.s + tok] = l == 0.f ? -INFINITY : (m * scale + log2f(l)) * kLn2;
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  tc::cluster_sync();  // the peer's copies and commits into this CTA are done
 }
 
 template <typename T>
 cudaError_t launch(const PromptParams& p, PromptMaps* m, cudaStream_t stream) {
   PromptMaps::Key key;
   memset(&key, 0, sizeof(key));
-  const PromptTensor* src[5] = {&p.q_nope, &p.q_pe, &p.k_nope, &p.k_pe, &p.value};
-  for (int i = 0; i < 5; ++i) key.t[i] = *src[i];
-  key.b = p.b; key.s = p.s; key.heads = p.heads; key.kv_heads = p.kv_heads;
+  const PromptTensor* src[3] = {&p.k_nope, &p.k_pe, &p.value};
+  for (int i = 0; i < 3; ++i) key.t[i] = *src[i];
+  key.b = p.b; key.s = p.s; key.kv_heads = p.kv_heads;
   if (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0) {
     m->valid = false;
-    const int width[5] = {kNope, kRope, kNope, kRope, kV};
-    const int heads[5] = {p.heads, p.heads, p.kv_heads, 1, p.kv_heads};
+    const int width[3] = {kNope, kRope, kV};
+    const int heads[3] = {p.kv_heads, 1, p.kv_heads};
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 3; ++i) {
       const PromptTensor& t = *src[i];
-      if (!encode_tmap_4d_rows(&m->map[i], dt, t.ptr, width[i], p.s, heads[i], p.b, t.st, heads[i] > 1 ? t.sh : width[i], t.sb, kPtTile))
+      if (!encode_tmap_4d_rows(&m->map[i], dt, t.ptr, width[i], p.s, heads[i], p.b, t.st, heads[i] > 1 ? t.sh : width[i], t.sb, kPtTile / 2))
         return cudaErrorInvalidValue;
     }
     m->key = key;
     m->valid = true;
   }
   PtArgs a;
-  a.qn = m->map[0]; a.qp = m->map[1]; a.kn = m->map[2]; a.kp = m->map[3]; a.v = m->map[4];
+  a.kn = m->map[0]; a.kp = m->map[1]; a.v = m->map[2];
   a.p = p;
   cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem);
   if (e != cudaSuccess) return e;
-  prompt_tc_kernel<T><<<dim3(prompt_blocks(p, kPtRows), p.heads), kPtThreads, kPtSmem, stream>>>(a);
+  prompt_tc_kernel<T><<<dim3(2 * prompt_blocks(p, kPtRows), p.heads), kPtThreads, kPtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
