@@ -403,6 +403,26 @@ mla_status mla_attn_status(mla_attn* h, cudaStream_t stream);
 /* Number of kernels the last call on this handle enqueued (-1: null handle). */
 int mla_attn_last_launches(mla_attn* h);
 
+typedef struct mla_latent_append_args {
+  const void* compressed_kv;   /* [T, 512]                     */
+  const void* k_pe;            /* [T, 64]                      */
+  const void* q_pe;            /* [T, H, 64] or NULL           */
+  const int32_t* positions;    /* [T] or NULL                  */
+  const void* gamma_kv;        /* [512] or NULL                */
+  const float* cos_table;      /* [max_pos, 64] or NULL        */
+  const float* sin_table;
+  const int32_t* slot_mapping; /* [T]                          */
+  void* latent_cache;
+  void* kpe_cache;
+  void* q_pe_out;              /* [T, H, 64] or NULL           */
+  int T;
+  int page_size, num_blocks;
+  int compressed_kv_stride, k_pe_stride;         /* between token rows */
+  int q_pe_token_stride, q_pe_head_stride;
+  int latent_row_stride, kpe_row_stride;         /* between cache rows */
+  int q_pe_out_token_stride, q_pe_out_head_stride;
+} mla_latent_append_args;
+
 /* Append T token rows to a paged latent cache, rotating positions on the way.
  *   compressed_kv [T, 512]   dtype   first 512 columns of kv_a_proj's rows
  *   k_pe          [T, 64]    dtype   its last 64 columns
@@ -428,14 +448,25 @@ int mla_attn_last_launches(mla_attn* h);
  * outside [0, max_pos) are clamped and reported (MLA_ERR_BAD_POSITION).
  * Errors: MLA_ERR_INVALID_ARG (also num_blocks * page_size > INT_MAX, bad
  * strides), MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
-mla_status mla_latent_append(mla_attn* h, int T, const void* compressed_kv, int ckv_stride,
-                             const void* k_pe, int k_pe_stride, const void* q_pe,
-                             int q_pe_token_stride, int q_pe_head_stride, const int32_t* positions,
-                             const void* gamma_kv, const float* cos_table, const float* sin_table,
-                             const int32_t* slot_mapping, int page_size, int num_blocks,
-                             void* latent_cache, int latent_row_stride, void* kpe_cache,
-                             int kpe_row_stride, void* q_pe_out, int q_pe_out_token_stride,
-                             int q_pe_out_head_stride, cudaStream_t stream);
+mla_status mla_latent_append(mla_attn* h, const mla_latent_append_args* args, cudaStream_t stream);
+
+typedef struct mla_attn_paged_args {
+  const void* q_latent;        /* [T, H, 512]                  */
+  const void* q_pe;            /* [T, H, 64]                   */
+  const int32_t* cu_q;         /* [num_seqs + 1] or NULL       */
+  const int32_t* kv_lens;      /* [num_seqs]                   */
+  const int32_t* block_table;  /* [num_seqs, table_stride]     */
+  const void* latent_cache;
+  const void* kpe_cache;
+  void* out;                   /* [T, H, 512], dense           */
+  float* lse;                  /* [T, H], dense, or NULL       */
+  int num_seqs, T;
+  int table_stride;
+  int page_size, num_blocks;
+  int q_latent_token_stride, q_latent_head_stride;
+  int q_pe_token_stride, q_pe_head_stride;
+  int latent_row_stride, kpe_row_stride;
+} mla_attn_paged_args;
 
 /* Attention of the newest tokens of num_seqs sequences over their paged
  * latent cache.  Per token row t and head h the query is [q_latent | q_pe]
@@ -465,13 +496,25 @@ mla_status mla_latent_append(mla_attn* h, int T, const void* compressed_kv, int 
  * reported (MLA_ERR_BAD_LENGTH).  Errors: MLA_ERR_INVALID_ARG (also T %
  * num_seqs != 0 without cu_q), MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED,
  * MLA_ERR_CUDA. */
-mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_latent,
-                              int q_latent_token_stride, int q_latent_head_stride, const void* q_pe,
-                              int q_pe_token_stride, int q_pe_head_stride, const int32_t* cu_q,
-                              const int32_t* kv_lens, const int32_t* block_table, int table_stride,
-                              const void* latent_cache, int latent_row_stride, const void* kpe_cache,
-                              int kpe_row_stride, int page_size, int num_blocks, void* out,
-                              float* lse, cudaStream_t stream);
+mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cudaStream_t stream);
+
+typedef struct mla_attn_prompt_args {
+  const void* q_nope;          /* [b, H, s, 128]               */
+  const void* q_pe;            /* [b, H, s, 64]                */
+  const void* k_nope;          /* [b, KH, s, 128]              */
+  const void* k_pe;            /* [b, 1, s, 64]                */
+  const void* value;           /* [b, KH, s, 128]              */
+  void* out;                   /* [b, H, s, 128]               */
+  float* lse;                  /* [b, H, s], dense, or NULL    */
+  const int32_t* cu_seqlens;   /* [num_seqs + 1] or NULL       */
+  int b, s, num_seqs, causal;
+  int q_nope_batch_stride, q_nope_head_stride, q_nope_token_stride;
+  int q_pe_batch_stride, q_pe_head_stride, q_pe_token_stride;
+  int k_nope_batch_stride, k_nope_head_stride, k_nope_token_stride;
+  int k_pe_batch_stride, k_pe_token_stride;
+  int value_batch_stride, value_head_stride, value_token_stride;
+  int out_batch_stride, out_head_stride, out_token_stride;
+} mla_attn_prompt_args;
 
 /* Attention over whole prompts in the up-projected form, on the outputs of
  * mla_kv_prolog_run (or mla_prolog_w8a8_run):
@@ -490,16 +533,7 @@ mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_la
  * must be finite within a sequence.  Offsets outside [0, s] or decreasing
  * are clamped and reported (MLA_ERR_BAD_LENGTH).  Errors as above; cu_seqlens
  * with b > 1 is MLA_ERR_INVALID_ARG. */
-mla_status mla_attn_prompt_run(mla_attn* h, int b, int s, const int32_t* cu_seqlens, int num_seqs,
-                               int causal, const void* q_nope, int q_nope_batch_stride,
-                               int q_nope_head_stride, int q_nope_token_stride, const void* q_pe,
-                               int q_pe_batch_stride, int q_pe_head_stride, int q_pe_token_stride,
-                               const void* k_nope, int k_nope_batch_stride, int k_nope_head_stride,
-                               int k_nope_token_stride, const void* k_pe, int k_pe_batch_stride,
-                               int k_pe_token_stride, const void* value, int value_batch_stride,
-                               int value_head_stride, int value_token_stride, void* out,
-                               int out_batch_stride, int out_head_stride, int out_token_stride,
-                               float* lse, cudaStream_t stream);
+mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cudaStream_t stream);
 
 /* Text of a status code (static storage), the text of the last CUDA error
  * seen by this library on the calling thread, and the ABI version. */

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -99,9 +100,8 @@ def load(path: str | None = None):
     L.mla_attn_destroy.argtypes = [H]
     L.mla_attn_status.argtypes = [H, P]
     L.mla_attn_last_launches.argtypes = [H]
-    L.mla_latent_append.argtypes = [H, I, P, I, P, I, P, I, I] + [P] * 5 + [I, I, P, I, P, I, P, I, I, P]
-    L.mla_attn_paged_run.argtypes = [H, I, I, P, I, I, P, I, I, P, P, P, I, P, I, P, I, I, I, P, P, P]
-    L.mla_attn_prompt_run.argtypes = [H, I, I, P, I, I] + [P, I, I, I] * 3 + [P, I, I] + [P, I, I, I] * 2 + [P, P]
+    for fn in (L.mla_latent_append, L.mla_attn_paged_run, L.mla_attn_prompt_run):
+        fn.argtypes = [H, P, P]
     for fn in ("mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
                "mla_kv_prolog_status", "mla_kv_prolog_destroy", "mla_kv_prolog_set_path",
                "mla_kv_prolog_last_launches", "mla_kv_prolog_last_path", "mla_w8a8_quant_rows",
@@ -430,6 +430,12 @@ def mla_attn_status(h, stream=None) -> int:
     return load().mla_attn_status(h, _stream(stream))
 
 
+# mla_latent_append_args, mla_attn_paged_args, mla_attn_prompt_args: pointers, then ints
+_APPEND_ARGS = struct.Struct("@11Q11i4x")
+_PAGED_ARGS = struct.Struct("@9Q11i4x")
+_PROMPT_ARGS = struct.Struct("@8Q21i4x")
+
+
 class MLAAttention:
     """Attention on the prolog's outputs: latent cache append, paged latent
     attention, prompt attention (one library handle, one workspace).
@@ -440,14 +446,17 @@ class MLAAttention:
 
     def __init__(self, cfg: dict, max_tokens: int, num_kv_heads: int | None = None, scale: float | None = None,
                  spin_budget_ns: int = 0):
+        self.h = None
         self.cfg = cfg
         self.max_tokens = max_tokens
         self.dtype = _tdt(cfg)
         self.heads = cfg["num_heads"]
         self.kv_heads = num_kv_heads or cfg["num_heads"]
-        self.h = None
+        self.rank, self.rope, self.nope, self.vdim = (cfg[k] for k in ("kv_lora_rank", "rope_dim", "nope_dim", "v_dim"))
+        self.table_numel = cfg["max_pos"] * cfg["rope_dim"]
         self.h = mla_attn_create(cfg, max_tokens, num_kv_heads, scale, spin_budget_ns)
         self.device = torch.cuda.current_device()
+        self._lib = load()
 
     def close(self):
         if self.h is not None:
@@ -473,82 +482,88 @@ class MLAAttention:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def _rows(self, t, shape, name):
-        """Address and element strides of a tensor of the handle's dtype whose last dimension is contiguous."""
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
-            raise TypeError(f"{name} must be a tensor on CUDA device {self.device}")
-        if t.dtype is not self.dtype:
-            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        """Element strides of a tensor of the handle's dtype whose last dimension is contiguous."""
+        if t.dtype is self.dtype and t.shape == shape and t.get_device() == self.device:
+            st = t.stride()
+            if st[-1] == 1 and max(st) <= _INT_MAX:
+                return st
+        return self._rows_checked(t, shape, name)
+
+    def _rows_checked(self, t, shape, name):
+        self._on_device(t, self.dtype, name)
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        st = t.stride()
-        if st[-1] != 1 and shape[-1] > 1:
+        # (the stride of a dimension of size 1 does not matter)
+        st = tuple(x if k > 1 else shape[-1] for x, k in zip(t.stride()[:-1], shape[:-1])) + (t.stride()[-1] if shape[-1] > 1 else 1,)
+        if st[-1] != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        if max(st) > _INT_MAX:  # (the stride of a dimension of size 1 does not matter)
-            st = tuple(x if k > 1 else shape[-1] for x, k in zip(st, shape))
-            if max(st) > _INT_MAX:
-                raise ValueError(f"{name}: strides must be below 2^31 elements")
-        return t.data_ptr(), st
+        if max(st) > _INT_MAX:
+            raise ValueError(f"{name}: strides must be below 2^31 elements")
+        return st
 
-    def _flat(self, t, dtype, shape, name):
-        """Address of a contiguous tensor."""
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
+    def _on_device(self, t, dtype, name):
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
             raise TypeError(f"{name} must be a tensor on CUDA device {self.device}")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
 
-    def _cache(self, t, width, name):
-        """Address, row stride, blocks and page size of a cache [num_blocks, page_size, width]."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must have shape [num_blocks, page_size, {width}]")
-        nb, page, _ = t.shape
-        ptr, st = self._rows(t, (nb, page, width), name)
-        row = st[1] if page > 1 else st[0]
-        if nb > 1 and page > 1 and st[0] != page * row:
-            raise ValueError(f"{name}: rows must be evenly spaced")
-        # (a single row has no stride of its own)
-        return ptr, (row if nb * page > 1 else max(width, row)), nb, page
+    def _flat(self, t, dtype, numel, name):
+        """Address of a contiguous tensor of numel elements."""
+        if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == self.device:
+            return t.data_ptr()
+        self._on_device(t, dtype, name)
+        if t.numel() != numel:
+            raise ValueError(f"{name} must have {numel} elements, got shape {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
+
+    def _cache(self, t, nb, page, width, name):
+        """Row stride of a cache [num_blocks, page_size, width] with evenly spaced rows."""
+        st = self._rows(t, (nb, page, width), name)
+        if page > 1:
+            if nb > 1 and st[0] != page * st[1]:
+                raise ValueError(f"{name}: rows must be evenly spaced")
+            return st[1]
+        return st[0] if nb > 1 else width  # (a single row has no stride of its own)
 
     def alloc_latent_caches(self, num_blocks: int, page_size: int):
         """latent_cache [num_blocks, page_size, 512] and kpe_cache [num_blocks, page_size, 64]."""
-        c, dev = self.cfg, torch.device("cuda", self.device)
-        return dict(latent_cache=torch.empty(num_blocks, page_size, c["kv_lora_rank"], dtype=self.dtype, device=dev),
-                    kpe_cache=torch.empty(num_blocks, page_size, c["rope_dim"], dtype=self.dtype, device=dev))
+        dev = torch.device("cuda", self.device)
+        return dict(latent_cache=torch.empty(num_blocks, page_size, self.rank, dtype=self.dtype, device=dev),
+                    kpe_cache=torch.empty(num_blocks, page_size, self.rope, dtype=self.dtype, device=dev))
 
     def append_latent(self, compressed_kv, k_pe, positions, gamma_kv, cos, sin, slot_mapping, latent_cache, kpe_cache,
                       q_pe=None, q_pe_out=None, stream=None):
         """RMSNorm compressed_kv [T, 512] (gamma_kv None: as it is), rotate k_pe [T, 64] (cos, sin None: as it is)
         and store both at slot_mapping in the paged caches; rotate q_pe [T, H, 64] into q_pe_out (None: in place).
         Returns q_pe_out."""
+        rank, rope = self.rank, self.rope
         T = compressed_kv.shape[0]
-        f32, i32, rank, rope = torch.float32, torch.int32, self.cfg["kv_lora_rank"], self.cfg["rope_dim"]
-        ckv, ckv_st = self._rows(compressed_kv, (T, rank), "compressed_kv")
-        kp, kp_st = self._rows(k_pe, (T, rope), "k_pe")
-        lc, lc_row, nb, page = self._cache(latent_cache, rank, "latent_cache")
-        kc, kc_row, nb2, page2 = self._cache(kpe_cache, rope, "kpe_cache")
-        if nb2 != nb or page2 != page:
-            raise ValueError("latent_cache and kpe_cache must have the same blocks")
-        table = (self.cfg["max_pos"], rope)
-        qp = qo = None
-        q0 = q1 = o0 = o1 = 0
+        nb, page, _ = latent_cache.shape
+        qp = qo = q0 = q1 = o0 = o1 = 0
         if q_pe is not None:
-            if q_pe_out is None:
-                q_pe_out = q_pe
             shape = (T, self.heads, rope)
-            qp, (q0, q1, _) = self._rows(q_pe, shape, "q_pe")
-            qo, (o0, o1, _) = self._rows(q_pe_out, shape, "q_pe_out")
-        _check(load().mla_latent_append(
-            self.h, T, ckv, ckv_st[0], kp, kp_st[0], qp, q0, q1,
-            None if positions is None else self._flat(positions, i32, (T,), "positions"),
-            None if gamma_kv is None else self._flat(gamma_kv, self.dtype, (rank,), "gamma_kv"),
-            None if cos is None else self._flat(cos, f32, table, "cos"),
-            None if sin is None else self._flat(sin, f32, table, "sin"),
-            self._flat(slot_mapping, i32, (T,), "slot_mapping"), page, nb, lc, lc_row, kc, kc_row, qo, o0, o1,
-            self._stream(stream)), "mla_latent_append")
+            q0, q1, _ = self._rows(q_pe, shape, "q_pe")
+            qp = q_pe.data_ptr()
+            if q_pe_out is None:
+                q_pe_out, qo, o0, o1 = q_pe, qp, q0, q1
+            else:
+                o0, o1, _ = self._rows(q_pe_out, shape, "q_pe_out")
+                qo = q_pe_out.data_ptr()
+        f32, i32 = torch.float32, torch.int32
+        c0, _ = self._rows(compressed_kv, (T, rank), "compressed_kv")
+        k0, _ = self._rows(k_pe, (T, rope), "k_pe")
+        l0 = self._cache(latent_cache, nb, page, rank, "latent_cache")
+        p0 = self._cache(kpe_cache, nb, page, rope, "kpe_cache")
+        code = self._lib.mla_latent_append(self.h, _APPEND_ARGS.pack(
+            compressed_kv.data_ptr(), k_pe.data_ptr(), qp,
+            0 if positions is None else self._flat(positions, i32, T, "positions"),
+            0 if gamma_kv is None else self._flat(gamma_kv, self.dtype, rank, "gamma_kv"),
+            0 if cos is None else self._flat(cos, f32, self.table_numel, "cos"),
+            0 if sin is None else self._flat(sin, f32, self.table_numel, "sin"),
+            self._flat(slot_mapping, i32, T, "slot_mapping"), latent_cache.data_ptr(), kpe_cache.data_ptr(), qo,
+            T, page, nb, c0, k0, q0, q1, l0, p0, o0, o1), self._stream(stream))
+        if code:
+            _check(code, "mla_latent_append")
         return q_pe_out
 
     def run_paged(self, q_latent, q_pe, kv_lens, block_table, latent_cache, kpe_cache, out, cu_q=None, lse=None,
@@ -556,44 +571,47 @@ class MLAAttention:
         """Attention of the newest tokens over the paged latent cache: q_latent [T, H, 512], q_pe [T, H, 64],
         kv_lens [n], block_table [n, blocks], cu_q [n + 1] or None (T / n tokens each) -> out [T, H, 512] and
         lse [T, H] (float32, optional)."""
-        T, H, i32 = q_latent.shape[0], self.heads, torch.int32
-        rank, rope = self.cfg["kv_lora_rank"], self.cfg["rope_dim"]
-        ql, (ql0, ql1, _) = self._rows(q_latent, (T, H, rank), "q_latent")
-        qp, (qp0, qp1, _) = self._rows(q_pe, (T, H, rope), "q_pe")
-        lc, lc_row, nb, page = self._cache(latent_cache, rank, "latent_cache")
-        kc, kc_row, nb2, page2 = self._cache(kpe_cache, rope, "kpe_cache")
-        if nb2 != nb or page2 != page:
-            raise ValueError("latent_cache and kpe_cache must have the same blocks")
-        n = kv_lens.shape[0]
-        _check(load().mla_attn_paged_run(
-            self.h, n, T, ql, ql0, ql1, qp, qp0, qp1,
-            None if cu_q is None else self._flat(cu_q, i32, (n + 1,), "cu_q"),
-            self._flat(kv_lens, i32, (n,), "kv_lens"),
-            self._flat(block_table, i32, (n, block_table.shape[-1]), "block_table"), block_table.shape[-1],
-            lc, lc_row, kc, kc_row, page, nb, self._flat(out, self.dtype, (T, H, rank), "out"),
-            None if lse is None else self._flat(lse, torch.float32, (T, H), "lse"), self._stream(stream)),
-            "mla_attn_paged_run")
+        rank, rope, H, i32 = self.rank, self.rope, self.heads, torch.int32
+        T, n = q_latent.shape[0], kv_lens.shape[0]
+        nb, page, _ = latent_cache.shape
+        if block_table.dim() != 2:
+            raise ValueError("block_table must have shape [num_seqs, blocks]")
+        width = block_table.shape[1]
+        q0, q1, _ = self._rows(q_latent, (T, H, rank), "q_latent")
+        p0, p1, _ = self._rows(q_pe, (T, H, rope), "q_pe")
+        l0 = self._cache(latent_cache, nb, page, rank, "latent_cache")
+        k0 = self._cache(kpe_cache, nb, page, rope, "kpe_cache")
+        code = self._lib.mla_attn_paged_run(self.h, _PAGED_ARGS.pack(
+            q_latent.data_ptr(), q_pe.data_ptr(), 0 if cu_q is None else self._flat(cu_q, i32, n + 1, "cu_q"),
+            self._flat(kv_lens, i32, n, "kv_lens"), self._flat(block_table, i32, n * width, "block_table"),
+            latent_cache.data_ptr(), kpe_cache.data_ptr(), self._flat(out, self.dtype, T * H * rank, "out"),
+            0 if lse is None else self._flat(lse, torch.float32, T * H, "lse"),
+            n, T, width, page, nb, q0, q1, p0, p1, l0, k0), self._stream(stream))
+        if code:
+            _check(code, "mla_attn_paged_run")
         return out
 
     def run_prompt(self, q_nope, q_pe, k_nope, k_pe, value, out, cu_seqlens=None, causal=True, lse=None, stream=None):
         """Attention over whole prompts: q_nope [b, H, s, 128], q_pe [b, H, s, 64], k_nope and value
         [b, KH, s, 128], k_pe [b, 1, s, 64] -> out [b, H, s, 128] and lse [b, H, s] (float32, optional).
         cu_seqlens [n + 1]: packed sequences along the s tokens (b = 1)."""
-        b, H, s, d = q_nope.shape
-        c, KH = self.cfg, self.kv_heads
-        rope, vd = c["rope_dim"], c["v_dim"]
-        qn, (a0, a1, a2, _) = self._rows(q_nope, (b, self.heads, s, c["nope_dim"]), "q_nope")
-        qp, (b0, b1, b2, _) = self._rows(q_pe, (b, H, s, rope), "q_pe")
-        kn, (c0, c1, c2, _) = self._rows(k_nope, (b, KH, s, c["nope_dim"]), "k_nope")
-        kp, (d0, _, d2, _) = self._rows(k_pe, (b, 1, s, rope), "k_pe")
-        va, (e0, e1, e2, _) = self._rows(value, (b, KH, s, vd), "value")
-        ou, (f0, f1, f2, _) = self._rows(out, (b, H, s, vd), "out")
-        n = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-        _check(load().mla_attn_prompt_run(
-            self.h, b, s, None if cu_seqlens is None else self._flat(cu_seqlens, torch.int32, (n + 1,), "cu_seqlens"),
-            n, 1 if causal else 0, qn, a0, a1, a2, qp, b0, b1, b2, kn, c0, c1, c2, kp, d0, d2, va, e0, e1, e2,
-            ou, f0, f1, f2, None if lse is None else self._flat(lse, torch.float32, (b, H, s), "lse"),
-            self._stream(stream)), "mla_attn_prompt_run")
+        b, _, s, _ = q_nope.shape
+        H, KH, nope, rope, vd = self.heads, self.kv_heads, self.nope, self.rope, self.vdim
+        a0, a1, a2, _ = self._rows(q_nope, (b, H, s, nope), "q_nope")
+        b0, b1, b2, _ = self._rows(q_pe, (b, H, s, rope), "q_pe")
+        c0, c1, c2, _ = self._rows(k_nope, (b, KH, s, nope), "k_nope")
+        d0, _, d2, _ = self._rows(k_pe, (b, 1, s, rope), "k_pe")
+        e0, e1, e2, _ = self._rows(value, (b, KH, s, vd), "value")
+        f0, f1, f2, _ = self._rows(out, (b, H, s, vd), "out")
+        n = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+        code = self._lib.mla_attn_prompt_run(self.h, _PROMPT_ARGS.pack(
+            q_nope.data_ptr(), q_pe.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), value.data_ptr(), out.data_ptr(),
+            0 if lse is None else self._flat(lse, torch.float32, b * H * s, "lse"),
+            0 if cu_seqlens is None else self._flat(cu_seqlens, torch.int32, n + 1, "cu_seqlens"),
+            b, s, n, 1 if causal else 0, a0, a1, a2, b0, b1, b2, c0, c1, c2, d0, d2, e0, e1, e2, f0, f1, f2),
+            self._stream(stream))
+        if code:
+            _check(code, "mla_attn_prompt_run")
         return out
 
 

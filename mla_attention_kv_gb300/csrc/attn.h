@@ -55,6 +55,7 @@ struct PagedParams {
 };
 // mma.sync kernel: items of 16 or 32 query rows.
 constexpr int kPagedMmaRows = 32;
+cudaError_t paged_mma_prepare(bool bf16);  // kernel attributes, once per device
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
 // tcgen05 kernel: items of 128 query rows, two CTAs per worker; pages whose
 // size is a multiple of 8.
@@ -74,6 +75,7 @@ inline int paged_tc_box(int page) {
   const int b = page & -page;
   return b > 64 ? 64 : b;
 }
+cudaError_t paged_tc_prepare(bool bf16);
 cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream);
 // Joins the partial results of items split over workers.
 cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
@@ -102,6 +104,7 @@ struct PromptMaps {
   bool valid;
   CUtensorMap map[3];  // k_nope, k_pe, value
 };
+cudaError_t prompt_tc_prepare(bool bf16);
 cudaError_t prompt_tc_launch(bool bf16, const PromptParams& p, PromptMaps* maps, cudaStream_t stream);
 
 }  // namespace mla

@@ -108,6 +108,16 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   h->status = reinterpret_cast<unsigned*>(base);
   h->part_ml = reinterpret_cast<float*>(base + ml_off);
   h->part_o = reinterpret_cast<float*>(base + o_off);
+  // (shared memory beyond the default is asked for once, not per call)
+  const bool bf16 = c.dtype == MLA_BF16;
+  e = paged_mma_prepare(bf16);
+  if (e == cudaSuccess) e = paged_tc_prepare(bf16);
+  if (e == cudaSuccess) e = prompt_tc_prepare(bf16);
+  if (e != cudaSuccess) {
+    cudaFree(h->ws);
+    delete h;
+    return fail(e, "kernel attributes");
+  }
   *out = h;
   return MLA_OK;
 }
@@ -141,85 +151,80 @@ mla_status mla_attn_status(mla_attn* h, cudaStream_t stream) {
 
 int mla_attn_last_launches(mla_attn* h) { return h ? h->last_launches : -1; }
 
-mla_status mla_latent_append(mla_attn* h, int T, const void* compressed_kv, int ckv_stride, const void* k_pe,
-                             int k_pe_stride, const void* q_pe, int q_pe_token_stride, int q_pe_head_stride,
-                             const int32_t* positions, const void* gamma_kv, const float* cos_table,
-                             const float* sin_table, const int32_t* slot_mapping, int page_size, int num_blocks,
-                             void* latent_cache, int latent_row_stride, void* kpe_cache, int kpe_row_stride,
-                             void* q_pe_out, int q_pe_out_token_stride, int q_pe_out_head_stride,
-                             cudaStream_t stream) {
-  if (!h || T < 0 || page_size <= 0 || num_blocks <= 0 || (long long)page_size * num_blocks > 0x7fffffffLL)
+mla_status mla_latent_append(mla_attn* h, const mla_latent_append_args* args, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_latent_append_args& a = *args;
+  if (a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
     return MLA_ERR_INVALID_ARG;
   h->last_launches = 0;
-  if (T == 0) return MLA_OK;
-  if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  if (a.T == 0) return MLA_OK;
+  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
   const int H = h->cfg.num_heads;
-  if (!compressed_kv || !k_pe || !slot_mapping || !latent_cache || !kpe_cache || (!cos_table != !sin_table) ||
-      (cos_table && !positions) || (q_pe && (!cos_table || !q_pe_out)))
+  if (!a.compressed_kv || !a.k_pe || !a.slot_mapping || !a.latent_cache || !a.kpe_cache ||
+      (!a.cos_table != !a.sin_table) || (a.cos_table && !a.positions) || (a.q_pe && (!a.cos_table || !a.q_pe_out)))
     return MLA_ERR_INVALID_ARG;
-  if (!stride_ok(ckv_stride, kRank, T > 1) || !stride_ok(k_pe_stride, kRope, T > 1) ||
-      !stride_ok(latent_row_stride, kRank, true) || !stride_ok(kpe_row_stride, kRope, true))
+  if (!stride_ok(a.compressed_kv_stride, kRank, a.T > 1) || !stride_ok(a.k_pe_stride, kRope, a.T > 1) ||
+      !stride_ok(a.latent_row_stride, kRank, true) || !stride_ok(a.kpe_row_stride, kRope, true))
     return MLA_ERR_INVALID_ARG;
-  if (q_pe && (!stride_ok(q_pe_token_stride, kRope, T > 1) || !stride_ok(q_pe_head_stride, kRope, H > 1) ||
-               !stride_ok(q_pe_out_token_stride, kRope, T > 1) || !stride_ok(q_pe_out_head_stride, kRope, H > 1)))
+  if (a.q_pe && (!stride_ok(a.q_pe_token_stride, kRope, a.T > 1) || !stride_ok(a.q_pe_head_stride, kRope, H > 1) ||
+                 !stride_ok(a.q_pe_out_token_stride, kRope, a.T > 1) || !stride_ok(a.q_pe_out_head_stride, kRope, H > 1)))
     return MLA_ERR_INVALID_ARG;
-  if (q_pe == q_pe_out && q_pe &&
-      (q_pe_token_stride != q_pe_out_token_stride || q_pe_head_stride != q_pe_out_head_stride))
+  if (a.q_pe && a.q_pe == a.q_pe_out &&
+      ((a.T > 1 && a.q_pe_token_stride != a.q_pe_out_token_stride) || (H > 1 && a.q_pe_head_stride != a.q_pe_out_head_stride)))
     return MLA_ERR_INVALID_ARG;
-  const void* ptrs[] = {compressed_kv, k_pe, slot_mapping, latent_cache, kpe_cache, gamma_kv, cos_table, sin_table,
-                        positions, q_pe, q_pe ? q_pe_out : nullptr};
+  const void* ptrs[] = {a.compressed_kv, a.k_pe, a.slot_mapping, a.latent_cache, a.kpe_cache, a.gamma_kv, a.cos_table,
+                        a.sin_table, a.positions, a.q_pe, a.q_pe ? a.q_pe_out : nullptr};
   for (const void* q : ptrs)
     if (!aligned16(q)) return MLA_ERR_MISALIGNED;
   DeviceGuard g(h->device);
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
   AppendParams p = {};
-  p.ckv = compressed_kv; p.kpe = k_pe; p.qpe = q_pe; p.positions = positions; p.gamma = gamma_kv;
-  p.cos_t = cos_table; p.sin_t = sin_table; p.slots = slot_mapping; p.latent_cache = latent_cache;
-  p.kpe_cache = kpe_cache; p.qpe_out = q_pe_out; p.status = h->status; p.ckv_stride = ckv_stride;
-  p.kpe_stride = k_pe_stride; p.q_ts = q_pe_token_stride; p.q_hs = q_pe_head_stride; p.lat_rs = latent_row_stride;
-  p.kpe_rs = kpe_row_stride; p.qo_ts = q_pe_out_token_stride; p.qo_hs = q_pe_out_head_stride; p.T = T; p.heads = H;
-  p.nslots = page_size * num_blocks; p.max_pos = h->cfg.max_pos; p.eps = h->cfg.eps;
+  p.ckv = a.compressed_kv; p.kpe = a.k_pe; p.qpe = a.q_pe; p.positions = a.positions; p.gamma = a.gamma_kv;
+  p.cos_t = a.cos_table; p.sin_t = a.sin_table; p.slots = a.slot_mapping; p.latent_cache = a.latent_cache;
+  p.kpe_cache = a.kpe_cache; p.qpe_out = a.q_pe_out; p.status = h->status; p.ckv_stride = a.compressed_kv_stride;
+  p.kpe_stride = a.k_pe_stride; p.q_ts = a.q_pe_token_stride; p.q_hs = a.q_pe_head_stride; p.lat_rs = a.latent_row_stride;
+  p.kpe_rs = a.kpe_row_stride; p.qo_ts = a.q_pe_out_token_stride; p.qo_hs = a.q_pe_out_head_stride; p.T = a.T; p.heads = H;
+  p.nslots = a.page_size * a.num_blocks; p.max_pos = h->cfg.max_pos; p.eps = h->cfg.eps;
   cudaError_t e = append_launch(h->cfg.dtype == MLA_BF16, p, stream);
   if (e != cudaSuccess) return fail(e, "append launch");
   h->last_launches = 1;
   return MLA_OK;
 }
 
-mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_latent, int q_latent_token_stride,
-                              int q_latent_head_stride, const void* q_pe, int q_pe_token_stride,
-                              int q_pe_head_stride, const int32_t* cu_q, const int32_t* kv_lens,
-                              const int32_t* block_table, int table_stride, const void* latent_cache,
-                              int latent_row_stride, const void* kpe_cache, int kpe_row_stride, int page_size,
-                              int num_blocks, void* out, float* lse, cudaStream_t stream) {
-  if (!h || num_seqs < 0 || T < 0 || page_size <= 0 || num_blocks <= 0 || table_stride < 0 ||
-      (long long)page_size * num_blocks > 0x7fffffffLL)
+mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_attn_paged_args& a = *args;
+  if (a.num_seqs < 0 || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
+      (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
     return MLA_ERR_INVALID_ARG;
   h->last_launches = 0;
-  if (num_seqs == 0 || T == 0) return MLA_OK;
-  if (!cu_q && T % num_seqs != 0) return MLA_ERR_INVALID_ARG;
-  if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  if (a.num_seqs == 0 || a.T == 0) return MLA_OK;
+  if (!a.cu_q && a.T % a.num_seqs != 0) return MLA_ERR_INVALID_ARG;
+  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
   const int H = h->cfg.num_heads;
-  if (!q_latent || !q_pe || !kv_lens || !block_table || !latent_cache || !kpe_cache || !out) return MLA_ERR_INVALID_ARG;
-  if (!stride_ok(q_latent_token_stride, kRank, T > 1) || !stride_ok(q_latent_head_stride, kRank, H > 1) ||
-      !stride_ok(q_pe_token_stride, kRope, T > 1) || !stride_ok(q_pe_head_stride, kRope, H > 1) ||
-      !stride_ok(latent_row_stride, kRank, true) || !stride_ok(kpe_row_stride, kRope, true))
+  if (!a.q_latent || !a.q_pe || !a.kv_lens || !a.block_table || !a.latent_cache || !a.kpe_cache || !a.out)
     return MLA_ERR_INVALID_ARG;
-  const void* ptrs[] = {q_latent, q_pe, cu_q, kv_lens, block_table, latent_cache, kpe_cache, out, lse};
+  if (!stride_ok(a.q_latent_token_stride, kRank, a.T > 1) || !stride_ok(a.q_latent_head_stride, kRank, H > 1) ||
+      !stride_ok(a.q_pe_token_stride, kRope, a.T > 1) || !stride_ok(a.q_pe_head_stride, kRope, H > 1) ||
+      !stride_ok(a.latent_row_stride, kRank, true) || !stride_ok(a.kpe_row_stride, kRope, true))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.q_latent, a.q_pe, a.cu_q, a.kv_lens, a.block_table, a.latent_cache, a.kpe_cache, a.out, a.lse};
   for (const void* q : ptrs)
     if (!aligned16(q)) return MLA_ERR_MISALIGNED;
   DeviceGuard g(h->device);
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
   const bool bf16 = h->cfg.dtype == MLA_BF16;
   PagedParams p = {};
-  p.q_lat = q_latent; p.q_pe = q_pe; p.cu_q = cu_q; p.kv_lens = kv_lens; p.table = block_table; p.latent = latent_cache;
-  p.kpe = kpe_cache; p.out = out; p.lse = lse; p.part_o = h->part_o; p.part_ml = h->part_ml; p.status = h->status;
-  p.ql_ts = q_latent_token_stride; p.ql_hs = q_latent_head_stride; p.qp_ts = q_pe_token_stride;
-  p.qp_hs = q_pe_head_stride; p.table_stride = table_stride; p.lat_rs = latent_row_stride; p.kpe_rs = kpe_row_stride;
-  p.page = page_size; p.nblocks = num_blocks; p.nseq = num_seqs; p.T = T; p.heads = H;
-  p.n_uniform = cu_q ? 0 : T / num_seqs; p.workers = h->num_sms; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
+  p.q_lat = a.q_latent; p.q_pe = a.q_pe; p.cu_q = a.cu_q; p.kv_lens = a.kv_lens; p.table = a.block_table;
+  p.latent = a.latent_cache; p.kpe = a.kpe_cache; p.out = a.out; p.lse = a.lse; p.part_o = h->part_o;
+  p.part_ml = h->part_ml; p.status = h->status; p.ql_ts = a.q_latent_token_stride; p.ql_hs = a.q_latent_head_stride;
+  p.qp_ts = a.q_pe_token_stride; p.qp_hs = a.q_pe_head_stride; p.table_stride = a.table_stride;
+  p.lat_rs = a.latent_row_stride; p.kpe_rs = a.kpe_row_stride; p.page = a.page_size; p.nblocks = a.num_blocks;
+  p.nseq = a.num_seqs; p.T = a.T; p.heads = H; p.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs; p.workers = h->num_sms;
+  p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   // (with ragged chunks the host knows only the average)
-  const long long rows_per_seq = (long long)(T / num_seqs > 0 ? T / num_seqs : 1) * H;
-  const bool tc = rows_per_seq > kPagedMmaRows && paged_tc_box(page_size) >= 8;
+  const long long rows_per_seq = (long long)(a.T / a.num_seqs > 0 ? a.T / a.num_seqs : 1) * H;
+  const bool tc = rows_per_seq > kPagedMmaRows && paged_tc_box(a.page_size) >= 8;
   const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
   if (tc) p.workers = h->num_sms / 2;
   cudaError_t e = tc ? paged_tc_launch(bf16, p, &h->paged_maps, stream) : paged_mma_launch(bf16, p, rows, stream);
@@ -230,46 +235,40 @@ mla_status mla_attn_paged_run(mla_attn* h, int num_seqs, int T, const void* q_la
   return MLA_OK;
 }
 
-mla_status mla_attn_prompt_run(mla_attn* h, int b, int s, const int32_t* cu_seqlens, int num_seqs, int causal,
-                               const void* q_nope, int q_nope_batch_stride, int q_nope_head_stride,
-                               int q_nope_token_stride, const void* q_pe, int q_pe_batch_stride,
-                               int q_pe_head_stride, int q_pe_token_stride, const void* k_nope,
-                               int k_nope_batch_stride, int k_nope_head_stride, int k_nope_token_stride,
-                               const void* k_pe, int k_pe_batch_stride, int k_pe_token_stride, const void* value,
-                               int value_batch_stride, int value_head_stride, int value_token_stride, void* out,
-                               int out_batch_stride, int out_head_stride, int out_token_stride, float* lse,
-                               cudaStream_t stream) {
-  if (!h || b < 0 || s < 0 || (causal != 0 && causal != 1) || (cu_seqlens && (num_seqs < 0 || b > 1)))
+mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_attn_prompt_args& a = *args;
+  if (a.b < 0 || a.s < 0 || (a.causal != 0 && a.causal != 1) || (a.cu_seqlens && (a.num_seqs < 0 || a.b > 1)))
     return MLA_ERR_INVALID_ARG;
   h->last_launches = 0;
-  const long long T = (long long)b * s;
-  if (T == 0 || (cu_seqlens && num_seqs == 0)) return MLA_OK;
+  const long long T = (long long)a.b * a.s;
+  if (T == 0 || (a.cu_seqlens && a.num_seqs == 0)) return MLA_OK;
   if (T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
-  if (!q_nope || !q_pe || !k_nope || !k_pe || !value || !out) return MLA_ERR_INVALID_ARG;
+  if (!a.q_nope || !a.q_pe || !a.k_nope || !a.k_pe || !a.value || !a.out) return MLA_ERR_INVALID_ARG;
   const int H = h->cfg.num_heads, KH = h->cfg.num_kv_heads;
   PromptParams p = {};
-  p.q_nope = {q_nope, q_nope_batch_stride, q_nope_head_stride, q_nope_token_stride};
-  p.q_pe = {q_pe, q_pe_batch_stride, q_pe_head_stride, q_pe_token_stride};
-  p.k_nope = {k_nope, k_nope_batch_stride, k_nope_head_stride, k_nope_token_stride};
-  p.k_pe = {k_pe, k_pe_batch_stride, 0, k_pe_token_stride};
-  p.value = {value, value_batch_stride, value_head_stride, value_token_stride};
-  p.out = {out, out_batch_stride, out_head_stride, out_token_stride};
+  p.q_nope = {a.q_nope, a.q_nope_batch_stride, a.q_nope_head_stride, a.q_nope_token_stride};
+  p.q_pe = {a.q_pe, a.q_pe_batch_stride, a.q_pe_head_stride, a.q_pe_token_stride};
+  p.k_nope = {a.k_nope, a.k_nope_batch_stride, a.k_nope_head_stride, a.k_nope_token_stride};
+  p.k_pe = {a.k_pe, a.k_pe_batch_stride, 0, a.k_pe_token_stride};
+  p.value = {a.value, a.value_batch_stride, a.value_head_stride, a.value_token_stride};
+  p.out = {a.out, a.out_batch_stride, a.out_head_stride, a.out_token_stride};
   const struct { PromptTensor* t; int width, heads; } all[] = {
       {&p.q_nope, kNope, H}, {&p.q_pe, kRope, H}, {&p.k_nope, kNope, KH}, {&p.k_pe, kRope, 1}, {&p.value, kV, KH}, {&p.out, kV, H}};
   for (const auto& x : all)
-    if (!stride_ok(x.t->sb, x.width, b > 1) || !stride_ok(x.t->sh, x.width, x.heads > 1) || !stride_ok(x.t->st, x.width, s > 1))
+    if (!stride_ok(x.t->sb, x.width, a.b > 1) || !stride_ok(x.t->sh, x.width, x.heads > 1) || !stride_ok(x.t->st, x.width, a.s > 1))
       return MLA_ERR_INVALID_ARG;
   for (const auto& x : all) {
     if (!aligned16(x.t->ptr)) return MLA_ERR_MISALIGNED;
-    if (b == 1) x.t->sb = x.width;
+    if (a.b == 1) x.t->sb = x.width;
     if (x.heads == 1) x.t->sh = x.width;
-    if (s == 1) x.t->st = x.width;
+    if (a.s == 1) x.t->st = x.width;
   }
-  if (!aligned16(cu_seqlens) || !aligned16(lse)) return MLA_ERR_MISALIGNED;
+  if (!aligned16(a.cu_seqlens) || !aligned16(a.lse)) return MLA_ERR_MISALIGNED;
   DeviceGuard g(h->device);
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
-  p.lse = lse; p.cu = cu_seqlens; p.status = h->status; p.b = b; p.s = s; p.nseq = cu_seqlens ? num_seqs : b;
-  p.heads = H; p.kv_heads = KH; p.causal = causal; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
+  p.lse = a.lse; p.cu = a.cu_seqlens; p.status = h->status; p.b = a.b; p.s = a.s; p.nseq = a.cu_seqlens ? a.num_seqs : a.b;
+  p.heads = H; p.kv_heads = KH; p.causal = a.causal; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   cudaError_t e = prompt_tc_launch(h->cfg.dtype == MLA_BF16, p, &h->prompt_maps, stream);
   if (e != cudaSuccess) return fail(e, "prompt attention launch");
   h->last_launches = 1;

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.heads;
 
+  grid_dep_launch_dependents();  // (the joining kernel may take its place and plan)
   const long long total = plan_total(p, plan, R, blockIdx.x == 0);
   if (total == 0) return;
   const int W = plan_workers(total, p.workers);
@@ -302,7 +303,10 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p,
   using E = Elem<T>;
   __shared__ PlanShared plan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the lengths were complete before the kernel that makes the pieces began; every block waits for the pieces, so
+  // that this kernel never ends before that one
   const long long total = plan_total(p, &plan, R, false);
+  grid_dep_wait();
   if (total == 0) return;
   const int W = plan_workers(total, p.workers);
   const int v = blockIdx.x + 1;
@@ -351,15 +355,22 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p,
 }
 
 template <typename T, int MT>
+cudaError_t prepare_mma() {
+  return cudaFuncSetAttribute(paged_mma_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PmSmem<MT>::kBytes);
+}
+template <typename T, int MT>
 cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PmSmem<MT>::kBytes);
-  if (e != cudaSuccess) return e;
   paged_mma_kernel<T, MT><<<p.workers, kPmThreads, PmSmem<MT>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t paged_mma_prepare(bool bf16) {
+  const cudaError_t e = bf16 ? prepare_mma<__nv_bfloat16, 1>() : prepare_mma<__half, 1>();
+  if (e != cudaSuccess) return e;
+  return bf16 ? prepare_mma<__nv_bfloat16, 2>() : prepare_mma<__half, 2>();
+}
 
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream) {
   if (rows == 16)
@@ -369,12 +380,18 @@ cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStre
 
 cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
-  const dim3 grid(p.workers - 1, (rows + 7) / 8);
-  if (bf16)
-    paged_combine_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p, rows);
-  else
-    paged_combine_kernel<__half><<<grid, 256, 0, stream>>>(p, rows);
-  return cudaGetLastError();
+  // launched while the kernel before it runs (it waits for that one's end before it reads the pieces)
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(p.workers - 1, (rows + 7) / 8);
+  c.blockDim = dim3(256);
+  c.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&c, paged_combine_kernel<__nv_bfloat16>, p, rows)
+              : cudaLaunchKernelEx(&c, paged_combine_kernel<__half>, p, rows);
 }
 
 }  // namespace mla

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
   const int half = blockIdx.x & 1, w = blockIdx.x >> 1;
 
   PlanShared* plan = reinterpret_cast<PlanShared*>(smem + kUtN);
+  grid_dep_launch_dependents();  // (the joining kernel may take its place and plan)
   const long long total = plan_total(p, plan, kUtRows, blockIdx.x == 0);
   if (total == 0) return;
   const int W = plan_workers(total, p.workers);
@@ -460,13 +461,16 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   }
   UtArgs a;
   a.lat = m->lat; a.kpe = m->kpe; a.p = p; a.box = box;
-  cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
-  if (e != cudaSuccess) return e;
   paged_tc_kernel<T><<<p.workers * 2, kUtThreads, kUtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t paged_tc_prepare(bool bf16) {
+  return bf16 ? cudaFuncSetAttribute(paged_tc_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem)
+              : cudaFuncSetAttribute(paged_tc_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
+}
 
 cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream) {
   return bf16 ? launch<__nv_bfloat16>(p, maps, stream) : launch<__half>(p, maps, stream);

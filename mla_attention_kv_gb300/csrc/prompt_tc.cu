@@ -404,13 +404,16 @@ cudaError_t launch(const PromptParams& p, PromptMaps* m, cudaStream_t stream) {
   PtArgs a;
   a.kn = m->map[0]; a.kp = m->map[1]; a.v = m->map[2];
   a.p = p;
-  cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem);
-  if (e != cudaSuccess) return e;
   prompt_tc_kernel<T><<<dim3(2 * prompt_blocks(p, kPtRows), p.heads), kPtThreads, kPtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t prompt_tc_prepare(bool bf16) {
+  return bf16 ? cudaFuncSetAttribute(prompt_tc_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem)
+              : cudaFuncSetAttribute(prompt_tc_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem);
+}
 
 cudaError_t prompt_tc_launch(bool bf16, const PromptParams& p, PromptMaps* maps, cudaStream_t stream) {
   return bf16 ? launch<__nv_bfloat16>(p, maps, stream) : launch<__half>(p, maps, stream);

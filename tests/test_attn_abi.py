@@ -50,9 +50,10 @@ def test_null_handles(L):
     assert L.mla_attn_destroy(None) == 1
     assert L.mla_attn_status(None, None) == 1
     assert L.mla_attn_last_launches(None) == -1
-    assert L.mla_latent_append(None, *APPEND.values()) == 1
-    assert L.mla_attn_paged_run(None, *PAGED.values()) == 1
-    assert L.mla_attn_prompt_run(None, *PROMPT.values()) == 1
+    h = FakeHandle()
+    for fn, base in ((L.mla_latent_append, APPEND), (L.mla_attn_paged_run, PAGED), (L.mla_attn_prompt_run, PROMPT)):
+        assert fn(None, packed(fn, base), None) == 1
+        assert fn(h.ptr, None, None) == 1
 
 
 _at = [0x100000]
@@ -63,14 +64,23 @@ def fake():
     return P(_at[0])
 
 
-APPEND = dict(T=2, ckv=fake(), ckv_s=576, kpe=fake(), kpe_s=576, q=fake(), q_t=16 * 192, q_h=192, pos=fake(), gamma=fake(),
-              cos=fake(), sin=fake(), slots=fake(), page=16, nb=4, lat=fake(), lat_s=512, kc=fake(), kc_s=64, qo=fake(),
-              qo_t=1024, qo_h=64, stream=None)
-PAGED = dict(n=2, T=2, ql=fake(), ql_t=8192, ql_h=512, qp=fake(), qp_t=1024, qp_h=64, cu=None, lens=fake(), table=fake(),
-             ts=4, lat=fake(), lat_s=512, kc=fake(), kc_s=64, page=16, nb=8, out=fake(), lse=fake(), stream=None)
-PROMPT = dict(b=1, s=4, cu=None, n=0, causal=1, qn=fake(), qn_b=8192, qn_h=512, qn_t=128, qp=fake(), qp_b=4096, qp_h=256,
-              qp_t=64, kn=fake(), kn_b=8192, kn_h=512, kn_t=128, kp=fake(), kp_b=256, kp_t=64, v=fake(), v_b=8192, v_h=512,
-              v_t=128, o=fake(), o_b=8192, o_h=512, o_t=128, lse=fake(), stream=None)
+# in the order of the structs' fields
+APPEND = dict(ckv=fake(), kpe=fake(), q=fake(), pos=fake(), gamma=fake(), cos=fake(), sin=fake(), slots=fake(), lat=fake(),
+              kc=fake(), qo=fake(), T=2, page=16, nb=4, ckv_s=576, kpe_s=576, q_t=16 * 192, q_h=192, lat_s=512, kc_s=64,
+              qo_t=1024, qo_h=64)
+PAGED = dict(ql=fake(), qp=fake(), cu=None, lens=fake(), table=fake(), lat=fake(), kc=fake(), out=fake(), lse=fake(), n=2, T=2,
+             ts=4, page=16, nb=8, ql_t=8192, ql_h=512, qp_t=1024, qp_h=64, lat_s=512, kc_s=64)
+PROMPT = dict(qn=fake(), qp=fake(), kn=fake(), kp=fake(), v=fake(), o=fake(), lse=fake(), cu=None, b=1, s=4, n=0, causal=1,
+              qn_b=8192, qn_h=512, qn_t=128, qp_b=4096, qp_h=256, qp_t=64, kn_b=8192, kn_h=512, kn_t=128, kp_b=256, kp_t=64,
+              v_b=8192, v_h=512, v_t=128, o_b=8192, o_h=512, o_t=128)
+STRUCTS = dict(mla_latent_append_args=B._APPEND_ARGS, mla_attn_paged_args=B._PAGED_ARGS, mla_attn_prompt_args=B._PROMPT_ARGS)
+
+
+def packed(fn, base, **over):
+    args = dict(base)
+    args.update(over)
+    st = {"mla_latent_append": B._APPEND_ARGS, "mla_attn_paged_run": B._PAGED_ARGS, "mla_attn_prompt_run": B._PROMPT_ARGS}[fn.__name__]
+    return st.pack(*[(x.value if isinstance(x, P) else 0 if x is None else x) for x in args.values()])
 
 
 class FakeHandle:
@@ -86,10 +96,8 @@ class FakeHandle:
 
 
 def refuse(fn, base, code, **over):
-    args = dict(base)
-    args.update(over)
     h = FakeHandle()
-    assert fn(h.ptr, *args.values()) == code, over
+    assert fn(h.ptr, packed(fn, base, **over), None) == code, over
 
 
 @pytest.mark.parametrize("over,code", [
@@ -156,6 +164,7 @@ def test_binding_rejects_host_tensors():
     a = B.MLAAttention.__new__(B.MLAAttention)
     a.cfg = dict(kv_lora_rank=512, rope_dim=64, nope_dim=128, v_dim=128, num_heads=4, max_pos=8)
     a.h, a.device, a.dtype, a.heads, a.kv_heads = None, 0, torch.float16, 4, 4
+    a.rank, a.rope, a.nope, a.vdim, a.table_numel = 512, 64, 128, 128, 512
     x = torch.zeros(2, 576, dtype=torch.float16)
     i = torch.zeros(2, dtype=torch.int32)
     c = torch.zeros(2, 4, 512, dtype=torch.float16)
@@ -165,3 +174,30 @@ def test_binding_rejects_host_tensors():
         a.run_paged(c, c[..., :64], i, i[None], c, c[..., :64], c)
     with pytest.raises(TypeError):
         a.run_prompt(c[None, ..., :128], c[None, ..., :64], c[None, ..., :128], c[None, :, :1, :64], c[None, ..., :128], c[None])
+
+
+@pytest.mark.parametrize("name", list(STRUCTS))
+def test_argument_structs_match_the_header(name, tmp_path):
+    """The binding packs pointers, then ints, in the header's order, to the C compiler's size."""
+    src = open(os.path.join(ROOT, "include", "mla_prolog.h")).read()
+    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), src, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    kinds = []
+    for line in body.split(";"):
+        line = line.strip()
+        if not line:
+            continue
+        kinds += ["Q"] if "*" in line else ["i"] * (line.count(",") + 1)
+    assert kinds == sorted(kinds), "pointers come first"
+    assert STRUCTS[name].format == "@%dQ%di4x" % (kinds.count("Q"), kinds.count("i"))
+    base = dict(mla_latent_append_args=APPEND, mla_attn_paged_args=PAGED, mla_attn_prompt_args=PROMPT)[name]
+    assert len(base) == len(kinds)
+    gcc = shutil.which("gcc")
+    if gcc is None or not os.path.isdir("/usr/local/cuda/include"):
+        pytest.skip("gcc or the CUDA headers are missing")
+    prog = tmp_path / "size.c"
+    prog.write_text('#include <stdio.h>\n#include "mla_prolog.h"\nint main(void) { printf("%%zu\\n", sizeof(%s)); return 0; }\n' % name)
+    exe = tmp_path / "size"
+    subprocess.run([gcc, str(prog), "-I", os.path.join(ROOT, "include"), "-I", "/usr/local/cuda/include", "-o", str(exe)],
+                   check=True, capture_output=True)
+    assert int(subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout) == STRUCTS[name].size
