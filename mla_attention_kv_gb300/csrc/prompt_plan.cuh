@@ -1,19 +1,27 @@
-// prompt_plan.cuh -- which query block of which sequence a CTA of the prompt
-// attention works on.
+// prompt_plan.cuh -- which query block of which sequence and head a cluster
+// of the prompt attention works on.
+//
+// Items are (head, block of query rows of a sequence), head after head, so
+// that the clusters at work share few heads' keys in L2; the blocks of a
+// sequence are taken from its end, where a causal block has the most keys.
+// Cluster c of C takes items c, 2C - 1 - c, 2C + c, 4C - 1 - c, ...: the
+// direction alternates so that no cluster always gets the longer blocks.
 #pragma once
 #include "attn.h"
 #include "common.cuh"
 
 namespace mla {
 
+constexpr int kPromptPlanThreads = 320;
+
 struct PromptPlace {
   int batch, begin, len, row0;  // sequence: rows begin .. begin + len of `batch`; first query row in it
+  int head;
 };
 
-struct PromptPlanShared {
+struct PromptPlan {
+  int base[kPromptPlanThreads + 1];  // packed: blocks before each thread's strip of sequences
   int warp_sum[32];
-  PromptPlace place;
-  int found;
 };
 
 // Length of packed sequence i, clamped to the s rows there are.
@@ -27,21 +35,11 @@ __device__ __forceinline__ int prompt_seq(const PromptParams& p, int i, int* beg
   return b - a;
 }
 
-// Query block `index` (of `rows` rows) of the call; false past the last
-// one.  Blocks of one sequence are taken from its end: causal blocks late in
-// a sequence have the most keys and start first.  All threads of the block.
-__device__ __forceinline__ bool prompt_place(const PromptParams& p, PromptPlanShared* ps, int index, int rows,
-                                             PromptPlace* out, bool report) {
-  if (!p.cu) {
-    const int per = (p.s + rows - 1) / rows;
-    if (index >= per * p.b) return false;
-    out->batch = index % p.b;
-    out->begin = 0;
-    out->len = p.s;
-    out->row0 = (per - 1 - index / p.b) * rows;
-    return true;
-  }
-  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Number of query blocks (of `rows` rows) per head; all threads of a block
+// of kPromptPlanThreads.
+__device__ __forceinline__ int prompt_plan(const PromptParams& p, PromptPlan* ps, int rows, bool report) {
+  if (!p.cu) return (p.s + rows - 1) / rows * p.b;
+  const int nt = kPromptPlanThreads, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int strip = (p.nseq + nt - 1) / nt;
   int mine = 0, begin;
   for (int i = 0; i < strip; ++i)
@@ -53,29 +51,52 @@ __device__ __forceinline__ bool prompt_place(const PromptParams& p, PromptPlanSh
     if (lane >= d) inc += o;
   }
   if (lane == 31) ps->warp_sum[warp] = inc;
-  if (tid == 0) ps->found = 0;
   __syncthreads();
   int before = inc - mine;
   for (int w = 0; w < warp; ++w) before += ps->warp_sum[w];
-  if (index >= before && index < before + mine) {
-    int left = index - before;
-    for (int i = 0; i < strip; ++i) {
-      const int len = prompt_seq(p, tid * strip + i, &begin, false);
-      const int nb = (len + rows - 1) / rows;
-      if (left < nb) {
-        ps->place = PromptPlace{0, begin, len, (nb - 1 - left) * rows};
-        ps->found = 1;
-        break;
-      }
-      left -= nb;
-    }
-  }
+  ps->base[tid] = before;
+  if (tid == nt - 1) ps->base[nt] = before + mine;
   __syncthreads();
-  *out = ps->place;
-  return ps->found != 0;
+  return ps->base[nt];
 }
 
-// Upper bound of the number of query blocks, known on the host.
+// Item of cluster c of C in its k-th round.
+__device__ __forceinline__ long long prompt_item(int c, int C, int k) {
+  return (long long)k * C + ((k & 1) ? C - 1 - c : c);
+}
+
+// Place of item x (of blocks * heads); any thread by itself.
+__device__ __forceinline__ PromptPlace prompt_place(const PromptParams& p, const PromptPlan* ps, long long x, int blocks, int rows) {
+  PromptPlace r;
+  r.head = (int)(x / blocks);
+  int i = (int)(x - (long long)r.head * blocks);
+  if (!p.cu) {
+    const int per = (p.s + rows - 1) / rows;
+    r.batch = i / per;
+    r.begin = 0;
+    r.len = p.s;
+    r.row0 = (per - 1 - (i - r.batch * per)) * rows;
+    return r;
+  }
+  int a = 0, b = kPromptPlanThreads;  // last strip with base <= i
+  while (b - a > 1) {
+    const int m = (a + b) / 2;
+    if (ps->base[m] <= i) a = m; else b = m;
+  }
+  i -= ps->base[a];
+  r.batch = 0;
+  for (int s = a * ((p.nseq + kPromptPlanThreads - 1) / kPromptPlanThreads);; ++s) {
+    r.len = prompt_seq(p, s, &r.begin, false);
+    const int nb = (r.len + rows - 1) / rows;
+    if (i < nb) {
+      r.row0 = (nb - 1 - i) * rows;
+      return r;
+    }
+    i -= nb;
+  }
+}
+
+// Upper bound of the number of query blocks per head, known on the host.
 inline int prompt_blocks(const PromptParams& p, int rows) {
   return p.cu ? p.s / rows + (p.nseq < p.s ? p.nseq : p.s) : (p.s + rows - 1) / rows * p.b;
 }

@@ -25,6 +25,8 @@
 //
 // MMA order: scores of tile i + 1, then output of tile i, so the softmax of
 // a tile runs under the scores of the next and the output of the previous.
+// The clusters are persistent: copies and scores of the next item begin while
+// the last one's result is stored.
 //
 // The output is rescaled only when a row's maximum has grown by more than 2^8
 // since the last time (weights are then at most 2^8: the sums stay exact to
@@ -46,7 +48,7 @@
 namespace mla {
 namespace {
 
-constexpr int kPtThreads = 320;
+constexpr int kPtThreads = kPromptPlanThreads;
 constexpr int kPtTile = 128;   // query rows per CTA, keys per tile
 constexpr int kPtRows = 256;   // query rows per cluster
 constexpr int kKStages = 3, kVStages = 2;
@@ -54,7 +56,7 @@ constexpr uint32_t kBlock = 16384;  // 128 keys x 64 columns
 constexpr uint32_t kKBytes = 3 * kBlock, kVBytes = 2 * kBlock;
 constexpr uint32_t kPtV = kKStages * kKBytes;
 constexpr uint32_t kPtBar = kPtV + kVStages * kVBytes;
-constexpr uint32_t kPtSmem = kPtBar + 4096 + 1024;  // + alignment slack
+constexpr uint32_t kPtSmem = kPtBar + 5120 + 1024;  // + alignment slack
 static_assert(kPtSmem <= 232448, "shared memory of one CTA");
 constexpr uint32_t kTmO = 256, kTmQ = 384;  // tensor memory columns; S0 at 0, S1 at 128
 constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that rescales the output
@@ -62,13 +64,13 @@ constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that resc
 struct PtShared {
   uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
   uint64_t sfull[2], pfull[2];
-  uint64_t qready, pvdone, done, pair[4];
-  float row[2][2][128];  // exchange between the two threads of a row: [tile parity][half][row]
-  PromptPlanShared plan;
+  uint64_t qready, ofree, pvdone, olast, done, pair[4];
+  float row[2][2][128];  // exchange between the two threads of a row: [parity of the meeting][half][row]
+  PromptPlan plan;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(PtShared) <= 4096, "barrier block");
+static_assert(sizeof(PtShared) <= 5120, "barrier block");
 
 struct PtArgs {
   CUtensorMap kn, kp, v;
@@ -89,17 +91,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   auto bar = [](uint64_t* b) { return smem_u32(b); };
   const int rank = blockIdx.x & 1;  // (clusters are pairs of neighbours along x)
 
-  PromptPlace pl;
-  if (!prompt_place(p, &sh->plan, blockIdx.x >> 1, kPtRows, &pl, blockIdx.x == 0 && blockIdx.y == 0)) return;
-  const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-  // key tiles of the two CTAs (the second may have no rows)
-  auto tiles_of = [&](int w) {
-    const int r0 = pl.row0 + w * kPtTile;
-    if (r0 >= pl.len) return 0;
-    const int end = p.causal ? min(pl.len, r0 + kPtTile) : pl.len;
-    return (end + kPtTile - 1) / kPtTile;
+  // the items of this cluster: key tiles n of this CTA's 128 rows, nt of the pair (the second CTA may have none)
+  const int blocks = prompt_plan(p, &sh->plan, kPtRows, blockIdx.x == 0);
+  const int cluster = blockIdx.x >> 1;
+  const long long items = (long long)blocks * p.heads;
+  if (cluster >= items) return;
+  struct Item {
+    PromptPlace pl;
+    int n, nt;
   };
-  const int n = uniform(tiles_of(rank)), nt = uniform(max(tiles_of(0), tiles_of(1)));
+  auto item_at = [&](long long x) {
+    Item it;
+    it.pl = prompt_place(p, &sh->plan, x, blocks, kPtRows);
+    auto tiles_of = [&](int w) {
+      const int r0 = it.pl.row0 + w * kPtTile;
+      if (r0 >= it.pl.len) return 0;
+      const int end = p.causal ? min(it.pl.len, r0 + kPtTile) : it.pl.len;
+      return (end + kPtTile - 1) / kPtTile;
+    };
+    it.n = tiles_of(rank);
+    it.nt = max(tiles_of(0), tiles_of(1));
+    return it;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -115,8 +128,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       mbar_init(bar(&sh->pfull[i]), 8);
     }
     mbar_init(bar(&sh->qready), 8);
+    mbar_init(bar(&sh->ofree), 8);
     for (int i = 0; i < 4; ++i) mbar_init(bar(&sh->pair[i]), 2);
     mbar_init(bar(&sh->pvdone), 1);
+    mbar_init(bar(&sh->olast), 1);
     mbar_init(bar(&sh->done), 1);
     sh->abort = 0;
     fence_mbar_init();
@@ -133,32 +148,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     if (tc::elect_one()) {
       int nk = 0, nv = 0;  // stages filled
       bool ok = true;
-      // this CTA's 64 rows of every block go to both CTAs
-      auto keys = [&](int i) {
-        const uint32_t s = i % kKStages, b = bar(&sh->kfull[s]), d = sbase + s * kKBytes + rank * (kBlock / 2);
-        ok = ok && at_wait(bar(&sh->kempty[s]), ((i / kKStages) & 1) ^ 1, abort, p.budget_ns, p.status);
-        if (!ok) return;
-        const int tok = pl.begin + i * kPtTile + rank * 64;
-        mbar_arrive_expect_tx(b, kKBytes);
-        tma_load_4d_multicast(d, &a.kn, 0, tok, hk, pl.batch, b, 3);
-        tma_load_4d_multicast(d + kBlock, &a.kn, 64, tok, hk, pl.batch, b, 3);
-        tma_load_4d_multicast(d + 2 * kBlock, &a.kp, 0, tok, 0, pl.batch, b, 3);
-        ++nk;
-      };
-      auto values = [&](int i) {
-        const uint32_t s = i % kVStages, b = bar(&sh->vfull[s]), d = sbase + kPtV + s * kVBytes + rank * (kBlock / 2);
-        ok = ok && at_wait(bar(&sh->vempty[s]), ((i / kVStages) & 1) ^ 1, abort, p.budget_ns, p.status);
-        if (!ok) return;
-        const int tok = pl.begin + i * kPtTile + rank * 64;
-        mbar_arrive_expect_tx(b, kVBytes);
-        tma_load_4d_multicast(d, &a.v, 0, tok, hk, pl.batch, b, 3);
-        tma_load_4d_multicast(d + kBlock, &a.v, 64, tok, hk, pl.batch, b, 3);
-        ++nv;
-      };
-      keys(0);
-      for (int i = 0; i < nt && ok; ++i) {
-        if (i + 1 < nt) keys(i + 1);
-        values(i);
+      for (int k = 0; ok; ++k) {
+        const long long x = prompt_item(cluster, p.clusters, k);
+        if (x >= items) break;
+        const Item it = item_at(x);
+        const int hk = it.pl.head / (p.heads / p.kv_heads), t0 = it.pl.begin + rank * 64;
+        // this CTA's 64 rows of every block go to both CTAs
+        auto keys = [&](int i) {
+          const uint32_t s = nk % kKStages, b = bar(&sh->kfull[s]), d = sbase + s * kKBytes + rank * (kBlock / 2);
+          ok = ok && at_wait(bar(&sh->kempty[s]), ((nk / kKStages) & 1) ^ 1, abort, p.budget_ns, p.status);
+          if (!ok) return;
+          const int tok = t0 + i * kPtTile;
+          mbar_arrive_expect_tx(b, kKBytes);
+          tma_load_4d_multicast(d, &a.kn, 0, tok, hk, it.pl.batch, b, 3);
+          tma_load_4d_multicast(d + kBlock, &a.kn, 64, tok, hk, it.pl.batch, b, 3);
+          tma_load_4d_multicast(d + 2 * kBlock, &a.kp, 0, tok, 0, it.pl.batch, b, 3);
+          ++nk;
+        };
+        auto values = [&](int i) {
+          const uint32_t s = nv % kVStages, b = bar(&sh->vfull[s]), d = sbase + kPtV + s * kVBytes + rank * (kBlock / 2);
+          ok = ok && at_wait(bar(&sh->vempty[s]), ((nv / kVStages) & 1) ^ 1, abort, p.budget_ns, p.status);
+          if (!ok) return;
+          const int tok = t0 + i * kPtTile;
+          mbar_arrive_expect_tx(b, kVBytes);
+          tma_load_4d_multicast(d, &a.v, 0, tok, hk, it.pl.batch, b, 3);
+          tma_load_4d_multicast(d + kBlock, &a.v, 64, tok, hk, it.pl.batch, b, 3);
+          ++nv;
+        };
+        keys(0);
+        for (int i = 0; i < it.nt && ok; ++i) {
+          if (i + 1 < it.nt) keys(i + 1);
+          values(i);
+        }
       }
       // every copy into this CTA, and every release of a stage by the peer, has landed before the cluster may exit
       const uint64_t t0 = globaltimer_ns();
@@ -189,15 +210,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         return ok;
       };
       uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stage and phase of the rings
-      auto qk = [&](int i) {  // S = Q K_i^T (past this CTA's last tile: release the stage only)
+      uint32_t g_qk = 0, g_pv = 0, mine = 0;    // tiles done, items with rows
+      auto qk = [&](bool own) {  // S = Q K^T (past this CTA's last tile: release the stage only)
         if (!wait(&sh->kfull[ks], kp)) return;
-        if (i < n) {
+        if (own) {
           const uint64_t bd = dk + ks * (kKBytes >> 4);
-          const uint32_t d = tmem + (i & 1) * 128;
+          const uint32_t d = tmem + (g_qk & 1) * 128;
 #pragma unroll
           for (int k = 0; k < 12; ++k)
             tc::mma_f16_ts(d, tmem + kTmQ + k * 8, bd + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), id_qk, k > 0);
-          tc::commit(bar(&sh->sfull[i & 1]));
+          tc::commit(bar(&sh->sfull[g_qk & 1]));
+          ++g_qk;
         }
         tc::commit_multicast(bar(&sh->kempty[ks]), 3);
         if (++ks == kKStages) {
@@ -205,17 +228,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
           kp ^= 1;
         }
       };
-      auto pv = [&](int i) {  // O += P V_i
+      auto pv = [&](bool own, bool first, bool last) {  // O (+)= P V
         if (!wait(&sh->vfull[vs], vp)) return;
-        if (i < n) {
-          if (!wait(&sh->pfull[i & 1], (i >> 1) & 1)) return;
+        if (own) {
+          // (the item before this one has been read from O)
+          if (first && mine > 0 && !wait(&sh->ofree, (mine - 1) & 1)) return;
+          if (!wait(&sh->pfull[g_pv & 1], (g_pv >> 1) & 1)) return;
           tc::fence_after_sync();
           const uint64_t bd = dv + vs * (kVBytes >> 4);
-          const uint32_t pa = tmem + (i & 1) * 128;
-          tc::mma_f16_ts(tmem + kTmO, pa, bd, id_pv, i > 0);
+          const uint32_t pa = tmem + (g_pv & 1) * 128;
+          tc::mma_f16_ts(tmem + kTmO, pa, bd, id_pv, !first);
 #pragma unroll
           for (int k = 1; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, true);
           tc::commit(bar(&sh->pvdone));
+          if (last) tc::commit(bar(&sh->olast));
+          ++g_pv;
         }
         tc::commit_multicast(bar(&sh->vempty[vs]), 3);
         if (++vs == kVStages) {
@@ -223,156 +250,193 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
           vp ^= 1;
         }
       };
-      if (n > 0 && wait(&sh->qready, 0)) tc::fence_after_sync();
-      if (ok) qk(0);
-      for (int i = 0; i < nt && ok; ++i) {
-        if (i + 1 < nt) qk(i + 1);
-        if (ok) pv(i);
+      for (int k = 0; ok; ++k) {
+        const long long x = prompt_item(cluster, p.clusters, k);
+        if (x >= items) break;
+        const Item it = item_at(x);
+        if (it.n > 0) {
+          if (!wait(&sh->qready, mine & 1)) break;
+          tc::fence_after_sync();
+        }
+        qk(it.n > 0);
+        for (int i = 0; i < it.nt && ok; ++i) {
+          if (i + 1 < it.nt) qk(i + 1 < it.n);
+          if (ok) pv(i < it.n, i == 0, i == it.n - 1);
+        }
+        mine += it.n > 0;
       }
       // every MMA issued so far has completed before TMEM is released
       tc::commit(bar(&sh->done));
       mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));
     }
     __syncwarp();
-  } else if (n > 0) {
+  } else {
     // ============================================================ queries, softmax, results
     const int q = warp & 3, hf = warp >> 2;
     const int r = q * 32 + lane;
-    const int qi = pl.row0 + rank * kPtTile + r;  // query's token in its sequence
-    const bool live = qi < pl.len;
-    const int tok = pl.begin + (live ? qi : 0);
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-    {  // queries: q_nope by one thread of the row, q_pe by the other
-      const PromptTensor& t = hf ? p.q_pe : p.q_nope;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(t.ptr) + (size_t)pl.batch * t.sb + (size_t)h * t.sh + (size_t)tok * t.st);
+    const float scale = p.scale_log2;
+    bool ok = true;
+    // A row's 24 16-byte units of q_nope and q_pe: 12 to each of its two threads.
+    auto q_unit = [&](const Item& it, int i) {
+      const int u = hf * 12 + i;
+      const bool pe = u >= 16;
+      const PromptTensor& t = pe ? p.q_pe : p.q_nope;
+      const int qi = it.pl.row0 + rank * kPtTile + r;
+      const int tok = it.pl.begin + (qi < it.pl.len ? qi : 0);
+      return reinterpret_cast<const uint4*>(static_cast<const T*>(t.ptr) + (size_t)it.pl.batch * t.sb + (size_t)it.pl.head * t.sh + (size_t)tok * t.st) + (pe ? u - 16 : u);
+    };
+    auto load_q = [&](const Item& it) {
+      const bool live = it.pl.row0 + rank * kPtTile + r < it.pl.len;
+      uint4 v[12];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (c && hf) break;
-        uint4 v[8];
+      for (int i = 0; i < 12; ++i) v[i] = live ? *q_unit(it, i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = live ? src[c * 8 + i] : make_uint4(0, 0, 0, 0);
-        const uint32_t d = tl + kTmQ + hf * 64 + c * 32;
-        tc::st16(d, reinterpret_cast<const uint32_t*>(v));
-        tc::st16(d + 16, reinterpret_cast<const uint32_t*>(v + 4));
-      }
+      for (int i = 0; i < 3; ++i) tc::st16(tl + kTmQ + hf * 48 + i * 16, reinterpret_cast<const uint32_t*>(v + 4 * i));
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&sh->qready));
-    }
-    float m = -INFINITY;  // maximum the weights are relative to (raw score units)
-    float l = 0.f;        // sum over this thread's keys
-    const float scale = p.scale_log2;
-    bool ok = true;
-    auto meet = [&](int k) {  // k-th meeting of the two warps of these rows
+    };
+    uint32_t meets = 0;
+    auto meet = [&]() {  // the two warps of these rows
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&sh->pair[q]));
-      return at_wait_warp(bar(&sh->pair[q]), k & 1, abort, p.budget_ns, p.status);
+      return at_wait_warp(bar(&sh->pair[q]), meets++ & 1, abort, p.budget_ns, p.status);
     };
-    for (int i = 0; i < n; ++i) {
-      const uint32_t ts = tl + (i & 1) * 128;
-      if (!at_wait_warp(bar(&sh->sfull[i & 1]), (i >> 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
-      tc::fence_after_sync();
-      uint32_t s[64];
-      tc::ld32(ts + hf * 64, s);
-      tc::ld32(ts + hf * 64 + 32, s + 32);
-      tc::wait_ld();
-      // keys this row sees among this thread's 64
-      const int limit = (p.causal ? min(qi + 1, pl.len) : pl.len) - i * kPtTile - hf * 64;
-      if (__any_sync(~0u, limit < 64)) {
-#pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (k >= limit) s[k] = 0xff800000u;
+    uint32_t g = 0, gv = 0, mine = 0;  // tiles of this CTA, tiles of the pair, items with rows
+    Item it = item_at(prompt_item(cluster, p.clusters, 0));
+    if (it.n > 0) load_q(it);
+    for (int round = 0; ok; ++round) {
+      const long long xn = prompt_item(cluster, p.clusters, round + 1);
+      const bool more = xn < items;
+      Item nx = it;
+      if (more) {
+        nx = item_at(xn);
+        if (nx.n > 0)
+          for (int i = 0; i < 12; i += 4)  // the next queries' lines into L2
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q_unit(nx, i)));
       }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
-#pragma unroll
-      for (int k = 4; k < 64; k += 4)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[k + j]));
-      float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      sh->row[i & 1][hf][r] = tile_max;
-      // both threads of a row have their scores in registers and their maxima in place
-      if (!meet(i)) { ok = false; break; }
-      tile_max = fmaxf(tile_max, sh->row[i & 1][hf ^ 1][r]);
-      if (__any_sync(~0u, (tile_max - m) * scale > kRescale)) {
-        const float m_new = fmaxf(m, tile_max);
-        const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * scale);
-        if (i > 0) {
-          if (!at_wait_warp(bar(&sh->pvdone), (i - 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
-          tc::fence_after_sync();
-          tmem_scale<64>(tl + kTmO + hf * 64, f);
-          tc::wait_st();
-        }
-        l *= f;
-        m = m_new;
-      }
-      const float mu = m == -INFINITY ? 0.f : m;
-      const uint64_t sc2 = f2_pack(scale, scale), ng2 = f2_pack(-mu * scale, -mu * scale);
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int j = c * 32 + 2 * k;
-          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), sc2, ng2);
-          float x0, x1;
-          f2_unpack(x, x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          sum[k & 1] = f2_add(sum[k & 1], f2_pack(x0, x1));
-          pk[k] = E::pack(x0, x1);
-        }
-        tc::st16(ts + hf * 32 + c * 16, pk);
-      }
-      tc::wait_st();
-      tc::fence_before_sync();
-      const int valid = pl.len - i * kPtTile;
-      if (valid < kPtTile) {
-        // value rows past the sequence's end: whole 128-byte rows, so the swizzle does not matter
-        const uint32_t vs = i % kVStages;
-        if (!at_wait_warp(bar(&sh->vfull[vs]), (i / kVStages) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
-        for (int x = tid; x < (kPtTile - valid) * 16; x += 256)
-          *reinterpret_cast<uint4*>(smem + kPtV + vs * kVBytes + ((x >> 3) & 1) * kBlock + (valid + x / 16) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-        tc::fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(&sh->pfull[i & 1]));
-      float a0, a1, b0, b1;
-      f2_unpack(sum[0], a0, a1);
-      f2_unpack(sum[1], b0, b1);
-      l += (a0 + a1) + (b0 + b1);
-    }
-    sh->row[n & 1][hf][r] = l;
-    // (phases of pvdone are awaited in order: a parity tells neighbours apart only, and the scores of tile
-    // n - 1 say no more than that the output of tile n - 3 is done)
-    ok = ok && meet(n) && (n < 2 || at_wait_warp(bar(&sh->pvdone), n & 1, abort, p.budget_ns, p.status)) &&
-         at_wait_warp(bar(&sh->pvdone), (n - 1) & 1, abort, p.budget_ns, p.status);
-    if (ok) {
-      tc::fence_after_sync();
-      l = sh->row[n & 1][0][r] + sh->row[n & 1][1][r];
-      const float iv = l == 0.f ? 0.f : 1.f / l;
-      T* out = static_cast<T*>(const_cast<void*>(p.out.ptr)) + (size_t)pl.batch * p.out.sb + (size_t)h * p.out.sh + (size_t)tok * p.out.st + hf * 64;
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t o[32];
-        tc::ld32(tl + kTmO + hf * 64 + c, o);
+      const int n = it.n;
+      const int qi = it.pl.row0 + rank * kPtTile + r;  // query's token in its sequence
+      const bool live = qi < it.pl.len;
+      float m = -INFINITY;  // maximum the weights are relative to (raw score units)
+      float l = 0.f;        // sum over this thread's keys
+      for (int i = 0; i < n; ++i, ++g) {
+        const uint32_t ts = tl + (g & 1) * 128;
+        if (!at_wait_warp(bar(&sh->sfull[g & 1]), (g >> 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+        tc::fence_after_sync();
+        uint32_t s[64];
+        tc::ld32(ts + hf * 64, s);
+        tc::ld32(ts + hf * 64 + 32, s + 32);
         tc::wait_ld();
+        // keys this row sees among this thread's 64
+        const int limit = (p.causal ? min(qi + 1, it.pl.len) : it.pl.len) - i * kPtTile - hf * 64;
+        if (__any_sync(~0u, limit < 64)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= limit) s[k] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
+#pragma unroll
+        for (int k = 4; k < 64; k += 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[k + j]));
+        float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const uint32_t par = meets & 1;
+        sh->row[par][hf][r] = tile_max;
+        // both threads of a row have their scores in registers and their maxima in place
+        if (!meet()) { ok = false; break; }
+        tile_max = fmaxf(tile_max, sh->row[par][hf ^ 1][r]);
+        if (__any_sync(~0u, (tile_max - m) * scale > kRescale)) {
+          const float m_new = fmaxf(m, tile_max);
+          const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * scale);
+          if (i > 0) {
+            if (!at_wait_warp(bar(&sh->pvdone), (g - 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+            tc::fence_after_sync();
+            tmem_scale<64>(tl + kTmO + hf * 64, f);
+            tc::wait_st();
+          }
+          l *= f;
+          m = m_new;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = f2_pack(scale, scale), ng2 = f2_pack(-mu * scale, -mu * scale);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int j = c * 32 + 2 * k;
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), sc2, ng2);
+            float x0, x1;
+            f2_unpack(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum[k & 1] = f2_add(sum[k & 1], f2_pack(x0, x1));
+            pk[k] = E::pack(x0, x1);
+          }
+          tc::st16(ts + hf * 32 + c * 16, pk);
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        const int valid = it.pl.len - i * kPtTile;
+        if (valid < kPtTile) {
+          // value rows past the sequence's end: whole 128-byte rows, so the swizzle does not matter
+          const uint32_t use = gv + i, vs = use % kVStages;
+          if (!at_wait_warp(bar(&sh->vfull[vs]), (use / kVStages) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+          for (int x = tid; x < (kPtTile - valid) * 16; x += 256)
+            *reinterpret_cast<uint4*>(smem + kPtV + vs * kVBytes + ((x >> 3) & 1) * kBlock + (valid + x / 16) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh->pfull[g & 1]));
+        float a0, a1, b0, b1;
+        f2_unpack(sum[0], a0, a1);
+        f2_unpack(sum[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
+      }
+      if (!ok) break;
+      gv += it.nt;
+      // the next item's queries go in while the last output MMA runs (all score MMAs of this one are done)
+      if (more && nx.n > 0) load_q(nx);
+      if (n > 0) {
+        const uint32_t par = meets & 1;
+        sh->row[par][hf][r] = l;
+        // (a barrier of its own: a parity says which of two neighbouring phases is done, and this warp has not followed
+        // those of pvdone)
+        ok = meet() && at_wait_warp(bar(&sh->olast), mine++ & 1, abort, p.budget_ns, p.status);
+        if (!ok) break;
+        tc::fence_after_sync();
+        l = sh->row[par][0][r] + sh->row[par][1][r];
+        const float iv = l == 0.f ? 0.f : 1.f / l;
+        const int tok = it.pl.begin + (live ? qi : 0);
+        T* out = static_cast<T*>(const_cast<void*>(p.out.ptr)) + (size_t)it.pl.batch * p.out.sb + (size_t)it.pl.head * p.out.sh + (size_t)tok * p.out.st + hf * 64;
+        uint32_t o[64];
+        tc::ld32(tl + kTmO + hf * 64, o);
+        tc::ld32(tl + kTmO + hf * 64 + 32, o + 32);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh->ofree));
         if (live) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
+          for (int k = 0; k < 64; k += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               w[j] = E::pack(__uint_as_float(o[k + 2 * j]) * iv, __uint_as_float(o[k + 2 * j + 1]) * iv);
-            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          if (hf == 0 && p.lse)
+            p.lse[((size_t)it.pl.batch * p.heads + it.pl.head) * p.s + tok] = l == 0.f ? -INFINITY : (m * scale + log2f(l)) * kLn2;
         }
       }
-      if (live && hf == 0 && p.lse)
-        p.lse[((size_t)pl.batch * p.heads + h) * p.s + tok] = l == 0.f ? -INFINITY : (m * scale + log2f(l)) * kLn2;
+      if (!more) break;
+      it = nx;
     }
   }
   tc::fence_before_sync();
@@ -404,7 +468,9 @@ cudaError_t launch(const PromptParams& p, PromptMaps* m, cudaStream_t stream) {
   PtArgs a;
   a.kn = m->map[0]; a.kp = m->map[1]; a.v = m->map[2];
   a.p = p;
-  prompt_tc_kernel<T><<<dim3(2 * prompt_blocks(p, kPtRows), p.heads), kPtThreads, kPtSmem, stream>>>(a);
+  const long long items = (long long)prompt_blocks(p, kPtRows) * p.heads;
+  if (items < a.p.clusters) a.p.clusters = (int)items;
+  prompt_tc_kernel<T><<<2 * a.p.clusters, kPtThreads, kPtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
