@@ -34,6 +34,13 @@ struct AppendParams {
 cudaError_t append_launch(bool bf16, const AppendParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged attention
+// An item that worker i began and others went on with (rows = 0: none).
+struct PagedJoin {
+  int row;          // first row of [T * H]
+  int rows;
+  int last_worker;  // the worker with its last piece
+  int pad;
+};
 struct PagedParams {
   const void* q_lat;
   const void* q_pe;
@@ -46,6 +53,7 @@ struct PagedParams {
   float* lse;  // [T, H] or null
   float* part_o;   // [workers][2][rows][512] fp32, unnormalised
   float* part_ml;  // [workers][2][rows][2]: running maximum (log2 units), sum
+  PagedJoin* joins;  // [workers]
   unsigned* status;
   int ql_ts, ql_hs, qp_ts, qp_hs, table_stride, lat_rs, kpe_rs;
   int page, nblocks, nseq, T, heads, n_uniform;
@@ -55,6 +63,7 @@ struct PagedParams {
 };
 // mma.sync kernel: items of 16 or 32 query rows.
 constexpr int kPagedMmaRows = 32;
+inline int paged_mma_workers(int rows, int num_sms) { return rows == 16 ? 2 * num_sms : num_sms; }  // CTAs that are resident
 cudaError_t paged_mma_prepare(bool bf16);  // kernel attributes, once per device
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
 // tcgen05 kernel: items of 128 query rows, two CTAs per worker; pages whose

@@ -25,6 +25,7 @@ struct mla_attn_s {
   unsigned* status;
   float* part_o;
   float* part_ml;
+  PagedJoin* joins;
   PagedMaps paged_maps;
   PromptMaps prompt_maps;
 };
@@ -88,10 +89,10 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     delete h;
     return fail(e, "device query");
   }
-  // workspace: [status, 256 bytes] | two partial results per worker
+  // workspace: [status, 256 bytes] | a join record per worker | two partial results per worker
   const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedTcRows;
   const size_t rows = rows_mma > rows_tc ? rows_mma : rows_tc;
-  const size_t ml_off = 256, o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+  const size_t join_off = 256, ml_off = join_off + (((size_t)h->num_sms * 2 * sizeof(PagedJoin) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
   e = cudaMalloc(&h->ws, o_off + rows * kRank * sizeof(float));
   if (e != cudaSuccess) {
     delete h;
@@ -106,6 +107,7 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   }
   unsigned char* base = static_cast<unsigned char*>(h->ws);
   h->status = reinterpret_cast<unsigned*>(base);
+  h->joins = reinterpret_cast<PagedJoin*>(base + join_off);
   h->part_ml = reinterpret_cast<float*>(base + ml_off);
   h->part_o = reinterpret_cast<float*>(base + o_off);
   // (shared memory beyond the default is asked for once, not per call)
@@ -217,16 +219,16 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   PagedParams p = {};
   p.q_lat = a.q_latent; p.q_pe = a.q_pe; p.cu_q = a.cu_q; p.kv_lens = a.kv_lens; p.table = a.block_table;
   p.latent = a.latent_cache; p.kpe = a.kpe_cache; p.out = a.out; p.lse = a.lse; p.part_o = h->part_o;
-  p.part_ml = h->part_ml; p.status = h->status; p.ql_ts = a.q_latent_token_stride; p.ql_hs = a.q_latent_head_stride;
+  p.part_ml = h->part_ml; p.joins = h->joins; p.status = h->status; p.ql_ts = a.q_latent_token_stride; p.ql_hs = a.q_latent_head_stride;
   p.qp_ts = a.q_pe_token_stride; p.qp_hs = a.q_pe_head_stride; p.table_stride = a.table_stride;
   p.lat_rs = a.latent_row_stride; p.kpe_rs = a.kpe_row_stride; p.page = a.page_size; p.nblocks = a.num_blocks;
-  p.nseq = a.num_seqs; p.T = a.T; p.heads = H; p.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs; p.workers = h->num_sms;
+  p.nseq = a.num_seqs; p.T = a.T; p.heads = H; p.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs;
   p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   // (with ragged chunks the host knows only the average)
   const long long rows_per_seq = (long long)(a.T / a.num_seqs > 0 ? a.T / a.num_seqs : 1) * H;
   const bool tc = rows_per_seq > kPagedMmaRows && paged_tc_box(a.page_size) >= 8;
   const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
-  if (tc) p.workers = h->num_sms / 2;
+  p.workers = tc ? h->num_sms / 2 : paged_mma_workers(rows, h->num_sms);
   cudaError_t e = tc ? paged_tc_launch(bf16, p, &h->paged_maps, stream) : paged_mma_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention launch");
   e = paged_combine_launch(bf16, p, rows, stream);

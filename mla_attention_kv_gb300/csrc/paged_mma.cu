@@ -13,10 +13,15 @@
 //
 // With at most 32 rows an item reads 1152 bytes per key for at most
 // 2 * 32 * 1088 FLOPs, well under the ratio at which the tensor cores
-// matter, so the kernel is built around the key stream: one CTA per SM, two
-// stages of 64 keys (74 KB each) filled by 16-byte cp.async (any page size;
-// a page may end anywhere in a tile), each key row used from shared memory
-// twice (as key and as value).
+// matter, so the kernel is built around the key stream: two stages of keys
+// filled by 16-byte cp.async (any page size; a page may end anywhere in a
+// tile), each key row used from shared memory twice (as key and as value).
+// What bounds it is the latency of the way through a tile (scores, softmax
+// over the warps, output), so the work of a tile is spread over many warps:
+// 16-row items run two CTAs of 8 warps per SM on tiles of 32 keys, 32-row
+// items one CTA of 16 warps on tiles of 64 (one CTA of 8 warps with tiles of
+// 64 reached 2.5 TB/s on 64 sequences of up to 4096 keys, at 20 % of the
+// issue slots).
 #include "attn.h"
 #include "common.cuh"
 #include "paged_plan.cuh"
@@ -24,22 +29,33 @@
 namespace mla {
 namespace {
 
-constexpr int kPmThreads = 256;
 constexpr int kPitch = kQkDim * 2 + 16;  // bytes per key / query row in shared memory: 73 16-byte units
-constexpr int kStageBytes = kKeyTile * kPitch;
-constexpr int kSPitch = kKeyTile + 4;    // floats
-constexpr int kPPitch = kKeyTile + 8;    // 16-bit values
+constexpr int kSplit = 4;                // parts of the 576 columns that a tile's scores are summed from
+constexpr int kRowsPerWarp = 4;          // key rows that a warp copies
 
+// MT 16-row blocks of query rows; KT keys per tile.
 template <int MT>
-struct PmSmem {
+struct PmCfg {
   static constexpr int R = 16 * MT;
+  static constexpr int KT = MT == 1 ? 32 : 64;
+  static constexpr int kWarps = KT / 16 * kSplit;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kCtas = MT == 1 ? 2 : 1;  // per SM
+  static constexpr int kCols = kRank / kWarps;   // output columns of a warp
+  static constexpr int TPR = kThreads / R;       // softmax threads per row
+  static constexpr int KPT = KT / TPR;           // keys per softmax thread
+  static constexpr int kSPitch = KT + 4;         // floats
+  static constexpr int kPPitch = KT + 8;         // 16-bit values
+  static constexpr int kStageBytes = KT * kPitch;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + R * kPitch;
   static constexpr int kS = kK + 2 * kStageBytes;
-  static constexpr int kP = kS + 2 * R * kSPitch * 4;
+  static constexpr int kP = kS + kSplit * R * kSPitch * 4;
   static constexpr int kRow = kP + R * kPPitch * 2;  // alpha [R], then 1 / l [R]
   static constexpr int kPlan = (kRow + 2 * R * 4 + 15) & ~15;
   static constexpr int kBytes = kPlan + (int)sizeof(PlanShared);
+  static_assert(kRowsPerWarp * kWarps == KT, "copies of a tile");
+  static_assert(TPR <= 32 && KPT * TPR == KT, "softmax threads");
 };
 
 // Row index (block * page + offset) of key k of sequence s in the cache, or
@@ -56,12 +72,10 @@ __device__ __forceinline__ int cache_row(const PagedParams& p, int s, int k, int
 }
 
 template <typename T, int MT>
-__global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_mma_kernel(const PagedParams p) {
   using E = Elem<T>;
-  using S = PmSmem<MT>;
-  constexpr int R = S::R;
-  constexpr int TPR = kPmThreads / R;        // softmax threads per row
-  constexpr int KPT = kKeyTile / TPR;        // keys per softmax thread
+  using S = PmCfg<MT>;
+  constexpr int R = S::R, KT = S::KT, TPR = S::TPR, KPT = S::KPT, NT = S::kCols / 8;
   extern __shared__ __align__(16) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   PlanShared* plan = reinterpret_cast<PlanShared*>(smem + S::kPlan);
@@ -71,14 +85,15 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.heads;
 
-  grid_dep_launch_dependents();  // (the joining kernel may take its place and plan)
+  grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = plan_total(p, plan, R, blockIdx.x == 0);
-  if (total == 0) return;
-  const int W = plan_workers(total, p.workers);
+  const int W = total > 0 ? plan_workers(total, p.workers) : 0;
   const int w = blockIdx.x;
-  if (w >= W) return;
+  if (w >= W) {
+    if (tid == 0) p.joins[w].rows = 0;
+    return;
+  }
   const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
-  if (x0 >= x1) return;
 
   PlanCursor c;
   c.seek(p, plan, R, x0);
@@ -89,34 +104,35 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
     const int keys = q.keys_of_item(c.j, R, H);
     const int tiles = (keys + kKeyTile - 1) / kKeyTile;
     const long long a = x0 > c.lo ? x0 : c.lo, b = x1 < c.hi ? x1 : c.hi;
-    const int t0 = c.tile_at(a, tiles), t1 = c.tile_at(b, tiles);
+    // this worker's tiles of KT keys
+    constexpr int kSub = kKeyTile / KT;
+    const int t0 = c.tile_at(a, tiles) * kSub, t1 = min(c.tile_at(b, tiles) * kSub, (keys + KT - 1) / KT);
     const bool whole = c.lo >= x0 && c.hi <= x1;
     const int s = c.s;
 
-    // ---- key tiles: warp w loads rows 8w .. 8w+7 of a stage
-    auto rows_of = [&](int tile) {  // lanes 0-7 hold their rows' cache rows
-      return lane < 8 ? cache_row(p, s, tile * kKeyTile + warp * 8 + lane, keys) : -1;
+    if (tid == 0 && c.hi >= x1) plan_post_join(p, c, R, w, x0, x1, total, W);
+
+    // ---- key tiles: warp w copies rows 4w .. 4w + 3 of a stage
+    auto rows_of = [&](int tile) {  // lanes 0-3 hold their rows' cache rows
+      return lane < kRowsPerWarp ? cache_row(p, s, tile * KT + warp * kRowsPerWarp + lane, keys) : -1;
     };
     auto load = [&](int tile, int rows) {
-      const uint32_t st = sb + S::kK + (tile & 1) * kStageBytes + warp * 8 * kPitch;
+      const uint32_t st = sb + S::kK + (tile & 1) * S::kStageBytes + warp * kRowsPerWarp * kPitch;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < kRowsPerWarp; ++r) {
         const int row = __shfl_sync(~0u, rows, r);
         const T* src = static_cast<const T*>(p.latent) + (size_t)max(row, 0) * p.lat_rs;
         const uint32_t d = st + r * kPitch;
         cp_async16(d + lane * 16, src + lane * 8, row < 0 ? 0 : 16);
         cp_async16(d + 512 + lane * 16, src + 256 + lane * 8, row < 0 ? 0 : 16);
       }
-#pragma unroll
-      for (int r = 0; r < 8; r += 4) {
-        const int row = __shfl_sync(~0u, rows, r + (lane >> 3));
-        const T* src = static_cast<const T*>(p.kpe) + (size_t)max(row, 0) * p.kpe_rs;
-        cp_async16(st + (r + (lane >> 3)) * kPitch + 1024 + (lane & 7) * 16, src + (lane & 7) * 8, row < 0 ? 0 : 16);
-      }
+      const int row = __shfl_sync(~0u, rows, lane >> 3);
+      const T* src = static_cast<const T*>(p.kpe) + (size_t)max(row, 0) * p.kpe_rs;
+      cp_async16(st + (lane >> 3) * kPitch + 1024 + (lane & 7) * 16, src + (lane & 7) * 8, row < 0 ? 0 : 16);
     };
     __syncthreads();  // the previous item's stages and queries are read
     // ---- queries (rows past the end are zero), together with the first tile
-    for (int r = warp; r < R; r += kPmThreads / 32) {
+    for (int r = warp; r < R; r += S::kWarps) {
       const int tok = (row0 + r) / H, hd = (row0 + r) - tok * H;
       const bool ok = r < live;
       const T* ql = static_cast<const T*>(p.q_lat) + (ok ? (size_t)(q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs : 0);
@@ -131,11 +147,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
     if (t0 + 1 < t1) load(t0 + 1, rows_of(t0 + 1));
     cp_async_commit();
 
-    float acc[MT][8][4];
+    float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     const int srow = tid / TPR, sk0 = tid % TPR;  // softmax: row, first key (keys sk0 + TPR * i)
@@ -143,12 +159,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
     float m_run = -INFINITY, l_run = 0.f;
 
     for (int tile = t0; tile < t1; ++tile) {
-      int rows_next = tile + 2 < t1 ? rows_of(tile + 2) : -1;
+      const int rows_next = tile + 2 < t1 ? rows_of(tile + 2) : -1;
       cp_async_wait<1>();
       __syncthreads();
-      const uint32_t st = sb + S::kK + (tile & 1) * kStageBytes;
-      {  // scores: warp = (16 keys kg, half kh of the 576 columns)
-        const int kg = warp & 3, kh = warp >> 2;
+      const uint32_t st = sb + S::kK + (tile & 1) * S::kStageBytes;
+      {  // scores: warp = (16 keys kg, quarter kq of the 576 columns)
+        const int kg = warp % (KT / 16), kq = warp / (KT / 16);
         float sc[MT][2][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -156,10 +172,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[m][n][i] = 0.f;
-        const uint32_t kaddr = st + (kg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kPitch + kh * 576 + ((lane >> 3) & 1) * 16;
-        const uint32_t qaddr = sb + S::kQ + (lane & 15) * kPitch + kh * 576 + (lane >> 4) * 16;
-#pragma unroll 6
-        for (int k = 0; k < 18; ++k) {
+        const uint32_t kaddr = st + (kg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kPitch + kq * 288 + ((lane >> 3) & 1) * 16;
+        const uint32_t qaddr = sb + S::kQ + (lane & 15) * kPitch + kq * 288 + (lane >> 4) * 16;
+#pragma unroll
+        for (int k = 0; k < kQkDim / 16 / kSplit; ++k) {
           uint32_t b0, b1, b2, b3;
           ldsm_x4(kaddr + k * 32, b0, b1, b2, b3);
 #pragma unroll
@@ -174,9 +190,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float* d = sS + (kh * R + m * 16 + (lane >> 2)) * kSPitch + kg * 16 + n * 8 + (lane & 3) * 2;
+            float* d = sS + (kq * R + m * 16 + (lane >> 2)) * S::kSPitch + kg * 16 + n * 8 + (lane & 3) * 2;
             *reinterpret_cast<float2*>(d) = make_float2(sc[m][n][0], sc[m][n][1]);
-            *reinterpret_cast<float2*>(d + 8 * kSPitch) = make_float2(sc[m][n][2], sc[m][n][3]);
+            *reinterpret_cast<float2*>(d + 8 * S::kSPitch) = make_float2(sc[m][n][2], sc[m][n][3]);
           }
       }
       __syncthreads();
@@ -185,8 +201,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
           const int k = sk0 + i * TPR;
-          const float x = sS[srow * kSPitch + k] + sS[(R + srow) * kSPitch + k];
-          v[i] = tile * kKeyTile + k < limit ? x * p.scale_log2 : -INFINITY;
+          const float* x4 = sS + srow * S::kSPitch + k;
+          const float x = (x4[0] + x4[R * S::kSPitch]) + (x4[2 * R * S::kSPitch] + x4[3 * R * S::kSPitch]);
+          v[i] = tile * KT + k < limit ? x * p.scale_log2 : -INFINITY;
           mx = fmaxf(mx, v[i]);
         }
 #pragma unroll
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
         const float mu = m_new == -INFINITY ? 0.f : m_new;  // (a row with no key so far)
         const float alpha = exp2f(m_run - mu);
         float ls = 0.f;
-        T* prow = reinterpret_cast<T*>(smem + S::kP) + srow * kPPitch;
+        T* prow = reinterpret_cast<T*>(smem + S::kP) + srow * S::kPPitch;
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
           const float e = exp2f(v[i] - mu);
@@ -207,13 +224,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
         if (sk0 == 0) sAlpha[srow] = alpha;
       }
       __syncthreads();
-      {  // output: warp = 64 latent columns
+      {  // output: warp = kCols latent columns
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const float a0 = sAlpha[m * 16 + (lane >> 2)], a1 = sAlpha[m * 16 + (lane >> 2) + 8];
           if (__any_sync(~0u, a0 != 1.f || a1 != 1.f)) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < NT; ++n) {
               acc[m][n][0] *= a0;
               acc[m][n][1] *= a0;
               acc[m][n][2] *= a1;
@@ -221,16 +238,16 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
             }
           }
         }
-        const uint32_t paddr = sb + S::kP + (lane & 15) * (kPPitch * 2) + (lane >> 4) * 16;
-        const uint32_t vaddr = st + (lane & 15) * kPitch + warp * 128 + (lane >> 4) * 16;
+        const uint32_t paddr = sb + S::kP + (lane & 15) * (S::kPPitch * 2) + (lane >> 4) * 16;
+        const uint32_t vaddr = st + (lane & 15) * kPitch + warp * (S::kCols * 2) + (lane >> 4) * 16;
 #pragma unroll
-        for (int k = 0; k < kKeyTile / 16; ++k) {
+        for (int k = 0; k < KT / 16; ++k) {
           uint32_t af[MT][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
-            ldsm_x4(paddr + m * 16 * kPPitch * 2 + k * 32, af[m][0], af[m][1], af[m][2], af[m][3]);
+            ldsm_x4(paddr + m * 16 * S::kPPitch * 2 + k * 32, af[m][0], af[m][1], af[m][2], af[m][3]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < NT / 2; ++n) {
             uint32_t b0, b1, b2, b3;
             ldsm_x4_trans(vaddr + k * 16 * kPitch + n * 32, b0, b1, b2, b3);
 #pragma unroll
@@ -266,9 +283,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
           const int r = m * 16 + (lane >> 2) + hf * 8;
           const float iv = sInv[r];
           if (r < live) {
-            uint32_t* o = reinterpret_cast<uint32_t*>(out + (size_t)r * kRank + warp * 64) + (lane & 3);
+            uint32_t* o = reinterpret_cast<uint32_t*>(out + (size_t)r * kRank + warp * S::kCols) + (lane & 3);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) o[n * 4] = E::pack(acc[m][n][2 * hf] * iv, acc[m][n][2 * hf + 1] * iv);
+            for (int n = 0; n < NT; ++n) o[n * 4] = E::pack(acc[m][n][2 * hf] * iv, acc[m][n][2 * hf + 1] * iv);
           }
         }
     } else {
@@ -285,9 +302,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int r = m * 16 + (lane >> 2) + hf * 8;
-            float2* o = reinterpret_cast<float2*>(po + (size_t)r * kRank + warp * 64) + (lane & 3);
+            float2* o = reinterpret_cast<float2*>(po + (size_t)r * kRank + warp * S::kCols) + (lane & 3);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) o[n * 4] = make_float2(acc[m][n][2 * hf], acc[m][n][2 * hf + 1]);
+            for (int n = 0; n < NT; ++n) o[n * 4] = make_float2(acc[m][n][2 * hf], acc[m][n][2 * hf + 1]);
           }
       }
     }
@@ -295,58 +312,70 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_mma_kernel(const PagedPar
 }
 
 // ---------------------------------------------------------------- combine
-// Block (v, y): the item that holds the beginning of worker v's range, if it
-// began in worker v - 1's range; rows 8y .. 8y + 7 of it, one warp per row.  With weights u_i = 2^(m_i - m):
+// Block (w1, y): the item that worker w1 began and others went on with (the
+// record that w1 left); rows 8y .. 8y + 7 of it, one warp per row.  With
+// weights u_i = 2^(m_i - m):
 //   l = sum u_i l_i,  out = sum u_i o_i / l,  lse = (m + log2 l) * ln 2.
+// Bound by latency: a lane reads the maximum and sum of one piece, and the
+// rows of four pieces are in flight at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p, int R) {
   using E = Elem<T>;
-  __shared__ PlanShared plan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the lengths were complete before the kernel that makes the pieces began; every block waits for the pieces, so
-  // that this kernel never ends before that one
-  const long long total = plan_total(p, &plan, R, false);
-  grid_dep_wait();
-  if (total == 0) return;
-  const int W = plan_workers(total, p.workers);
-  const int v = blockIdx.x + 1;
-  if (v >= W) return;
-  const long long x = plan_worker_begin(total, v, W);
-  if (x >= total) return;
-  PlanCursor c;
-  c.seek(p, &plan, R, x);
-  if (c.lo == x) return;                                   // no item is cut here
-  const int w1 = plan_worker_of(c.lo, total, W), w2 = plan_worker_of(c.hi - 1, total, W);
-  if (v != w1 + 1) return;                                 // (every range is at least kMinRange long)
+  grid_dep_wait();  // (every block waits, so that this kernel never ends before the one that makes the pieces)
+  const int w1 = blockIdx.x;
+  const PagedJoin join = p.joins[w1];
   const int r = blockIdx.y * 8 + warp;
-  if (r >= R || c.j * R + r >= c.q.n * p.heads) return;
+  if (r >= join.rows) return;
+  const int w2 = join.last_worker;
+  const size_t row = (size_t)join.row + r;
+  const int n = w2 - w1 + 1;
+  auto slot = [&](int i) { return (size_t)(w1 + i) * 2 + (i == 0 ? 1 : 0); };
+  auto ml = [&](int i) { return i < n ? reinterpret_cast<const float2*>(p.part_ml)[slot(i) * R + r] : make_float2(-INFINITY, 0.f); };
   float m = -INFINITY;
-  for (int u = w1; u <= w2; ++u) {
-    const size_t slot = (size_t)u * 2 + (u == w1 ? 1 : 0);
-    const float* ml = p.part_ml + (slot * R + r) * 2;
-    if (ml[1] != 0.f) m = fmaxf(m, ml[0]);
+  for (int i = lane; i < n; i += 32) {
+    const float2 a = ml(i);
+    if (a.y != 0.f) m = fmaxf(m, a.x);
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   float l = 0.f, o[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int u = w1; u <= w2; ++u) {
-    const size_t slot = (size_t)u * 2 + (u == w1 ? 1 : 0);
-    const float* ml = p.part_ml + (slot * R + r) * 2;
-    if (ml[1] == 0.f) continue;  // no key in this piece
-    const float f = exp2f(ml[0] - m);
-    l += f * ml[1];
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + (slot * R + r) * kRank);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float2 a = ml(i0 + lane);
+    const float f = a.y == 0.f ? 0.f : exp2f(a.x - m);  // (0: no key in this piece, its row is not written)
+    l += f * a.y;
+    const int end = min(32, n - i0);
+    for (int j0 = 0; j0 < end; j0 += 4) {
+      float4 x[4][4];
+      float w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = po[i * 32 + lane];
-      o[4 * i] += f * a.x;
-      o[4 * i + 1] += f * a.y;
-      o[4 * i + 2] += f * a.z;
-      o[4 * i + 3] += f * a.w;
+      for (int j = 0; j < 4; ++j) {
+        w[j] = __shfl_sync(~0u, f, (j0 + j) & 31);
+        if (j0 + j >= end) w[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[j] != 0.f) {
+          const float4* po = reinterpret_cast<const float4*>(p.part_o + (slot(i0 + j0 + j) * R + r) * kRank);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j][i] = po[i * 32 + lane];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[4 * i] += w[j] * x[j][i].x;
+          o[4 * i + 1] += w[j] * x[j][i].y;
+          o[4 * i + 2] += w[j] * x[j][i].z;
+          o[4 * i + 3] += w[j] * x[j][i].w;
+        }
     }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
   const float iv = l == 0.f ? 0.f : 1.f / l;
-  const size_t row = (size_t)c.q.begin * p.heads + c.j * R + r;
   uint2* d = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * kRank);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -356,11 +385,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p,
 
 template <typename T, int MT>
 cudaError_t prepare_mma() {
-  return cudaFuncSetAttribute(paged_mma_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PmSmem<MT>::kBytes);
+  return cudaFuncSetAttribute(paged_mma_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PmCfg<MT>::kBytes);
 }
 template <typename T, int MT>
 cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream) {
-  paged_mma_kernel<T, MT><<<p.workers, kPmThreads, PmSmem<MT>::kBytes, stream>>>(p);
+  paged_mma_kernel<T, MT><<<p.workers, PmCfg<MT>::kThreads, PmCfg<MT>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -382,7 +411,7 @@ cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cuda
   if (p.workers < 2) return cudaSuccess;
   // launched while the kernel before it runs (it waits for that one's end before it reads the pieces)
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(p.workers - 1, (rows + 7) / 8);
+  c.gridDim = dim3(p.workers, (rows + 7) / 8);
   c.blockDim = dim3(256);
   c.stream = stream;
   cudaLaunchAttribute at = {};

@@ -9,8 +9,7 @@
 // [total * w / W, total * (w + 1) / W).  A range may begin and end inside an
 // item; such items are computed in pieces whose results (unnormalised
 // output, maximum, sum) go to the workspace and are joined in a fixed order
-// by the combine kernel, so results do not depend on timing.  The joining
-// kernel derives the same split again from the same lengths.
+// by the combine kernel, so results do not depend on timing.
 //
 // The cumulative cost inside a sequence is the closed form
 //   F(j) = j * first + (last - first) * j^2 / (2 * items),
@@ -57,6 +56,7 @@ struct Seq {
     return keys_of_row((int)(last_row < rows ? last_row : rows - 1), H);
   }
   __host__ __device__ __forceinline__ long long cum(int j) const {
+    if (last == first) return (long long)j * first;  // (decode: no division)
     // (the divisor of a sequence without items only has to be nonzero)
     return (long long)j * first + (long long)(last - first) * j * j / (2 * (long long)(items > 0 ? items : 1));
   }
@@ -133,10 +133,14 @@ __host__ __device__ __forceinline__ int plan_workers(long long total, int W) {
   const long long w = total / kMinRange;
   return w < 1 ? 1 : (w < W ? (int)w : W);
 }
-__host__ __device__ __forceinline__ long long plan_worker_begin(long long total, int w, int W) { return total * w / W; }
+__host__ __device__ __forceinline__ long long plan_worker_begin(long long total, int w, int W) {
+  const long long n = total * w;
+  return n < (1ll << 32) ? (uint32_t)n / (uint32_t)W : n / W;
+}
 // The worker whose range holds position x.
 __host__ __device__ __forceinline__ int plan_worker_of(long long x, long long total, int W) {
-  return (int)(((x + 1) * W - 1) / total);
+  const long long n = (x + 1) * W - 1;
+  return n < (1ll << 32) && total < (1ll << 32) ? (int)((uint32_t)n / (uint32_t)total) : (int)(n / total);
 }
 
 // A place in the list of items: sequence, item, and the item's cost range.
@@ -192,8 +196,24 @@ struct PlanCursor {
   }
   // Key tile that position x of this item (lo <= x <= hi) stands for.
   __host__ __device__ __forceinline__ int tile_at(long long x, int tiles) const {
-    return (int)((x - lo) * tiles / (hi - lo));
+    const long long n = (x - lo) * tiles, d = hi - lo;
+    return n < (1u << 31) ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
   }
 };
+
+// Worker w's record for the joining kernel, made at the last item of its
+// range: the rows of that item if the item begins with it and goes on with
+// others.  One thread.
+__host__ __device__ __forceinline__ void plan_post_join(const PagedParams& p, const PlanCursor& c, int R, int w, long long x0,
+                                                        long long x1, long long total, int W) {
+  PagedJoin j = {0, 0, 0, 0};
+  if (c.lo >= x0 && c.hi > x1) {
+    const int left = c.q.n * p.heads - c.j * R;
+    j.row = c.q.begin * p.heads + c.j * R;
+    j.rows = left < R ? left : R;
+    j.last_worker = plan_worker_of(c.hi - 1, total, W);
+  }
+  p.joins[w] = j;
+}
 
 }  // namespace mla

@@ -85,11 +85,13 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
   const int half = blockIdx.x & 1, w = blockIdx.x >> 1;
 
   PlanShared* plan = reinterpret_cast<PlanShared*>(smem + kUtN);
-  grid_dep_launch_dependents();  // (the joining kernel may take its place and plan)
+  grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = plan_total(p, plan, kUtRows, blockIdx.x == 0);
-  if (total == 0) return;
-  const int W = plan_workers(total, p.workers);
-  if (w >= W) return;
+  const int W = total > 0 ? plan_workers(total, p.workers) : 0;
+  if (w >= W) {
+    if (tid == 0) p.joins[w].rows = 0;
+    return;
+  }
   const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
   PlanCursor first;
   first.seek(p, plan, kUtRows, x0);
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
     for (bool more = true; more && c.lo < x1 && ok;) {
       int t0, t1;
       const int keys = span(c, &t0, &t1);
+      if (tid == 0 && half == 0 && c.hi >= x1) plan_post_join(p, c, kUtRows, w, x0, x1, total, W);
       const int row = c.j * kUtRows + r;
       const bool live = row < c.q.n * H;
       const int limit0 = live ? c.q.keys_of_row(row, H) : 0;
@@ -338,9 +341,11 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
 #pragma unroll
-        for (int k = 4; k < 64; k += 4)
+        for (int k = 4; k < 60; k += 8)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[k + j]));
+          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + j + 4]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[60 + j]));
         const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         float f = 1.f;
         const bool grow_max = __any_sync(~0u, (tile_max - m) * scale > kRescale);

@@ -1,7 +1,7 @@
 // attn_plans.cu -- host check of the paged attention's work split
 // (paged_plan.cuh): the pieces that the workers take cover every key tile of
-// every item once, partial results have a slot of their own, and the joining
-// kernel's view of an item (first and last worker, slots) is the workers'.
+// every item once, partial results have a slot of their own, and the records
+// that the joining kernel works from (rows, last worker) fit the pieces.
 #include <cstdio>
 #include <cstdlib>
 #include <map>
@@ -80,22 +80,31 @@ static void run(const std::vector<int>& n, const std::vector<int>& L, int H, int
         got[{c.s, c.j}].push_back(pc);
       }
     }
-    // the joining kernel's view
+    // the records that the joining kernel works from
     std::map<std::pair<int, int>, int> joined;
-    for (int v = 1; v < We; ++v) {
-      const long long x = plan_worker_begin(total, v, We);
+    std::vector<PagedJoin> joins(W, PagedJoin{-1, -1, -1, -1});
+    p.joins = joins.data();
+    for (int w = 0; w < We; ++w) {
+      const long long x0 = plan_worker_begin(total, w, We), x1 = plan_worker_begin(total, w + 1, We);
       PlanCursor c;
-      c.seek(p, &ps, R, x);
-      if (c.lo == x) continue;
-      const int w1 = plan_worker_of(c.lo, total, We), w2 = plan_worker_of(c.hi - 1, total, We);
-      if (v != w1 + 1) continue;
-      CHECK(++joined[{c.s, c.j}] == 1);
-      const auto& ps2 = got[{c.s, c.j}];
-      CHECK((int)ps2.size() == w2 - w1 + 1);
-      for (size_t i = 0; i < ps2.size(); ++i) {
-        CHECK(ps2[i].worker == w1 + (int)i);
-        CHECK(ps2[i].slot == ps2[i].worker * 2 + (i == 0 ? 1 : 0));
-      }
+      c.seek(p, &ps, R, x0);
+      int posted = 0;
+      for (bool more = true; more && c.lo < x1; more = c.next(p, R))
+        if (c.hi >= x1) {
+          plan_post_join(p, c, R, w, x0, x1, total, We);
+          ++posted;
+          if (joins[w].rows == 0) continue;
+          CHECK(++joined[{c.s, c.j}] == 1);
+          const auto& ps2 = got[{c.s, c.j}];
+          CHECK(joins[w].row == c.q.begin * H + c.j * R);
+          CHECK(joins[w].rows == std::min(R, c.q.n * H - c.j * R));
+          CHECK(joins[w].last_worker - w + 1 == (int)ps2.size());
+          for (size_t i = 0; i < ps2.size(); ++i) {
+            CHECK(ps2[i].worker == w + (int)i);
+            CHECK(ps2[i].slot == ps2[i].worker * 2 + (i == 0 ? 1 : 0));
+          }
+        }
+      CHECK(posted == 1 && joins[w].rows >= 0);
     }
     for (auto& kv : got) CHECK((kv.second.size() > 1) == (joined.count(kv.first) == 1));
   }
