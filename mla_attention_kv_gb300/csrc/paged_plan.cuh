@@ -127,8 +127,9 @@ __device__ __forceinline__ long long plan_total(const PagedParams& p, PlanShared
   return ps->base[nt];
 }
 
-// Workers that take part: a range is not worth less than kMinRange.
-constexpr int kMinRange = 2;
+// Workers that take part: no range is shorter than kMinRange (with 2, one
+// sequence of 777 tokens took 16.5 us instead of 15.6).
+constexpr int kMinRange = 1;
 __host__ __device__ __forceinline__ int plan_workers(long long total, int W) {
   const long long w = total / kMinRange;
   return w < 1 ? 1 : (w < W ? (int)w : W);

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
       const int tok = live ? row / H : 0, hd = live ? row - tok * H : 0;
       const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_lat) + (size_t)(c.q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs);
       const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_pe) + (size_t)(c.q.begin + tok) * p.qp_ts + (size_t)hd * p.qp_hs);
-#pragma unroll 1
+#pragma unroll 3
       for (int j = 0; j < 9; ++j) {  // the score-only blocks' columns, then this half's
         const uint4* src = j < 4 ? ql + ((half ^ 1) * 4 + j) * 8 : j == 4 ? qp : ql + (half * 4 + j - 5) * 8;
         uint4 v[8];
