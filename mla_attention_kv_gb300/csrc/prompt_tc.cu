@@ -216,9 +216,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         if (own) {
           const uint64_t bd = dk + ks * (kKBytes >> 4);
           const uint32_t d = tmem + (g_qk & 1) * 128;
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c)
 #pragma unroll
-          for (int k = 0; k < 12; ++k)
-            tc::mma_f16_ts(d, tmem + kTmQ + k * 8, bd + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), id_qk, k > 0);
+            for (int k = 0; k < 4; ++k)
+              tc::mma_f16_ts(d, tmem + kTmQ + c * 32 + k * 8, bd + c * (kBlock >> 4) + 2 * k, id_qk, c > 0 || k > 0);
           tc::commit(bar(&sh->sfull[g_qk & 1]));
           ++g_qk;
         }
@@ -237,9 +239,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
           tc::fence_after_sync();
           const uint64_t bd = dv + vs * (kVBytes >> 4);
           const uint32_t pa = tmem + (g_pv & 1) * 128;
-          tc::mma_f16_ts(tmem + kTmO, pa, bd, id_pv, !first);
-#pragma unroll
-          for (int k = 1; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, true);
+#pragma unroll 2
+          for (int k = 0; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, !first || k > 0);
           tc::commit(bar(&sh->pvdone));
           if (last) tc::commit(bar(&sh->olast));
           ++g_pv;
