@@ -369,7 +369,8 @@ mla_status mla_kv_prolog_run_noalloc(const mla_prolog_config* cfg, int b, int s,
  * contiguous.  The calls run on the device that was current in create.
  * One handle holds one workspace: calls of it on two streams (or in two
  * graphs that run at the same time) need a handle each; mla_latent_append
- * and mla_attn_prompt_run use only its status word and may overlap.  */
+ * and mla_attn_prompt_run use only its status word there and may overlap.
+ * On the host a handle serves one thread at a time.  */
 typedef struct mla_attn_config {
   int num_heads;    /* H query heads, 1 .. 1024                                        */
   int num_kv_heads; /* heads of k_nope / value in mla_attn_prompt_run; divides H; 0: H */

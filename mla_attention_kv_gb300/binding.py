@@ -485,7 +485,7 @@ class MLAAttention:
         """Element strides of a tensor of the handle's dtype whose last dimension is contiguous."""
         if t.dtype is self.dtype and t.shape == shape and t.get_device() == self.device:
             st = t.stride()
-            if st[-1] == 1 and max(st) <= _INT_MAX:
+            if st[-1] == 1 and st[0] <= _INT_MAX and st[1] <= _INT_MAX and st[-2] <= _INT_MAX:
                 return st
         return self._rows_checked(t, shape, name)
 

@@ -66,8 +66,7 @@ constexpr int kPagedMmaRows = 32;
 inline int paged_mma_workers(int rows, int num_sms) { return rows == 16 ? 2 * num_sms : num_sms; }  // CTAs that are resident
 cudaError_t paged_mma_prepare(bool bf16);  // kernel attributes, once per device
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
-// tcgen05 kernel: items of 128 query rows, two CTAs per worker; pages whose
-// size is a multiple of 8.
+// tcgen05 kernel: items of 128 query rows, two CTAs per worker.
 constexpr int kPagedTcRows = 128;
 struct PagedMaps {  // tensor maps of the last call's caches and what they were made from
   struct Key {

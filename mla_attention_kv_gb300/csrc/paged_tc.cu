@@ -28,7 +28,11 @@
 // Rescaling the output only when a maximum grew by more than 2^8: as in
 // prompt_tc.cu.
 //
-// Warps: 0-3 queries, softmax, results (a thread owns a row), 4 TMA, 5 MMA.
+// Page sizes that 8 does not divide: three warps copy row by row with
+// cp.async into the same layout (the swizzle done by hand).
+//
+// Warps: 0-3 queries, softmax, results (a thread owns a row), 4 TMA (or 4, 6
+// and 7 copies of rows), 5 MMA.
 #include <string.h>
 
 #include "attn.h"
@@ -39,7 +43,9 @@
 namespace mla {
 namespace {
 
-constexpr int kUtThreads = 192;
+// kBox: the page size is a multiple of 8 and keys come by TMA (one warp); else by cp.async (three warps).
+template <bool kBox> constexpr int kUtThreads = kBox ? 192 : 256;
+constexpr int kCopyWarps = 3;
 constexpr int kUtRows = kPagedTcRows;  // 128
 constexpr uint32_t kBlk = 8192;        // 64 keys x 64 columns
 constexpr int kNTiles = 1, kVTiles = 3;  // stages of the two rings
@@ -70,8 +76,8 @@ struct UtArgs {
   int box;  // rows per TMA box
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_constant__ UtArgs a) {
+template <typename T, bool kBox>
+__global__ void __launch_bounds__(kUtThreads<kBox>, 1) paged_tc_kernel(const __grid_constant__ UtArgs a) {
   using E = Elem<T>;
   const PagedParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -98,11 +104,11 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
 
   if (tid == 0) {
     for (int i = 0; i < kNTiles; ++i) {
-      mbar_init(bar(&sh->nfull[i]), 1);
+      mbar_init(bar(&sh->nfull[i]), kBox ? 1 : kCopyWarps);
       mbar_init(bar(&sh->nempty[i]), 1);
     }
     for (int i = 0; i < kVTiles; ++i) {
-      mbar_init(bar(&sh->vfull[i]), 1);
+      mbar_init(bar(&sh->vfull[i]), kBox ? 1 : kCopyWarps);
       mbar_init(bar(&sh->vempty[i]), 1);
     }
     mbar_init(bar(&sh->qready), 4);
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
     return keys;
   };
 
-  if (warp == 4) {
+  if (kBox && warp == 4) {
     // ============================================================ TMA
     const int box = a.box, nbox = kKeyTile / box;
     const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
@@ -199,6 +205,85 @@ __global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_co
       mbar_wait_bounded(bar(&sh->nfull[u % kNTiles]), (u / kNTiles) & 1, drain_budget(p.budget_ns));
     for (uint32_t u = uv > kVTiles ? uv - kVTiles : 0; u < uv; ++u)
       mbar_wait_bounded(bar(&sh->vfull[u % kVTiles]), (u / kVTiles) & 1, drain_budget(p.budget_ns));
+  } else if (!kBox && (warp == 4 || warp > 5)) {
+    // ============================================================ copies of single rows (any page size)
+    // A warp takes every third group of four keys; lanes 0-23 look up their cache rows.  Rows past the keys and of
+    // bad blocks are zeros.  The values of the next tile are under way while a tile is completed.
+    const int cw = warp == 4 ? 0 : warp - 5;
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t par) {
+      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
+      return ok;
+    };
+    uint32_t un = 0, uv = 0, av = 0;  // stages filled, value stages announced
+    PlanCursor c = first;
+    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kUtRows)) {
+      int t0, t1;
+      const int keys = span(c, &t0, &t1);
+      auto rows_of = [&](int tile) {
+        const int group = cw + kCopyWarps * (lane >> 2);
+        const int k = tile * kKeyTile + group * 4 + (lane & 3);
+        if (group >= kKeyTile / 4 || k >= keys || tile >= t1) return -1;
+        const int pg = k / p.page;
+        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
+        if (blk < 0 || blk >= p.nblocks) {
+          atomicOr(p.status, kStatusBadSlot);
+          return -1;
+        }
+        return blk * p.page + (k - pg * p.page);
+      };
+      // 64 columns x 4 blocks of every row, from block b0 of the latents: lane = 16-byte unit
+      auto copy = [&](int rows, uint32_t base, int b0) {
+        for (int i = 0; cw + kCopyWarps * i < kKeyTile / 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = __shfl_sync(~0u, rows, i * 4 + j);
+            const int r = (cw + kCopyWarps * i) * 4 + j;
+            const T* src = static_cast<const T*>(p.latent) + (size_t)max(row, 0) * p.lat_rs + b0 * 64 + lane * 8;
+            cp_async16(base + (lane >> 3) * kBlk + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src, row < 0 ? 0 : 16);
+          }
+      };
+      auto values = [&](int rows) {
+        const uint32_t s = uv % kVTiles;
+        if (!wait(&sh->vempty[s], ((uv / kVTiles) & 1) ^ 1)) return;
+        copy(rows, sbase + kUtV + s * kVBytes, half * 4);
+        cp_async_commit();
+        ++uv;
+      };
+      int row = rows_of(t0);
+      if (t0 < t1) values(row);
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int next = rows_of(t + 1);
+        const uint32_t n = un % kNTiles;
+        if (!wait(&sh->nempty[n], ((un / kNTiles) & 1) ^ 1)) break;
+        const uint32_t base = sbase + kUtN + n * kNBytes;
+        copy(row, base, (half ^ 1) * 4);
+        for (int i = 0; cw + kCopyWarps * i < kKeyTile / 4; ++i) {  // k_pe: eight lanes a row
+          const int kr = __shfl_sync(~0u, row, i * 4 + (lane >> 3));
+          const int r = (cw + kCopyWarps * i) * 4 + (lane >> 3);
+          const T* src = static_cast<const T*>(p.kpe) + (size_t)max(kr, 0) * p.kpe_rs + (lane & 7) * 8;
+          cp_async16(base + 4 * kBlk + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src, kr < 0 ? 0 : 16);
+        }
+        cp_async_commit();
+        ++un;
+        if (t + 1 < t1) {
+          values(next);
+          if (!ok) break;
+          cp_async_wait<1>();
+        } else {
+          cp_async_wait<0>();
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(&sh->nfull[n]));
+          mbar_arrive(bar(&sh->vfull[av % kVTiles]));
+        }
+        ++av;
+        row = next;
+      }
+    }
+    cp_async_wait<0>();
   } else if (warp == 5) {
     // ============================================================ MMA (one thread)
     if (tc::elect_one()) {
@@ -455,7 +540,7 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   PagedMaps::Key key;
   memset(&key, 0, sizeof(key));
   key.lat = p.latent; key.kpe = p.kpe; key.lat_rs = p.lat_rs; key.kpe_rs = p.kpe_rs; key.rows = p.nblocks * p.page; key.box = box;
-  if (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0) {
+  if (box >= 8 && (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0)) {
     m->valid = false;
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -466,15 +551,23 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   }
   UtArgs a;
   a.lat = m->lat; a.kpe = m->kpe; a.p = p; a.box = box;
-  paged_tc_kernel<T><<<p.workers * 2, kUtThreads, kUtSmem, stream>>>(a);
+  if (box >= 8)
+    paged_tc_kernel<T, true><<<p.workers * 2, kUtThreads<true>, kUtSmem, stream>>>(a);
+  else
+    paged_tc_kernel<T, false><<<p.workers * 2, kUtThreads<false>, kUtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t paged_tc_prepare(bool bf16) {
-  return bf16 ? cudaFuncSetAttribute(paged_tc_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem)
-              : cudaFuncSetAttribute(paged_tc_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
+  const void* k[2] = {bf16 ? (const void*)paged_tc_kernel<__nv_bfloat16, true> : (const void*)paged_tc_kernel<__half, true>,
+                      bf16 ? (const void*)paged_tc_kernel<__nv_bfloat16, false> : (const void*)paged_tc_kernel<__half, false>};
+  for (const void* f : k) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream) {

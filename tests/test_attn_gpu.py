@@ -474,6 +474,28 @@ def test_prompt_captured_and_repeated():
     check("out", out[0, :, :333].transpose(0, 1), ref, tol)
 
 
+def test_waits_are_bounded():
+    """With a wait limit of 1 ns a call may give up: it ends, reports it, and leaves nothing behind for other handles."""
+    c = Paged([1, 2, 1], [3000, 70, 500], 128, 16, "bf16", 21)
+    a = B.MLAAttention(config(128, "bf16"), c.T, spin_budget_ns=1)
+    c.run(a)
+    assert a.status() in (0, 6) and a.status() == 0
+    b = B.MLAAttention(config(128, "bf16"), c.T)
+    c.run(b)
+    assert b.status() == 0
+    c.check()
+    x, p = rnd(gen(1), 1, 4, 900, 128, dtype=torch.bfloat16), rnd(gen(2), 1, 4, 900, 64, dtype=torch.bfloat16)
+    out = torch.empty_like(x)
+    for budget in (1, 0):
+        h = B.MLAAttention(config(4, "bf16"), 900, spin_budget_ns=budget)
+        h.run_prompt(x, p, x, p[:, :1], x, out)
+        assert h.status() in ((0, 6) if budget else (0,))
+    k = torch.cat((x, p[:, :1].expand(1, 4, 900, 64)), -1)[0].double()
+    q = torch.cat((x, p), -1)[0].double().transpose(0, 1)
+    ref, _, tol, _ = attend(q, k, x[0].double(), 0, SCALE, torch.bfloat16)
+    check("out", out[0].transpose(0, 1), ref, tol)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("base", ["v2lite", "r1"])
 def test_prolog_append_and_attention_together(base):
