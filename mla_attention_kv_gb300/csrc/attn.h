@@ -78,7 +78,7 @@ struct PagedMaps {  // tensor maps of the last call's caches and what they were 
   CUtensorMap lat, kpe;
 };
 // Cache rows per TMA box: the largest power of two that divides the page, at
-// most a key tile; below 8 the 128-byte swizzle pattern would not fit.
+// most a key tile.
 inline int paged_tc_box(int page) {
   const int b = page & -page;
   return b > 64 ? 64 : b;

@@ -19,9 +19,9 @@
 // What bounds it is the latency of the way through a tile (scores, softmax
 // over the warps, output), so the work of a tile is spread over many warps:
 // 16-row items run two CTAs of 8 warps per SM on tiles of 32 keys, 32-row
-// items one CTA of 16 warps on tiles of 64 (one CTA of 8 warps with tiles of
-// 64 reached 2.5 TB/s on 64 sequences of up to 4096 keys, at 20 % of the
-// issue slots).
+// items one CTA of 16 warps on tiles of 64.  Decode of 64 sequences of up to
+// 4096 keys, 16 heads, bf16 (154 MB of cache): 53 us, 2.9 TB/s (one CTA of 8
+// warps with tiles of 64: 61 us; with tiles requested into L2 ahead: 58 us).
 #include "attn.h"
 #include "common.cuh"
 #include "paged_plan.cuh"

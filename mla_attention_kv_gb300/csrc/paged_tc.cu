@@ -9,16 +9,23 @@
 //
 // A 128 x 512 fp32 output alone would fill the 512 columns of tensor memory,
 // so two CTAs share an item: both compute the scores, each accumulates half
-// (256 columns) of the output.  That costs 1664 MMA cycles per 64 keys for
-// each CTA instead of 1088, and needs no exchange between them.  Tensor
-// memory: output [0, 256), scores of a 64-key tile [256, 320), the rounded
-// weights [320, 352), and 320 of the queries' 576 columns [352, 512) as the A
-// operand of their part of the scores; the other 256 stay in shared memory
-// (64 KB), which leaves 160 KB for keys.
+// (256 columns) of the output, without any exchange.  (Half of the scores'
+// columns each and an exchange of partial scores would save 35 % of the MMA
+// cycles, but 32 KB per tile each way take 1700 cycles through distributed
+// shared memory, measured at 19 bytes per cycle.)  Tensor memory: output
+// [0, 256), scores of a 64-key tile [256, 320), the rounded weights
+// [320, 352), and 320 of the queries' 576 columns [352, 512) as the A operand
+// of their part of the scores; the other 256 stay in shared memory (64 KB),
+// which leaves 160 KB for keys.
+//
+// What bounds it: a score step of 16 columns takes the tensor core 32 cycles
+// with A in tensor memory and 48 with A in shared memory, an output step of 16
+// keys 128, so a tile takes 20 * 32 + 16 * 48 + 4 * 128 = 1920; the kernel
+// takes 2420.  Decode of 64 sequences of up to 32768 keys, 128 heads, bf16
+// (1.15 GB of cache): 325 us, 3.5 TB/s.
 //
 // Keys: a tile is nine blocks of 64 keys x 64 columns (8 KB, 128-byte
-// swizzle) by TMA, in boxes of the largest power of two that divides the
-// page (8 to 64 rows).  Five blocks serve the scores alone and are released
+// swizzle) by TMA, in boxes of 32 or 64 rows of a page.  Five blocks serve the scores alone and are released
 // as soon as their MMAs are done (one stage); the four of this CTA's output
 // half are the B operand of both products (three stages).  Tiles are
 // requested into L2 four tiles ahead of their copies.
@@ -28,8 +35,8 @@
 // Rescaling the output only when a maximum grew by more than 2^8: as in
 // prompt_tc.cu.
 //
-// Page sizes that 8 does not divide: three warps copy row by row with
-// cp.async into the same layout (the swizzle done by hand).
+// Pages that such boxes do not fit: three warps copy row by row with cp.async
+// into the same layout (the swizzle done by hand).
 //
 // Warps: 0-3 queries, softmax, results (a thread owns a row), 4 TMA (or 4, 6
 // and 7 copies of rows), 5 MMA.
@@ -43,7 +50,11 @@
 namespace mla {
 namespace {
 
-// kBox: the page size is a multiple of 8 and keys come by TMA (one warp); else by cp.async (three warps).
+// kBox: keys come by TMA (one warp), where the page size is a multiple of
+// kTmaBox; else by cp.async (three warps).  64 sequences of up to 16384 keys,
+// 128 heads, bf16, TMA / cp.async: page 64 186 / 247 us, 32 208 / 248 us, 16
+// 264 / 250 us, 8 393 / 253 us.
+constexpr int kTmaBox = 32;
 template <bool kBox> constexpr int kUtThreads = kBox ? 192 : 256;
 constexpr int kCopyWarps = 3;
 constexpr int kUtRows = kPagedTcRows;  // 128
@@ -540,7 +551,7 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   PagedMaps::Key key;
   memset(&key, 0, sizeof(key));
   key.lat = p.latent; key.kpe = p.kpe; key.lat_rs = p.lat_rs; key.kpe_rs = p.kpe_rs; key.rows = p.nblocks * p.page; key.box = box;
-  if (box >= 8 && (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0)) {
+  if (box >= kTmaBox && (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0)) {
     m->valid = false;
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -551,7 +562,7 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   }
   UtArgs a;
   a.lat = m->lat; a.kpe = m->kpe; a.p = p; a.box = box;
-  if (box >= 8)
+  if (box >= kTmaBox)
     paged_tc_kernel<T, true><<<p.workers * 2, kUtThreads<true>, kUtSmem, stream>>>(a);
   else
     paged_tc_kernel<T, false><<<p.workers * 2, kUtThreads<false>, kUtSmem, stream>>>(a);

@@ -16,12 +16,21 @@
 //
 // Tensor memory: scores S0, S1 (128 columns each, by the parity of the key
 // tile; the rounded weights overwrite the first 64 columns of theirs and are
-// the A operand of the second product), output (128), queries (96). With both
-// A operands in tensor memory an MMA of 128 x 128 x 16 takes 74 cycles
-// (measured; 107 with A in shared memory, 64 by the peak rate), so a tile of
-// 128 keys takes 12 * 74 + 8 * 74 = 1480 cycles, and all of shared memory is
-// a ring of thirteen 16 KB slots for keys (three slots of 64 columns, 128
-// bytes a row, 128-byte swizzle) and values (two).
+// the A operand of the second product), output (128), queries (96).  With both
+// A operands in tensor memory an MMA of 128 x 128 x 16 takes 64 cycles, so a
+// tile of 128 keys needs 1280, and all of shared memory holds keys (three
+// stages of 48 KB: three blocks of 64 columns, 128 bytes a row, 128-byte
+// swizzle) and values (two stages of 32 KB).  One barrier per stage: a wait on
+// an mbarrier takes a thread about 100 cycles even when the phase is complete,
+// so finer slots cost more than they hide.
+//
+// What bounds it (one prompt of 8192, 128 heads, causal, bf16: 1.88 ms, 1.46
+// PFLOP/s): about 1810 cycles per tile and 13000 per item around its tiles,
+// the tensor pipe busy 58 % of the time.  A tile's way is scores, softmax,
+// weights announced, output, with two tiles in flight.  Measured and slower:
+// the pair on the 2-SM MMA (half the shared-memory traffic, but every
+// announcement crosses the CTAs) 1.99 ms; four softmax warps per 32 rows
+// 2.10 ms; tiles of 64 keys, four in flight, 2.10 ms.
 //
 // MMA order: scores of tile i + 1, then output of tile i, so the softmax of
 // a tile runs under the scores of the next and the output of the previous.
