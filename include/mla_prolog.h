@@ -488,7 +488,8 @@ typedef struct mla_attn_paged_args {
  * with p = softmax(scale * q . key), lse = ln sum_j exp(scale * q . key_j).
  * A row that sees none (L < n) gets zeros and -infinity.  Token rows of no
  * sequence are left as they were; cache rows past L are not used (they may
- * hold anything, NaN included).  Scores, maxima, sums and outputs are
+ * hold anything, NaN included), but all rows below L must be finite, those
+ * that only newer tokens see among them.  Scores, maxima, sums and outputs are
  * accumulated in fp32; the softmax weights are rounded to dtype for their
  * product with the latents.  Results do not depend on timing.
  * Two launches.  A block index outside [0, num_blocks) reads as a block of
@@ -530,8 +531,9 @@ typedef struct mla_attn_prompt_args {
  * Token i of a sequence sees the tokens j <= i of it (causal = 1) or all of
  * them (causal = 0): out = sum_j p_j value_j, p = softmax(scale *
  * (q_nope . k_nope_j + q_pe . k_pe_j)), lse as above.  Tokens of no sequence
- * are neither read nor written.  Arithmetic as for mla_attn_paged_run; values
- * must be finite within a sequence.  Offsets outside [0, s] or decreasing
+ * do not enter any result and are not written.  Arithmetic as for
+ * mla_attn_paged_run; values must be finite within a sequence, those of later
+ * tokens among them.  Offsets outside [0, s] or decreasing
  * are clamped and reported (MLA_ERR_BAD_LENGTH).  Errors as above; cu_seqlens
  * with b > 1 is MLA_ERR_INVALID_ARG. */
 mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cudaStream_t stream);
