@@ -226,9 +226,9 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   // (with ragged chunks the host knows only the average)
   const long long rows_per_seq = (long long)(a.T / a.num_seqs > 0 ? a.T / a.num_seqs : 1) * H;
-  // 32 rows or fewer: the kernel built around the key stream (64 sequences of up to 4096 keys with 16 heads: 53 us, the
+  // 32 rows or fewer: the kernel built around the key stream (64 sequences of up to 4096 keys with 16 heads: 48 us, the
   // tcgen05 kernel 92 us); more: one pass of the tcgen05 kernel for 128 rows (64 sequences of up to 32768 keys with 128
-  // heads: 331 us, four passes of the other 1344 us)
+  // heads: 325 us, four passes of the other 1344 us)
   const bool tc = rows_per_seq > kPagedMmaRows;
   const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
   p.workers = tc ? h->num_sms / 2 : paged_mma_workers(rows, h->num_sms);

@@ -20,8 +20,11 @@
 // over the warps, output), so the work of a tile is spread over many warps:
 // 16-row items run two CTAs of 8 warps per SM on tiles of 32 keys, 32-row
 // items one CTA of 16 warps on tiles of 64.  Decode of 64 sequences of up to
-// 4096 keys, 16 heads, bf16 (154 MB of cache): 53 us, 2.9 TB/s (one CTA of 8
-// warps with tiles of 64: 61 us; with tiles requested into L2 ahead: 58 us).
+// 4096 keys, 16 heads, fp16 (154 MB of cache): 47.7 us, 3.2 TB/s; 53 us when
+// the queries were read from shared memory for every tile and a page's number
+// checked where it is looked up (61 us with one CTA of 8 warps and tiles of
+// 64).  Per tile of a CTA 5200 cycles: 1200 scores, 600 softmax, 850 output,
+// 700 each for the issue of the next copies and for their arrival.
 #include "attn.h"
 #include "common.cuh"
 #include "paged_plan.cuh"
@@ -58,17 +61,25 @@ struct PmCfg {
   static_assert(TPR <= 32 && KPT * TPR == KT, "softmax threads");
 };
 
-// Row index (block * page + offset) of key k of sequence s in the cache, or
-// -1 where it has none.
-__device__ __forceinline__ int cache_row(const PagedParams& p, int s, int k, int keys) {
-  if (k >= keys) return -1;
+// Where key k of sequence s lies: its block table entry and the row in that
+// block (-1: there is no such key).  The entry is not looked at here, so that
+// its load runs on under other work.
+struct CachePlace {
+  int blk, off;
+};
+__device__ __forceinline__ CachePlace cache_place(const PagedParams& p, int s, int k, int keys) {
+  if (k >= keys) return {0, -1};
   const int pg = k / p.page;
-  const int blk = p.table[(size_t)s * p.table_stride + pg];
-  if (blk < 0 || blk >= p.nblocks) {
+  return {p.table[(size_t)s * p.table_stride + pg], k - pg * p.page};
+}
+// Its row index in the cache, or -1.
+__device__ __forceinline__ int cache_row(const PagedParams& p, const CachePlace& c) {
+  if (c.off < 0) return -1;
+  if (c.blk < 0 || c.blk >= p.nblocks) {
     atomicOr(p.status, kStatusBadSlot);
     return -1;
   }
-  return blk * p.page + (k - pg * p.page);
+  return c.blk * p.page + c.off;
 }
 
 template <typename T, int MT>
@@ -113,10 +124,11 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
     if (tid == 0 && c.hi >= x1) plan_post_join(p, c, R, w, x0, x1, total, W);
 
     // ---- key tiles: warp w copies rows 4w .. 4w + 3 of a stage
-    auto rows_of = [&](int tile) {  // lanes 0-3 hold their rows' cache rows
-      return lane < kRowsPerWarp ? cache_row(p, s, tile * KT + warp * kRowsPerWarp + lane, keys) : -1;
+    auto rows_of = [&](int tile) {  // lanes 0-3 look up their rows
+      return tile < t1 && lane < kRowsPerWarp ? cache_place(p, s, tile * KT + warp * kRowsPerWarp + lane, keys) : CachePlace{0, -1};
     };
-    auto load = [&](int tile, int rows) {
+    auto load = [&](int tile, const CachePlace& place) {
+      const int rows = cache_row(p, place);
       const uint32_t st = sb + S::kK + (tile & 1) * S::kStageBytes + warp * kRowsPerWarp * kPitch;
 #pragma unroll
       for (int r = 0; r < kRowsPerWarp; ++r) {
@@ -130,6 +142,7 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
       const T* src = static_cast<const T*>(p.kpe) + (size_t)max(row, 0) * p.kpe_rs;
       cp_async16(st + (lane >> 3) * kPitch + 1024 + (lane & 7) * 16, src + (lane & 7) * 8, row < 0 ? 0 : 16);
     };
+    const CachePlace place0 = rows_of(t0), place1 = rows_of(t0 + 1);
     __syncthreads();  // the previous item's stages and queries are read
     // ---- queries (rows past the end are zero), together with the first tile
     for (int r = warp; r < R; r += S::kWarps) {
@@ -142,9 +155,9 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
       cp_async16(d + 512 + lane * 16, ql + 256 + lane * 8, ok ? 16 : 0);
       if (lane < 8) cp_async16(d + 1024 + lane * 16, qp + lane * 8, ok ? 16 : 0);
     }
-    if (t0 < t1) load(t0, rows_of(t0));
+    if (t0 < t1) load(t0, place0);
     cp_async_commit();
-    if (t0 + 1 < t1) load(t0 + 1, rows_of(t0 + 1));
+    if (t0 + 1 < t1) load(t0 + 1, place1);
     cp_async_commit();
 
     float acc[MT][NT][4];
@@ -158,8 +171,21 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
     const int limit = srow < live ? q.keys_of_row(row0 + srow, H) : 0;
     float m_run = -INFINITY, l_run = 0.f;
 
+    // 16-row items: a warp's quarter of the queries stays in registers (32-row items would need 72 of a thread's 128)
+    constexpr int kSteps = kQkDim / 16 / kSplit;
+    const uint32_t qaddr = sb + S::kQ + (lane & 15) * kPitch + warp / (KT / 16) * 288 + (lane >> 4) * 16;
+    uint32_t qf[MT == 1 ? kSteps : 1][4];
+    if (MT == 1 && t0 < t1) {
+      cp_async_wait<1>();
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t* f = qf[MT == 1 ? k : 0];
+        ldsm_x4(qaddr + k * 32, f[0], f[1], f[2], f[3]);
+      }
+    }
     for (int tile = t0; tile < t1; ++tile) {
-      const int rows_next = tile + 2 < t1 ? rows_of(tile + 2) : -1;
+      const CachePlace place = rows_of(tile + 2);
       cp_async_wait<1>();
       __syncthreads();
       const uint32_t st = sb + S::kK + (tile & 1) * S::kStageBytes;
@@ -173,15 +199,19 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[m][n][i] = 0.f;
         const uint32_t kaddr = st + (kg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kPitch + kq * 288 + ((lane >> 3) & 1) * 16;
-        const uint32_t qaddr = sb + S::kQ + (lane & 15) * kPitch + kq * 288 + (lane >> 4) * 16;
 #pragma unroll
-        for (int k = 0; k < kQkDim / 16 / kSplit; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
           uint32_t b0, b1, b2, b3;
           ldsm_x4(kaddr + k * 32, b0, b1, b2, b3);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             uint32_t af[4];
-            ldsm_x4(qaddr + m * 16 * kPitch + k * 32, af[0], af[1], af[2], af[3]);
+            if (MT == 1) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) af[i] = qf[MT == 1 ? k : 0][i];
+            } else {
+              ldsm_x4(qaddr + m * 16 * kPitch + k * 32, af[0], af[1], af[2], af[3]);
+            }
             mma16816<E::kBf16>(sc[m][0], af, b0, b1);
             mma16816<E::kBf16>(sc[m][1], af, b2, b3);
           }
@@ -259,7 +289,7 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
         }
       }
       __syncthreads();  // the stage is free
-      if (tile + 2 < t1) load(tile + 2, rows_next);
+      if (tile + 2 < t1) load(tile + 2, place);
       cp_async_commit();
     }
     cp_async_wait<0>();
