@@ -114,6 +114,7 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   const bool bf16 = c.dtype == MLA_BF16;
   e = paged_mma_prepare(bf16);
   if (e == cudaSuccess) e = paged_tc_prepare(bf16);
+  if (e == cudaSuccess) e = paged_pair_prepare(bf16);
   if (e == cudaSuccess) e = prompt_tc_prepare(bf16);
   if (e != cudaSuccess) {
     cudaFree(h->ws);
@@ -232,7 +233,9 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   const bool tc = rows_per_seq > kPagedMmaRows;
   const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
   p.workers = tc ? h->num_sms / 2 : paged_mma_workers(rows, h->num_sms);
-  cudaError_t e = tc ? paged_tc_launch(bf16, p, &h->paged_maps, stream) : paged_mma_launch(bf16, p, rows, stream);
+  cudaError_t e = !tc                            ? paged_mma_launch(bf16, p, rows, stream)
+                  : a.page_size % kPagedBox == 0 ? paged_pair_launch(bf16, p, &h->paged_maps, stream)
+                                                 : paged_tc_launch(bf16, p, stream);
   if (e != cudaSuccess) return fail(e, "paged attention launch");
   e = paged_combine_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention combine launch");

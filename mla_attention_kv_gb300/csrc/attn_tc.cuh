@@ -12,12 +12,14 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_syn
 
 // Bounded mbarrier wait shared by all roles of a CTA; gives up on the time
 // budget or when another role has already given up.
+// kCluster: some arrivals come from the other CTA of the cluster.
+template <bool kCluster = false>
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                         unsigned long long budget, unsigned* status) {
   // (the timer is read only after some tries: reading it costs about as much as a wait usually takes)
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kCluster ? tc::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if ((n & 63) == 0) {
       if (*abort) return false;
       const uint64_t t = globaltimer_ns();

@@ -1,0 +1,538 @@
+// paged_pair.cu -- attention of new tokens over the paged latent cache, for
+// items of 128 query rows and pages of whole 32-row boxes, on the 2-SM MMA
+// (tcgen05.mma.cta_group::2, M = 128) / TMEM / TMA.
+//
+// The mathematics is that of paged_mma.cu: per query row (a token and a
+// head; q = [q_latent | q_pe], 576 wide) softmax(scale * q . key) over the
+// cached rows, times the rows' first 512 columns, in one pass with a running
+// maximum and sum; the weights are rounded to the I/O dtype as the A operand
+// of the product with the latents.
+//
+// The two CTAs of a cluster take 64 rows of an item each.  With M = 128 over
+// the pair a CTA's tensor memory holds its 64 rows of an N-column result in
+// 128 lanes x N / 2 columns (lanes 64-127: the upper half of the columns), so
+// the whole 64 x 512 fp32 output takes 256 columns, scores of a tile of 128
+// keys 64 (two buffers), and nothing is computed twice.  As the B operand
+// each CTA holds its half of the keys for the scores (64 keys x 576 columns)
+// and its half of the columns of all keys for the output (128 keys x 256).
+//
+// Shared memory: queries 72 KB, weights 16 KB, keys 72 KB (three slots of
+// three 64-column blocks), values 64 KB (four slots of 32 keys); one tile of
+// each, refilled slot by slot behind the MMAs.  All with the 128-byte
+// swizzle.  Tiles are requested into L2 two ahead of their copies.  MMA order:
+// scores of tile t + 1, then output of tile t, so the softmax of a tile runs
+// under the output of the one before.  Cycles of a tile: 36 score steps of 32
+// and 16 output MMAs of 64, 2180 measured alone.
+// @FIG@
+//
+// Rescaling the output only when a maximum grew by more than 2^8: as in
+// prompt_tc.cu.
+//
+// Warps: 0-3 queries, softmax, results (a row belongs to two threads, 64 keys
+// of a tile each: warps w and w + 2), 4 key copies, 5 MMA (the even CTA's,
+// for both), 6 value copies.  The copies of both CTAs are counted on the even
+// CTA's barriers.  The values of the last tile of a sequence are awaited by
+// each CTA itself, which zeroes their rows past the keys (they may hold
+// anything) before it announces its weights.
+#include <string.h>
+
+#include "attn.h"
+#include "attn_tc.cuh"
+#include "paged_plan.cuh"
+#include "tma.h"
+
+namespace mla {
+namespace {
+
+constexpr int kPpThreads = 224;
+constexpr int kPpRows = kPagedTcRows;  // 128 per pair
+constexpr int kPpKeys = 128;           // keys of a tile
+constexpr int kBox = kPagedBox;        // cache rows per copy
+constexpr int kAhead = 2;
+constexpr uint32_t kBlk = 8192;  // 64 rows x 64 columns
+constexpr int kKSlots = 3, kVSlots = 4;
+constexpr uint32_t kKSlot = 3 * kBlk, kVSlot = 2 * kBlk;
+constexpr uint32_t kPpQ = 0, kPpP = kPpQ + 9 * kBlk, kPpK = kPpP + 2 * kBlk, kPpV = kPpK + kKSlots * kKSlot,
+                   kPpBar = kPpV + kVSlots * kVSlot, kPpSmem = kPpBar + 2048 + 1024;  // + alignment slack
+static_assert(kPpSmem <= 232448, "shared memory of one CTA");
+static_assert(sizeof(PlanShared) <= kKSlots * kKSlot, "the plan is made in the key slots before any copy");
+constexpr uint32_t kTmS = 256;  // tensor memory columns: output at 0, scores at 256 and 320
+constexpr float kRescale = 8.0f;
+
+struct PpShared {
+  uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
+  uint64_t sfull[2], qready, pfull, pvdone, vtail, done, pair[2];
+  float row[2][2][64];  // exchange between the two threads of a row: [parity of the meeting][half][row]
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(PpShared) <= 2048, "barrier block");
+
+struct PpArgs {
+  CUtensorMap lat, kpe, lat_wide;
+  PagedParams p;
+};
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged_pair_kernel(const __grid_constant__ PpArgs a) {
+  using E = Elem<T>;
+  const PagedParams& p = a.p;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  PpShared* sh = reinterpret_cast<PpShared*>(smem + kPpBar);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int H = p.heads;
+  volatile int* abort = &sh->abort;
+  auto bar = [](uint64_t* b) { return smem_u32(b); };
+  const int rank = blockIdx.x & 1, w = blockIdx.x >> 1;  // (clusters are pairs of neighbours along x)
+
+  PlanShared* plan = reinterpret_cast<PlanShared*>(smem + kPpK);
+  grid_dep_launch_dependents();  // (the joining kernel may take its place)
+  const long long total = plan_total(p, plan, kPpRows, blockIdx.x == 0);
+  const int W = total > 0 ? plan_workers(total, p.workers) : 0;
+  if (w >= W) {
+    if (tid == 0) p.joins[w].rows = 0;
+    return;
+  }
+  const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
+  PlanCursor first;
+  first.seek(p, plan, kPpRows, x0);
+
+  if (tid == 0) {
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(bar(&sh->kfull[i]), 1);
+      mbar_init(bar(&sh->kempty[i]), 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(bar(&sh->vfull[i]), 1);
+      mbar_init(bar(&sh->vempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(&sh->sfull[i]), 1);
+      mbar_init(bar(&sh->pair[i]), 2);
+    }
+    mbar_init(bar(&sh->qready), 8);  // the softmax warps of both CTAs
+    mbar_init(bar(&sh->pfull), 8);
+    mbar_init(bar(&sh->pvdone), 1);
+    mbar_init(bar(&sh->vtail), 1);
+    mbar_init(bar(&sh->done), 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tc::tmem_alloc2(smem_u32(&sh->tmem), 512);
+  // (the plan has been read: its place becomes key slots)
+  tc::fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers are initialised before any copy, commit or arrival reaches them
+  tc::fence_after_sync();
+  const uint32_t tmem = uniform(sh->tmem);
+
+  // the tiles [t0, t1) of an item that fall to this worker
+  auto span = [&](const PlanCursor& c, int* t0, int* t1) {
+    const int keys = c.q.keys_of_item(c.j, kPpRows, H);
+    const int tiles = (keys + kPpKeys - 1) / kPpKeys;
+    *t0 = c.tile_at(x0 > c.lo ? x0 : c.lo, tiles);
+    *t1 = c.tile_at(x1 < c.hi ? x1 : c.hi, tiles);
+    return keys;
+  };
+
+  if (warp == 4 || warp == 6) {
+    // ============================================================ copies
+    const bool values = warp == 6;
+    const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
+    uint32_t u = 0, tails = 0;                // tiles copied, last tiles of sequences among them
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t par) {
+      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
+      return ok;
+    };
+    auto lead = [&](uint64_t* b) { return tc::mapa(bar(b), 0); };  // of the even CTA
+    PlanCursor c = first;
+    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
+      int t0, t1;
+      const int keys = span(c, &t0, &t1);
+      // lane l < 4 holds the cache row of the l-th 32 keys of a tile (-1: past the keys)
+      auto rows_of = [&](int tile) {
+        const int k = tile * kPpKeys + lane * kBox;
+        if (lane >= kPpKeys / kBox || tile >= t1 || k >= keys) return -1;
+        const int pg = k / p.page;
+        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
+        if (blk < 0 || blk >= p.nblocks) {
+          atomicOr(p.status, kStatusBadSlot);
+          return zero_row;
+        }
+        return blk * p.page + (k - pg * p.page);
+      };
+      const bool own = lane >> 1 == rank;  // this CTA's half of the keys
+      auto request = [&](int row) {
+        if (values || !own || row < 0 || row >= zero_row) return;
+        tma_prefetch_2d(&a.lat_wide, 0, row);
+        tma_prefetch_2d(&a.lat_wide, 256, row);
+        tma_prefetch_2d(&a.kpe, 0, row);
+      };
+      int row = t0 < t1 ? rows_of(t0) : -1;
+      for (int t = t0 + 1; t < t0 + kAhead; ++t) request(rows_of(t));
+      for (int t = t0; t < t1 && ok; ++t, ++u) {
+        if (!values) request(rows_of(t + kAhead));
+        const int next = rows_of(t + 1);
+        const uint32_t boxes = __popc(__ballot_sync(~0u, row >= 0));
+        if (!values) {
+          for (int g = 0; g < kKSlots; ++g) {
+            if (!wait(&sh->kempty[g], (u & 1) ^ 1)) break;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(&sh->kfull[g]), boxes * kBox * 128 * 3);
+            __syncwarp();
+            if (own && row >= 0) {
+              const uint32_t d = sbase + kPpK + g * kKSlot + (lane & 1) * (kBlk / 2), b = lead(&sh->kfull[g]);
+#pragma unroll
+              for (int j = 0; j < 3; ++j) {
+                const int blk = 3 * g + j;
+                tma_load_2d_pair(d + j * kBlk, blk < 8 ? &a.lat : &a.kpe, blk < 8 ? blk * 64 : 0, row, b);
+              }
+            }
+          }
+        } else {
+          const bool tail = keys - t * kPpKeys < kPpKeys;
+          for (int s = 0; s < kVSlots; ++s) {
+            if (!wait(&sh->vempty[s], (u & 1) ^ 1)) break;
+            if (rank == 0 && lane == 0) {
+              if (tail)
+                mbar_arrive(bar(&sh->vfull[s]));
+              else
+                mbar_arrive_expect_tx(bar(&sh->vfull[s]), 2 * kVSlot);
+            }
+            __syncwarp();
+            if (lane == s && row >= 0) {
+              const uint32_t d = sbase + kPpV + s * kVSlot, b = tail ? bar(&sh->vtail) : lead(&sh->vfull[s]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int x = ((j >> 1) * 4 + rank * 2 + (j & 1)) * 64;
+                if (tail)
+                  tma_load_2d(d + j * (kBlk / 2), &a.lat, x, row, b);
+                else
+                  tma_load_2d_pair(d + j * (kBlk / 2), &a.lat, x, row, b);
+              }
+            }
+          }
+          if (tail && ok) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(&sh->vtail), boxes * kVSlot);
+            ++tails;
+          }
+        }
+        row = next;
+      }
+    }
+    // every copy has landed, and every release of a slot has arrived, before the CTAs may exit
+    __syncwarp();
+    const uint64_t t0 = globaltimer_ns();
+    auto drain = [&](uint64_t* b, uint32_t par) {
+      const uint64_t spent = globaltimer_ns() - t0, limit = drain_budget(p.budget_ns);
+      mbar_wait_bounded(bar(b), par, spent < limit ? limit - spent : 0);
+    };
+    if (u > 0) {
+      for (int i = 0; i < (values ? kVSlots : kKSlots); ++i) {
+        if (rank == 0) drain(values ? &sh->vfull[i] : &sh->kfull[i], (u - 1) & 1);
+        drain(values ? &sh->vempty[i] : &sh->kempty[i], (u - 1) & 1);
+      }
+      if (tails > 0) drain(&sh->vtail, (tails - 1) & 1);
+    }
+  } else if (warp == 5) {
+    // ============================================================ MMA (one thread of the even CTA)
+    if (rank == 0 && tc::elect_one()) {
+      const uint32_t id_qk = tc::idesc_f16(E::kBf16, 128, 128, false, false);
+      const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 256, false, true);
+      const uint64_t dq = tc::sdesc_sw128(sbase + kPpQ, 16, 1024), dk = tc::sdesc_sw128(sbase + kPpK, 16, 1024);
+      const uint64_t dp = tc::sdesc_sw128(sbase + kPpP, 16, 1024), dv = tc::sdesc_sw128(sbase + kPpV, kBlk / 2, 1024);
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        ok = ok && at_wait<true>(bar(b), par, abort, p.budget_ns, p.status);
+        return ok;
+      };
+      uint32_t g_qk = 0, g_pv = 0, item = 0;
+      auto qk = [&]() {  // scores of tile g_qk
+        const uint32_t d = tmem + kTmS + (g_qk & 1) * 64;
+#pragma unroll 1
+        for (int g = 0; g < kKSlots; ++g) {
+          if (!wait(&sh->kfull[g], g_qk & 1)) return;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < 12; ++k) {
+            const uint32_t o = (k >> 2) * (kBlk >> 4) + 2 * (k & 3);
+            tc::mma2_f16(d, dq + g * (kKSlot >> 4) + o, dk + g * (kKSlot >> 4) + o, id_qk, g > 0 || k > 0);
+          }
+          tc::commit2_both(bar(&sh->kempty[g]));
+        }
+        tc::commit2_both(bar(&sh->sfull[g_qk & 1]));
+        ++g_qk;
+      };
+      auto pv = [&](bool first_tile) {  // output of tile g_pv
+        if (!wait(&sh->pfull, g_pv & 1)) return;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int s = 0; s < kVSlots; ++s) {
+          if (!wait(&sh->vfull[s], g_pv & 1)) return;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              tc::mma2_f16(tmem + j * 128, dp + (s >> 1) * (kBlk >> 4) + 4 * (s & 1) + 2 * k,
+                           dv + s * (kVSlot >> 4) + k * 128 + j * (kBlk >> 4), id_pv, !first_tile || s > 0 || k > 0);
+          tc::commit2_both(bar(&sh->vempty[s]));
+        }
+        tc::commit2_both(bar(&sh->pvdone));
+        ++g_pv;
+      };
+      PlanCursor c = first;
+      for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
+        int t0, t1;
+        span(c, &t0, &t1);
+        if (t0 >= t1) continue;
+        if (!wait(&sh->qready, item++ & 1)) break;
+        tc::fence_after_sync();
+        qk();
+        for (int t = t0; t < t1 && ok; ++t) {
+          if (t + 1 < t1) qk();
+          if (ok) pv(t == t0);
+        }
+      }
+      tc::commit2_both(bar(&sh->done));
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ queries, softmax, results
+    const int r = tid & 63, hf = tid >> 6;  // row of this CTA's 64, half of a tile's keys
+    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+    const float scale = p.scale_log2;
+    uint32_t g = 0, tails = 0, meets = 0;  // tiles done, last tiles of sequences among them
+    bool ok = true;
+    auto announce = [&](uint64_t* b) {  // to the MMA thread
+      __syncwarp();
+      if (lane == 0) tc::arrive_cluster(tc::mapa(bar(b), 0));
+    };
+    auto meet = [&]() {  // the two warps of these rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh->pair[warp & 1]));
+      return at_wait_warp(bar(&sh->pair[warp & 1]), meets++ & 1, abort, p.budget_ns, p.status);
+    };
+    auto load_q = [&](const PlanCursor& c) {  // the first five of the nine blocks, or the others
+      const int row = c.j * kPpRows + rank * 64 + r;
+      const bool live = row < c.q.n * H;
+      const int tok = live ? row / H : 0, hd = live ? row - tok * H : 0;
+      const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_lat) + (size_t)(c.q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs);
+      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_pe) + (size_t)(c.q.begin + tok) * p.qp_ts + (size_t)hd * p.qp_hs);
+      const int end = hf ? 9 : 5;
+#pragma unroll 2
+      for (int j = hf ? 5 : 0; j < end; ++j) {
+        const uint4* src = j < 8 ? ql + j * 8 : qp;
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + kPpQ + j * kBlk + r * 128 + ((i ^ (r & 7)) * 16)) = v[i];
+      }
+      tc::fence_proxy_async_smem();
+      announce(&sh->qready);
+    };
+    PlanCursor c = first;
+    {
+      int t0, t1;
+      span(c, &t0, &t1);
+      if (t0 < t1) load_q(c);
+    }
+    for (bool more = true; more && c.lo < x1 && ok;) {
+      int t0, t1;
+      const int keys = span(c, &t0, &t1);
+      if (tid == 0 && rank == 0 && c.hi >= x1) plan_post_join(p, c, kPpRows, w, x0, x1, total, W);
+      const int row = c.j * kPpRows + rank * 64 + r;
+      const bool live = row < c.q.n * H;
+      const int limit0 = (live ? c.q.keys_of_row(row, H) : 0) - hf * 64;
+      const bool whole = c.lo >= x0 && c.hi <= x1;
+      const size_t grow = (size_t)c.q.begin * H + row;
+      const size_t slot = (size_t)w * 2 + (c.lo < x0 ? 0 : 1);
+      float m = -INFINITY, l = 0.f;  // maximum of the row, sum over this thread's keys
+      for (int t = t0; t < t1; ++t, ++g) {
+        const uint32_t ts = tl + kTmS + (g & 1) * 64;
+        if (!at_wait_warp(bar(&sh->sfull[g & 1]), (g >> 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+        tc::fence_after_sync();
+        uint32_t s[64];
+        tc::ld32(ts, s);
+        tc::ld32(ts + 32, s + 32);
+        tc::wait_ld();
+        const int limit = limit0 - t * kPpKeys;
+        if (__any_sync(~0u, limit < 64)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= limit) s[k] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
+#pragma unroll
+        for (int k = 4; k < 60; k += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + j + 4]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[60 + j]));
+        float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const uint32_t par = meets & 1;
+        sh->row[par][hf][r] = tile_max;
+        if (!meet()) { ok = false; break; }
+        tile_max = fmaxf(tile_max, sh->row[par][hf ^ 1][r]);
+        float f = 1.f;
+        const bool grow_max = __any_sync(~0u, (tile_max - m) * scale > kRescale);  // (both warps of the rows alike)
+        if (grow_max) {
+          const float m_new = fmaxf(m, tile_max);
+          f = m == -INFINITY ? 0.f : ex2((m - m_new) * scale);
+          l *= f;
+          m = m_new;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = f2_pack(scale, scale), ng2 = f2_pack(-mu * scale, -mu * scale);
+        uint64_t sum[2] = {0, 0};
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2, ng2);
+          float y0, y1;
+          f2_unpack(x, y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          sum[k & 1] = f2_add(sum[k & 1], f2_pack(y0, y1));
+          pk[k] = E::pack(y0, y1);
+        }
+        float a0, a1, b0, b1;
+        f2_unpack(sum[0], a0, a1);
+        f2_unpack(sum[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
+        // the previous tile's output MMA has read the weights and left the output at rest
+        if (g > 0 && !at_wait_warp(bar(&sh->pvdone), (g - 1) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+        tc::fence_after_sync();
+        if (grow_max && t > t0) {
+          tmem_scale<256>(tl, f);
+          tc::wait_st();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + kPpP + hf * kBlk + r * 128 + ((i ^ (r & 7)) * 16)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        const int valid = keys - t * kPpKeys;
+        if (valid < kPpKeys) {
+          // latents past the keys: whole 128-byte rows, so the swizzle does not matter
+          if (!at_wait_warp(bar(&sh->vtail), tails++ & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+          for (int x = tid; x < (kPpKeys - valid) * 32; x += 128) {
+            const int k = valid + (x >> 5);
+            *reinterpret_cast<uint4*>(smem + kPpV + (k >> 5) * kVSlot + ((x >> 3) & 3) * (kBlk / 2) + (k & 31) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::fence_before_sync();
+        announce(&sh->pfull);
+      }
+      if (!ok) break;
+      // the next item's queries go in while the last output MMA runs (all score MMAs of this one are done)
+      more = c.next(p, kPpRows);
+      if (more && c.lo < x1) {
+        int u0, u1;
+        span(c, &u0, &u1);
+        if (u0 < u1) load_q(c);
+      }
+      if (t0 < t1) {
+        const uint32_t par = meets & 1;
+        sh->row[par][hf][r] = l;
+        ok = meet() && at_wait_warp(bar(&sh->pvdone), (g - 1) & 1, abort, p.budget_ns, p.status);
+        if (!ok) break;
+        tc::fence_after_sync();
+        l = sh->row[par][0][r] + sh->row[par][1][r];
+      }
+      // this thread's columns: 128 hf .. 128 hf + 127 of either half of the output
+      const float iv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      T* out = static_cast<T*>(p.out) + (live ? grow : 0) * kRank + hf * 128;
+      float* po = p.part_o + (slot * kPpRows + rank * 64 + r) * kRank + hf * 128;
+      if (t0 < t1) {
+#pragma unroll 1
+        for (int cc = 0; cc < 256; cc += 32) {
+          uint32_t o[32];
+          tc::ld32(tl + cc, o);
+          tc::wait_ld();
+          if (!live) continue;
+          const int col = (cc >> 7) * 256 + (cc & 127);
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t q[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                q[j] = E::pack(__uint_as_float(o[k + 2 * j]) * iv, __uint_as_float(o[k + 2 * j + 1]) * iv);
+              *reinterpret_cast<uint4*>(out + col + k) = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(po + col + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        tc::fence_before_sync();
+      } else if (whole && live) {  // no key at all
+        for (int cc = 0; cc < 256; cc += 8)
+          *reinterpret_cast<uint4*>(out + (cc >> 7) * 256 + (cc & 127)) = make_uint4(0, 0, 0, 0);
+      }
+      if (hf == 0 && live) {
+        if (!whole) {
+          float* ml = p.part_ml + (slot * kPpRows + rank * 64 + r) * 2;
+          ml[0] = m * scale;
+          ml[1] = l;
+        } else if (p.lse) {
+          p.lse[grow] = l == 0.f ? -INFINITY : (m * scale + log2f(l)) * kLn2;
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));  // every MMA issued has completed
+  // neither CTA leaves, or releases the pair's tensor memory, while its peer may still copy into it, read it, or arrive
+  // on its barriers
+  tc::cluster_sync();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc2(tmem, 512);
+  }
+}
+
+template <typename T>
+cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
+  PagedMaps::Key key;
+  memset(&key, 0, sizeof(key));
+  key.lat = p.latent; key.kpe = p.kpe; key.lat_rs = p.lat_rs; key.kpe_rs = p.kpe_rs; key.rows = p.nblocks * p.page;
+  if (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0) {
+    m->valid = false;
+    const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&m->lat_wide, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 256, kBox, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+    m->key = key;
+    m->valid = true;
+  }
+  PpArgs a;
+  a.lat = m->lat; a.kpe = m->kpe; a.lat_wide = m->lat_wide; a.p = p;
+  paged_pair_kernel<T><<<p.workers * 2, kPpThreads, kPpSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t paged_pair_prepare(bool bf16) {
+  return bf16 ? cudaFuncSetAttribute(paged_pair_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem)
+              : cudaFuncSetAttribute(paged_pair_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+}
+
+cudaError_t paged_pair_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream) {
+  return bf16 ? launch<__nv_bfloat16>(p, maps, stream) : launch<__half>(p, maps, stream);
+}
+
+}  // namespace mla

@@ -40,27 +40,18 @@
 //
 // Warps: 0-3 queries, softmax, results (a thread owns a row), 4 TMA (or 4, 6
 // and 7 copies of rows), 5 MMA.
-#include <string.h>
-
 #include "attn.h"
 #include "attn_tc.cuh"
 #include "paged_plan.cuh"
-#include "tma.h"
 
 namespace mla {
 namespace {
 
-// kBox: keys come by TMA (one warp), where the page size is a multiple of
-// kTmaBox; else by cp.async (three warps).  64 sequences of up to 16384 keys,
-// 128 heads, bf16, TMA / cp.async: page 64 186 / 247 us, 32 208 / 248 us, 16
-// 264 / 250 us, 8 393 / 253 us.
-constexpr int kTmaBox = 32;
-template <bool kBox> constexpr int kUtThreads = kBox ? 192 : 256;
+constexpr int kUtThreads = 256;
 constexpr int kCopyWarps = 3;
 constexpr int kUtRows = kPagedTcRows;  // 128
 constexpr uint32_t kBlk = 8192;        // 64 keys x 64 columns
 constexpr int kNTiles = 1, kVTiles = 3;  // stages of the two rings
-constexpr int kAhead = 4;                // key tiles requested into L2 ahead of their copies
 constexpr uint32_t kNBytes = 5 * kBlk, kVBytes = 4 * kBlk;
 constexpr uint32_t kUtQ = 0;                              // 4 chunks of [128 x 64]
 constexpr uint32_t kUtV = kUtQ + 4 * 16384;               // [kVTiles][4] blocks
@@ -81,16 +72,9 @@ struct UtShared {
 };
 static_assert(sizeof(UtShared) <= 512, "barrier block");
 
-struct UtArgs {
-  CUtensorMap lat, kpe;
-  PagedParams p;
-  int box;  // rows per TMA box
-};
-
-template <typename T, bool kBox>
-__global__ void __launch_bounds__(kUtThreads<kBox>, 1) paged_tc_kernel(const __grid_constant__ UtArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kUtThreads, 1) paged_tc_kernel(const __grid_constant__ PagedParams p) {
   using E = Elem<T>;
-  const PagedParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   UtShared* sh = reinterpret_cast<UtShared*>(smem + kUtBar);
@@ -115,11 +99,11 @@ __global__ void __launch_bounds__(kUtThreads<kBox>, 1) paged_tc_kernel(const __g
 
   if (tid == 0) {
     for (int i = 0; i < kNTiles; ++i) {
-      mbar_init(bar(&sh->nfull[i]), kBox ? 1 : kCopyWarps);
+      mbar_init(bar(&sh->nfull[i]), kCopyWarps);
       mbar_init(bar(&sh->nempty[i]), 1);
     }
     for (int i = 0; i < kVTiles; ++i) {
-      mbar_init(bar(&sh->vfull[i]), kBox ? 1 : kCopyWarps);
+      mbar_init(bar(&sh->vfull[i]), kCopyWarps);
       mbar_init(bar(&sh->vempty[i]), 1);
     }
     mbar_init(bar(&sh->qready), 4);
@@ -149,75 +133,8 @@ __global__ void __launch_bounds__(kUtThreads<kBox>, 1) paged_tc_kernel(const __g
     return keys;
   };
 
-  if (kBox && warp == 4) {
-    // ============================================================ TMA
-    const int box = a.box, nbox = kKeyTile / box;
-    const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
-    uint32_t un = 0, uv = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t par) {
-      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
-      return ok;
-    };
-    PlanCursor c = first;
-    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kUtRows)) {
-      int t0, t1;
-      const int keys = span(c, &t0, &t1);
-      // lane l holds the cache row of box l of the next tile (-1: past the keys)
-      auto rows_of = [&](int tile) {
-        const int k = tile * kKeyTile + lane * box;
-        if (lane >= nbox || k >= keys || tile >= t1) return -1;
-        const int pg = k / p.page;
-        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
-        if (blk < 0 || blk >= p.nblocks) {
-          atomicOr(p.status, kStatusBadSlot);
-          return zero_row;
-        }
-        return blk * p.page + (k - pg * p.page);
-      };
-      // (both CTAs copy every row; each requests its own half of the columns)
-      auto request = [&](int r) {
-        if (r < 0 || r >= zero_row) return;
-        for (int j = 0; j < 4; ++j) tma_prefetch_2d(&a.lat, (half * 4 + j) * 64, r);
-        if (half) tma_prefetch_2d(&a.kpe, 0, r);
-      };
-      int row = t0 < t1 ? rows_of(t0) : -1;
-      for (int t = t0 + 1; t < t0 + kAhead; ++t) request(rows_of(t));
-      int far = rows_of(t0 + kAhead);
-      for (int t = t0; t < t1 && ok; ++t) {
-        request(far);
-        far = rows_of(t + 1 + kAhead);
-        const int next = rows_of(t + 1);
-        const uint32_t boxes = __popc(__ballot_sync(~0u, row >= 0));
-        const uint32_t n = un % kNTiles;
-        if (!wait(&sh->nempty[n], ((un / kNTiles) & 1) ^ 1)) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(&sh->nfull[n]), boxes * box * 640);
-        __syncwarp();
-        if (row >= 0) {
-          const uint32_t d = sbase + kUtN + n * kNBytes + lane * box * 128;
-          for (int j = 0; j < 4; ++j) tma_load_2d(d + j * kBlk, &a.lat, ((half ^ 1) * 4 + j) * 64, row, bar(&sh->nfull[n]));
-          tma_load_2d(d + 4 * kBlk, &a.kpe, 0, row, bar(&sh->nfull[n]));
-        }
-        ++un;
-        const uint32_t s = uv % kVTiles;
-        if (!wait(&sh->vempty[s], ((uv / kVTiles) & 1) ^ 1)) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(&sh->vfull[s]), boxes * box * 512);
-        __syncwarp();
-        if (row >= 0)
-          for (int j = 0; j < 4; ++j)
-            tma_load_2d(sbase + kUtV + s * kVBytes + j * kBlk + lane * box * 128, &a.lat, (half * 4 + j) * 64, row, bar(&sh->vfull[s]));
-        ++uv;
-        row = next;
-      }
-    }
-    // every issued copy has landed before the CTA may exit
-    __syncwarp();
-    for (uint32_t u = un > kNTiles ? un - kNTiles : 0; u < un; ++u)
-      mbar_wait_bounded(bar(&sh->nfull[u % kNTiles]), (u / kNTiles) & 1, drain_budget(p.budget_ns));
-    for (uint32_t u = uv > kVTiles ? uv - kVTiles : 0; u < uv; ++u)
-      mbar_wait_bounded(bar(&sh->vfull[u % kVTiles]), (u / kVTiles) & 1, drain_budget(p.budget_ns));
-  } else if (!kBox && (warp == 4 || warp > 5)) {
-    // ============================================================ copies of single rows (any page size)
+  if (warp == 4 || warp > 5) {
+    // ============================================================ copies of key rows
     // A warp takes every third group of four keys; lanes 0-23 look up their cache rows.  Rows past the keys and of
     // bad blocks are zeros.  The values of the next tile are under way while a tile is completed.
     const int cw = warp == 4 ? 0 : warp - 5;
@@ -545,44 +462,19 @@ __global__ void __launch_bounds__(kUtThreads<kBox>, 1) paged_tc_kernel(const __g
   if (warp == 5) tc::tmem_dealloc(tmem, 512);
 }
 
-template <typename T>
-cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
-  const int box = paged_tc_box(p.page);
-  PagedMaps::Key key;
-  memset(&key, 0, sizeof(key));
-  key.lat = p.latent; key.kpe = p.kpe; key.lat_rs = p.lat_rs; key.kpe_rs = p.kpe_rs; key.rows = p.nblocks * p.page; key.box = box;
-  if (box >= kTmaBox && (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0)) {
-    m->valid = false;
-    const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-    m->key = key;
-    m->valid = true;
-  }
-  UtArgs a;
-  a.lat = m->lat; a.kpe = m->kpe; a.p = p; a.box = box;
-  if (box >= kTmaBox)
-    paged_tc_kernel<T, true><<<p.workers * 2, kUtThreads<true>, kUtSmem, stream>>>(a);
-  else
-    paged_tc_kernel<T, false><<<p.workers * 2, kUtThreads<false>, kUtSmem, stream>>>(a);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t paged_tc_prepare(bool bf16) {
-  const void* k[2] = {bf16 ? (const void*)paged_tc_kernel<__nv_bfloat16, true> : (const void*)paged_tc_kernel<__half, true>,
-                      bf16 ? (const void*)paged_tc_kernel<__nv_bfloat16, false> : (const void*)paged_tc_kernel<__half, false>};
-  for (const void* f : k) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return bf16 ? cudaFuncSetAttribute(paged_tc_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem)
+              : cudaFuncSetAttribute(paged_tc_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUtSmem);
 }
 
-cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream) {
-  return bf16 ? launch<__nv_bfloat16>(p, maps, stream) : launch<__half>(p, maps, stream);
+cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, cudaStream_t stream) {
+  if (bf16)
+    paged_tc_kernel<__nv_bfloat16><<<p.workers * 2, kUtThreads, kUtSmem, stream>>>(p);
+  else
+    paged_tc_kernel<__half><<<p.workers * 2, kUtThreads, kUtSmem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace mla
