@@ -310,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     bool ok = true;
     auto announce = [&](uint64_t* b) {  // to the MMA thread
       __syncwarp();
-      if (lane == 0) tc::arrive_cluster(tc::mapa(bar(b), 0));
+      if (lane == 0) tc::arrive_operands(tc::mapa(bar(b), 0));
     };
     auto meet = [&]() {  // the two warps of these rows
       __syncwarp();
