@@ -75,7 +75,7 @@ struct PagedMaps {  // tensor maps of the last call's caches and what they were 
     int lat_rs, kpe_rs, rows;
   } key;
   bool valid;
-  CUtensorMap lat, kpe, lat_wide;
+  CUtensorMap lat, kpe;
 };
 constexpr int kPagedBox = 32;  // cache rows of a TMA copy
 cudaError_t paged_pair_prepare(bool bf16);

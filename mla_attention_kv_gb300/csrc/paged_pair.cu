@@ -19,7 +19,7 @@
 // Shared memory: queries 72 KB, weights 16 KB, keys 72 KB (three slots of
 // three 64-column blocks), values 64 KB (four slots of 32 keys); one tile of
 // each, refilled slot by slot behind the MMAs.  All with the 128-byte
-// swizzle.  Tiles are requested into L2 two ahead of their copies.  MMA order:
+// swizzle.  MMA order:
 // scores of tile t + 1, then output of tile t, so the softmax of a tile runs
 // under the output of the one before.  Cycles of a tile: 36 score steps of 32
 // and 16 output MMAs of 64, 2180 measured alone.
@@ -30,10 +30,9 @@
 //
 // Warps: 0-3 queries, softmax, results (a row belongs to two threads, 64 keys
 // of a tile each: warps w and w + 2), 4 key copies, 5 MMA (the even CTA's,
-// for both), 6 value copies.  The copies of both CTAs are counted on the even
-// CTA's barriers.  The values of the last tile of a sequence are awaited by
-// each CTA itself, which zeroes their rows past the keys (they may hold
-// anything) before it announces its weights.
+// for both), 6-9 value copies (a slot each).  Keys come by TMA, values by
+// cp.async: with both by TMA a copy engine's 30 bytes per cycle and SM bounded
+// the tile (4500 cycles).  Value rows past the keys are zeros.
 #include <string.h>
 
 #include "attn.h"
@@ -44,11 +43,10 @@
 namespace mla {
 namespace {
 
-constexpr int kPpThreads = 224;
+constexpr int kPpThreads = 320;
 constexpr int kPpRows = kPagedTcRows;  // 128 per pair
 constexpr int kPpKeys = 128;           // keys of a tile
 constexpr int kBox = kPagedBox;        // cache rows per copy
-constexpr int kAhead = 2;
 constexpr uint32_t kBlk = 8192;  // 64 rows x 64 columns
 constexpr int kKSlots = 3, kVSlots = 4;
 constexpr uint32_t kKSlot = 3 * kBlk, kVSlot = 2 * kBlk;
@@ -61,7 +59,7 @@ constexpr float kRescale = 8.0f;
 
 struct PpShared {
   uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
-  uint64_t sfull[2], qready, pfull, pvdone, vtail, done, pair[2];
+  uint64_t sfull[2], qready, pfull, pvdone, done, pair[2];
   float row[2][2][64];  // exchange between the two threads of a row: [parity of the meeting][half][row]
   uint32_t tmem;
   int abort;
@@ -69,7 +67,7 @@ struct PpShared {
 static_assert(sizeof(PpShared) <= 2048, "barrier block");
 
 struct PpArgs {
-  CUtensorMap lat, kpe, lat_wide;
+  CUtensorMap lat, kpe;
   PagedParams p;
 };
 
@@ -105,7 +103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       mbar_init(bar(&sh->kempty[i]), 1);
     }
     for (int i = 0; i < kVSlots; ++i) {
-      mbar_init(bar(&sh->vfull[i]), 1);
+      mbar_init(bar(&sh->vfull[i]), 2);  // the copying warps of both CTAs
       mbar_init(bar(&sh->vempty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -115,7 +113,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     mbar_init(bar(&sh->qready), 8);  // the softmax warps of both CTAs
     mbar_init(bar(&sh->pfull), 8);
     mbar_init(bar(&sh->pvdone), 1);
-    mbar_init(bar(&sh->vtail), 1);
     mbar_init(bar(&sh->done), 1);
     sh->abort = 0;
     fence_mbar_init();
@@ -138,17 +135,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     return keys;
   };
 
-  if (warp == 4 || warp == 6) {
-    // ============================================================ copies
-    const bool values = warp == 6;
+  if (warp == 4) {
+    // ============================================================ keys, by TMA
     const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
-    uint32_t u = 0, tails = 0;                // tiles copied, last tiles of sequences among them
+    uint32_t u = 0;                           // tiles copied
     bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t par) {
-      ok = ok && at_wait_warp(bar(b), par, abort, p.budget_ns, p.status);
-      return ok;
-    };
-    auto lead = [&](uint64_t* b) { return tc::mapa(bar(b), 0); };  // of the even CTA
     PlanCursor c = first;
     for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
       int t0, t1;
@@ -165,60 +156,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
         }
         return blk * p.page + (k - pg * p.page);
       };
-      const bool own = lane >> 1 == rank;  // this CTA's half of the keys
-      auto request = [&](int row) {
-        if (values || !own || row < 0 || row >= zero_row) return;
-        tma_prefetch_2d(&a.lat_wide, 0, row);
-        tma_prefetch_2d(&a.lat_wide, 256, row);
-        tma_prefetch_2d(&a.kpe, 0, row);
-      };
-      int row = t0 < t1 ? rows_of(t0) : -1;
-      for (int t = t0 + 1; t < t0 + kAhead; ++t) request(rows_of(t));
+      int row = rows_of(t0);
       for (int t = t0; t < t1 && ok; ++t, ++u) {
-        if (!values) request(rows_of(t + kAhead));
         const int next = rows_of(t + 1);
         const uint32_t boxes = __popc(__ballot_sync(~0u, row >= 0));
-        if (!values) {
-          for (int g = 0; g < kKSlots; ++g) {
-            if (!wait(&sh->kempty[g], (u & 1) ^ 1)) break;
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(&sh->kfull[g]), boxes * kBox * 128 * 3);
-            __syncwarp();
-            if (own && row >= 0) {
-              const uint32_t d = sbase + kPpK + g * kKSlot + (lane & 1) * (kBlk / 2), b = lead(&sh->kfull[g]);
+        for (int g = 0; g < kKSlots; ++g) {
+          ok = ok && at_wait_warp(bar(&sh->kempty[g]), (u & 1) ^ 1, abort, p.budget_ns, p.status);
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(&sh->kfull[g]), boxes * kBox * 128 * 3);
+          __syncwarp();
+          if (lane >> 1 == rank && row >= 0) {  // this CTA's half of the keys
+            const uint32_t d = sbase + kPpK + g * kKSlot + (lane & 1) * (kBlk / 2), b = tc::mapa(bar(&sh->kfull[g]), 0);
 #pragma unroll
-              for (int j = 0; j < 3; ++j) {
-                const int blk = 3 * g + j;
-                tma_load_2d_pair(d + j * kBlk, blk < 8 ? &a.lat : &a.kpe, blk < 8 ? blk * 64 : 0, row, b);
-              }
+            for (int j = 0; j < 3; ++j) {
+              const int blk = 3 * g + j;
+              tma_load_2d_pair(d + j * kBlk, blk < 8 ? &a.lat : &a.kpe, blk < 8 ? blk * 64 : 0, row, b);
             }
-          }
-        } else {
-          const bool tail = keys - t * kPpKeys < kPpKeys;
-          for (int s = 0; s < kVSlots; ++s) {
-            if (!wait(&sh->vempty[s], (u & 1) ^ 1)) break;
-            if (rank == 0 && lane == 0) {
-              if (tail)
-                mbar_arrive(bar(&sh->vfull[s]));
-              else
-                mbar_arrive_expect_tx(bar(&sh->vfull[s]), 2 * kVSlot);
-            }
-            __syncwarp();
-            if (lane == s && row >= 0) {
-              const uint32_t d = sbase + kPpV + s * kVSlot, b = tail ? bar(&sh->vtail) : lead(&sh->vfull[s]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int x = ((j >> 1) * 4 + rank * 2 + (j & 1)) * 64;
-                if (tail)
-                  tma_load_2d(d + j * (kBlk / 2), &a.lat, x, row, b);
-                else
-                  tma_load_2d_pair(d + j * (kBlk / 2), &a.lat, x, row, b);
-              }
-            }
-          }
-          if (tail && ok) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar(&sh->vtail), boxes * kVSlot);
-            ++tails;
           }
         }
         row = next;
@@ -231,13 +184,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       const uint64_t spent = globaltimer_ns() - t0, limit = drain_budget(p.budget_ns);
       mbar_wait_bounded(bar(b), par, spent < limit ? limit - spent : 0);
     };
-    if (u > 0) {
-      for (int i = 0; i < (values ? kVSlots : kKSlots); ++i) {
-        if (rank == 0) drain(values ? &sh->vfull[i] : &sh->kfull[i], (u - 1) & 1);
-        drain(values ? &sh->vempty[i] : &sh->kempty[i], (u - 1) & 1);
-      }
-      if (tails > 0) drain(&sh->vtail, (tails - 1) & 1);
+    for (int i = 0; i < kKSlots && u > 0; ++i) {
+      if (rank == 0) drain(&sh->kfull[i], (u - 1) & 1);
+      drain(&sh->kempty[i], (u - 1) & 1);
     }
+  } else if (warp > 5) {
+    // ============================================================ values, by cp.async: a warp fills a slot
+    const int slot = warp - 6;
+    const uint32_t empty = bar(&sh->vempty[slot]), lead = tc::mapa(bar(&sh->vfull[slot]), 0);
+    uint32_t u = 0;
+    bool ok = true;
+    PlanCursor c = first;
+    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
+      int t0, t1;
+      const int keys = span(c, &t0, &t1);
+      auto rows_of = [&](int tile) {  // of this lane's key (-1: none, reads as zeros)
+        const int k = tile * kPpKeys + slot * 32 + lane;
+        if (tile >= t1 || k >= keys) return -1;
+        const int pg = k / p.page;
+        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
+        if (blk < 0 || blk >= p.nblocks) {
+          atomicOr(p.status, kStatusBadSlot);
+          return -1;
+        }
+        return blk * p.page + (k - pg * p.page);
+      };
+      int row = rows_of(t0);
+      for (int t = t0; t < t1; ++t, ++u) {
+        ok = at_wait_warp(empty, (u & 1) ^ 1, abort, p.budget_ns, p.status);
+        if (!ok) break;
+        // lane = 16-byte unit of this CTA's columns 128 rank .. + 127 of either half of the latents
+        const T* src = static_cast<const T*>(p.latent) + (lane >> 4) * 256 + rank * 128 + (lane & 15) * 8;
+        const uint32_t d = sbase + kPpV + slot * kVSlot + (lane >> 3) * (kBlk / 2);
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+          const int cr = __shfl_sync(~0u, row, r);
+          cp_async16(d + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src + (size_t)max(cr, 0) * p.lat_rs, cr < 0 ? 0 : 16);
+        }
+        cp_async_commit();
+        row = rows_of(t + 1);
+        cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::arrive_operands(lead);
+      }
+    }
+    cp_async_wait<0>();
+    if (u > 0) mbar_wait_bounded(empty, (u - 1) & 1, drain_budget(p.budget_ns));  // the last release has arrived
   } else if (warp == 5) {
     // ============================================================ MMA (one thread of the even CTA)
     if (rank == 0 && tc::elect_one()) {
@@ -306,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     const int r = tid & 63, hf = tid >> 6;  // row of this CTA's 64, half of a tile's keys
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     const float scale = p.scale_log2;
-    uint32_t g = 0, tails = 0, meets = 0;  // tiles done, last tiles of sequences among them
+    uint32_t g = 0, meets = 0;  // tiles done
     bool ok = true;
     auto announce = [&](uint64_t* b) {  // to the MMA thread
       __syncwarp();
@@ -345,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     }
     for (bool more = true; more && c.lo < x1 && ok;) {
       int t0, t1;
-      const int keys = span(c, &t0, &t1);
+      span(c, &t0, &t1);
       if (tid == 0 && rank == 0 && c.hi >= x1) plan_post_join(p, c, kPpRows, w, x0, x1, total, W);
       const int row = c.j * kPpRows + rank * 64 + r;
       const bool live = row < c.q.n * H;
@@ -419,15 +412,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<uint4*>(smem + kPpP + hf * kBlk + r * 128 + ((i ^ (r & 7)) * 16)) =
               make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        const int valid = keys - t * kPpKeys;
-        if (valid < kPpKeys) {
-          // latents past the keys: whole 128-byte rows, so the swizzle does not matter
-          if (!at_wait_warp(bar(&sh->vtail), tails++ & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
-          for (int x = tid; x < (kPpKeys - valid) * 32; x += 128) {
-            const int k = valid + (x >> 5);
-            *reinterpret_cast<uint4*>(smem + kPpV + (k >> 5) * kVSlot + ((x >> 3) & 3) * (kBlk / 2) + (k & 31) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         announce(&sh->pfull);
@@ -512,14 +496,13 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
     m->valid = false;
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&m->lat_wide, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 256, kBox, CU_TENSOR_MAP_SWIZZLE_NONE))
+        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     m->key = key;
     m->valid = true;
   }
   PpArgs a;
-  a.lat = m->lat; a.kpe = m->kpe; a.lat_wide = m->lat_wide; a.p = p;
+  a.lat = m->lat; a.kpe = m->kpe; a.p = p;
   paged_pair_kernel<T><<<p.workers * 2, kPpThreads, kPpSmem, stream>>>(a);
   return cudaGetLastError();
 }
