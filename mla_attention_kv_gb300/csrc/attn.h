@@ -66,8 +66,8 @@ constexpr int kPagedMmaRows = 32;
 inline int paged_mma_workers(int rows, int num_sms) { return rows == 16 ? 2 * num_sms : num_sms; }  // CTAs that are resident
 cudaError_t paged_mma_prepare(bool bf16);  // kernel attributes, once per device
 cudaError_t paged_mma_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
-// tcgen05 kernels: items of 128 query rows, two CTAs per worker.  paged_pair: pages of whole boxes; paged_tc: any page.
-constexpr int kPagedTcRows = 128;
+// tcgen05 kernel: items of 128 query rows, two CTAs per worker.
+constexpr int kPagedPairRows = 128;
 struct PagedMaps {  // tensor maps of the last call's caches and what they were made from
   struct Key {
     const void* lat;
@@ -77,11 +77,8 @@ struct PagedMaps {  // tensor maps of the last call's caches and what they were 
   bool valid;
   CUtensorMap lat, kpe;
 };
-constexpr int kPagedBox = 32;  // cache rows of a TMA copy
 cudaError_t paged_pair_prepare(bool bf16);
 cudaError_t paged_pair_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream);
-cudaError_t paged_tc_prepare(bool bf16);
-cudaError_t paged_tc_launch(bool bf16, const PagedParams& p, cudaStream_t stream);
 // Joins the partial results of items split over workers.
 cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
 

@@ -90,7 +90,7 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     return fail(e, "device query");
   }
   // workspace: [status, 256 bytes] | a join record per worker | two partial results per worker
-  const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedTcRows;
+  const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedPairRows;
   const size_t rows = rows_mma > rows_tc ? rows_mma : rows_tc;
   const size_t join_off = 256, ml_off = join_off + (((size_t)h->num_sms * 2 * sizeof(PagedJoin) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
   e = cudaMalloc(&h->ws, o_off + rows * kRank * sizeof(float));
@@ -113,7 +113,6 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   // (shared memory beyond the default is asked for once, not per call)
   const bool bf16 = c.dtype == MLA_BF16;
   e = paged_mma_prepare(bf16);
-  if (e == cudaSuccess) e = paged_tc_prepare(bf16);
   if (e == cudaSuccess) e = paged_pair_prepare(bf16);
   if (e == cudaSuccess) e = prompt_tc_prepare(bf16);
   if (e != cudaSuccess) {
@@ -227,15 +226,13 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   // (with ragged chunks the host knows only the average)
   const long long rows_per_seq = (long long)(a.T / a.num_seqs > 0 ? a.T / a.num_seqs : 1) * H;
-  // 32 rows or fewer: the kernel built around the key stream (64 sequences of up to 4096 keys with 16 heads: 48 us, the
-  // tcgen05 kernel 92 us); more: one pass of the tcgen05 kernel for 128 rows (64 sequences of up to 32768 keys with 128
-  // heads: 325 us, four passes of the other 1344 us)
+  // 32 rows or fewer: the kernel built around the key stream (64 sequences of up to 4096 keys with 16 heads: 48 us, a
+  // tcgen05 kernel for 128 rows 92 us); more: one pass of the tcgen05 kernel (64 sequences of up to 32768 keys with 128
+  // heads: 245 us, four passes of the other 1344 us)
   const bool tc = rows_per_seq > kPagedMmaRows;
-  const int rows = tc ? kPagedTcRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
+  const int rows = tc ? kPagedPairRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
   p.workers = tc ? h->num_sms / 2 : paged_mma_workers(rows, h->num_sms);
-  cudaError_t e = !tc                            ? paged_mma_launch(bf16, p, rows, stream)
-                  : a.page_size % kPagedBox == 0 ? paged_pair_launch(bf16, p, &h->paged_maps, stream)
-                                                 : paged_tc_launch(bf16, p, stream);
+  cudaError_t e = tc ? paged_pair_launch(bf16, p, &h->paged_maps, stream) : paged_mma_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention launch");
   e = paged_combine_launch(bf16, p, rows, stream);
   if (e != cudaSuccess) return fail(e, "paged attention combine launch");

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
 
   grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = plan_total(p, plan, R, blockIdx.x == 0);
-  const int W = total > 0 ? plan_workers(total, p.workers) : 0;
+  const int W = total > 0 ? plan_workers(total, p.workers, R) : 0;
   const int w = blockIdx.x;
   if (w >= W) {
     if (tid == 0) p.joins[w].rows = 0;

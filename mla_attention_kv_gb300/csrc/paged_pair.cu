@@ -1,6 +1,6 @@
 // paged_pair.cu -- attention of new tokens over the paged latent cache, for
-// items of 128 query rows and pages of whole 32-row boxes, on the 2-SM MMA
-// (tcgen05.mma.cta_group::2, M = 128) / TMEM / TMA.
+// items of 128 query rows, on the 2-SM MMA (tcgen05.mma.cta_group::2,
+// M = 128) / TMEM / TMA.
 //
 // The mathematics is that of paged_mma.cu: per query row (a token and a
 // head; q = [q_latent | q_pe], 576 wide) softmax(scale * q . key) over the
@@ -15,24 +15,33 @@
 // keys 64 (two buffers), and nothing is computed twice.  As the B operand
 // each CTA holds its half of the keys for the scores (64 keys x 576 columns)
 // and its half of the columns of all keys for the output (128 keys x 256).
+// (One 128-row M per CTA would fill tensor memory with the output alone; two
+// CTAs with half of the output and all of the scores each: 325 us below.)
 //
 // Shared memory: queries 72 KB, weights 16 KB, keys 72 KB (three slots of
 // three 64-column blocks), values 64 KB (four slots of 32 keys); one tile of
-// each, refilled slot by slot behind the MMAs.  All with the 128-byte
-// swizzle.  MMA order:
-// scores of tile t + 1, then output of tile t, so the softmax of a tile runs
-// under the output of the one before.  Cycles of a tile: 36 score steps of 32
-// and 16 output MMAs of 64, 2180 measured alone.
-// @FIG@
+// each, refilled slot by slot behind the MMAs, all with the 128-byte swizzle.
+// MMA order: scores of tile t + 1, then output of tile t, so the softmax of a
+// tile runs under the output of the one before.
+//
+// What bounds it: a tile's 36 score steps take 32 cycles each and its 16
+// output MMAs 64, 2180 together (measured alone), but they read 240 KB of
+// shared memory and 152 KB are written beside them, 3060 cycles at 128 bytes
+// each; the kernel takes 3100 where the cache is in L2 and 3700 from HBM.
+// Both key and value copies by TMA reached 30 bytes per cycle and SM (4500
+// cycles a tile), so the values come by cp.async, on the load/store path.
+// Requests into L2 ahead of the copies changed nothing.  Decode of 64
+// sequences of up to 32768 keys, 128 heads, bf16 (1.15 GB of cache): 245 us,
+// 4.7 TB/s; chunks of up to 512 tokens over 8192 keys: 1.00 ms, 1.45 PFLOP/s.
 //
 // Rescaling the output only when a maximum grew by more than 2^8: as in
 // prompt_tc.cu.
 //
 // Warps: 0-3 queries, softmax, results (a row belongs to two threads, 64 keys
-// of a tile each: warps w and w + 2), 4 key copies, 5 MMA (the even CTA's,
-// for both), 6-9 value copies (a slot each).  Keys come by TMA, values by
-// cp.async: with both by TMA a copy engine's 30 bytes per cycle and SM bounded
-// the tile (4500 cycles).  Value rows past the keys are zeros.
+// of a tile each: warps w and w + 2), 4 key copies by TMA (or 10 and 11 by
+// cp.async), 5 MMA (the even CTA's, for both), 6-9 value copies, a slot each.
+// What the MMAs wait for is counted on the even CTA's barriers.  Value rows
+// past the keys are zeros; scores of such keys are masked.
 #include <string.h>
 
 #include "attn.h"
@@ -43,10 +52,15 @@
 namespace mla {
 namespace {
 
-constexpr int kPpThreads = 320;
-constexpr int kPpRows = kPagedTcRows;  // 128 per pair
+// kBox: the page size is a multiple of kBoxRows and the keys come by TMA;
+// else by cp.async (two more warps).  64 sequences of up to 16384 keys, 128
+// heads, bf16, TMA / cp.async: page 64 141 / 199 us, 32 142 / 200 us; 16 and 8
+// by cp.async 201 us (boxes of 16 and 8 rows, in a kernel that TMA bounded
+// more: 1.27 and 1.9 times the time of 32).
+template <bool kBox> constexpr int kPpThreads = kBox ? 320 : 384;
+constexpr int kPpRows = kPagedPairRows;  // 128 per pair
 constexpr int kPpKeys = 128;           // keys of a tile
-constexpr int kBox = kPagedBox;        // cache rows per copy
+constexpr int kBoxRows = 32;           // cache rows of a TMA copy
 constexpr uint32_t kBlk = 8192;  // 64 rows x 64 columns
 constexpr int kKSlots = 3, kVSlots = 4;
 constexpr uint32_t kKSlot = 3 * kBlk, kVSlot = 2 * kBlk;
@@ -71,8 +85,8 @@ struct PpArgs {
   PagedParams p;
 };
 
-template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged_pair_kernel(const __grid_constant__ PpArgs a) {
+template <typename T, bool kBox>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1) paged_pair_kernel(const __grid_constant__ PpArgs a) {
   using E = Elem<T>;
   const PagedParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -88,7 +102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
   PlanShared* plan = reinterpret_cast<PlanShared*>(smem + kPpK);
   grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = plan_total(p, plan, kPpRows, blockIdx.x == 0);
-  const int W = total > 0 ? plan_workers(total, p.workers) : 0;
+  const int W = total > 0 ? plan_workers(total, p.workers, kPpRows) : 0;
   if (w >= W) {
     if (tid == 0) p.joins[w].rows = 0;
     return;
@@ -99,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
 
   if (tid == 0) {
     for (int i = 0; i < kKSlots; ++i) {
-      mbar_init(bar(&sh->kfull[i]), 1);
+      mbar_init(bar(&sh->kfull[i]), kBox ? 1 : 4);  // (the copying warps of both CTAs)
       mbar_init(bar(&sh->kempty[i]), 1);
     }
     for (int i = 0; i < kVSlots; ++i) {
@@ -135,7 +149,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     return keys;
   };
 
-  if (warp == 4) {
+  // the cache row of a key (-1: past the keys, or in a block that there is not)
+  auto row_of = [&](const PlanCursor& c, int k, int keys) {
+    if (k >= keys) return -1;
+    const int pg = k / p.page;
+    const int blk = p.table[(size_t)c.s * p.table_stride + pg];
+    if (blk < 0 || blk >= p.nblocks) {
+      atomicOr(p.status, kStatusBadSlot);
+      return -1;
+    }
+    return blk * p.page + (k - pg * p.page);
+  };
+
+  if (kBox && warp == 4) {
     // ============================================================ keys, by TMA
     const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
     uint32_t u = 0;                           // tiles copied
@@ -146,15 +172,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       const int keys = span(c, &t0, &t1);
       // lane l < 4 holds the cache row of the l-th 32 keys of a tile (-1: past the keys)
       auto rows_of = [&](int tile) {
-        const int k = tile * kPpKeys + lane * kBox;
-        if (lane >= kPpKeys / kBox || tile >= t1 || k >= keys) return -1;
-        const int pg = k / p.page;
-        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
-        if (blk < 0 || blk >= p.nblocks) {
-          atomicOr(p.status, kStatusBadSlot);
-          return zero_row;
-        }
-        return blk * p.page + (k - pg * p.page);
+        const int k = tile * kPpKeys + lane * kBoxRows;
+        if (lane >= kPpKeys / kBoxRows || tile >= t1 || k >= keys) return -1;
+        const int r = row_of(c, k, keys);
+        return r < 0 ? zero_row : r;
       };
       int row = rows_of(t0);
       for (int t = t0; t < t1 && ok; ++t, ++u) {
@@ -163,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
         for (int g = 0; g < kKSlots; ++g) {
           ok = ok && at_wait_warp(bar(&sh->kempty[g]), (u & 1) ^ 1, abort, p.budget_ns, p.status);
           if (!ok) break;
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(&sh->kfull[g]), boxes * kBox * 128 * 3);
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(&sh->kfull[g]), boxes * kBoxRows * 128 * 3);
           __syncwarp();
           if (lane >> 1 == rank && row >= 0) {  // this CTA's half of the keys
             const uint32_t d = sbase + kPpK + g * kKSlot + (lane & 1) * (kBlk / 2), b = tc::mapa(bar(&sh->kfull[g]), 0);
@@ -188,6 +209,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       if (rank == 0) drain(&sh->kfull[i], (u - 1) & 1);
       drain(&sh->kempty[i], (u - 1) & 1);
     }
+  } else if (!kBox && warp > 9) {
+    // ============================================================ keys, by cp.async: 32 of this CTA's 64 to a warp
+    const int part = rank * 2 + warp - 10;  // which 32 keys of a tile
+    uint32_t u = 0;
+    bool ok = true;
+    PlanCursor c = first;
+    for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
+      int t0, t1;
+      const int keys = span(c, &t0, &t1);
+      int row = row_of(c, t0 * kPpKeys + part * 32 + lane, t0 < t1 ? keys : 0);
+      for (int t = t0; t < t1 && ok; ++t, ++u) {
+        for (int g = 0; g < kKSlots; ++g) {
+          ok = at_wait_warp(bar(&sh->kempty[g]), (u & 1) ^ 1, abort, p.budget_ns, p.status);
+          if (!ok) break;
+          // lane = 16-byte unit of the slot's three blocks (the last of all is k_pe)
+          const bool pe = g == kKSlots - 1 && lane >= 16;
+          const T* src = pe ? static_cast<const T*>(p.kpe) + (lane & 7) * 8 : static_cast<const T*>(p.latent) + g * 192 + lane * 8;
+          const size_t rs = pe ? p.kpe_rs : p.lat_rs;
+          const uint32_t d = sbase + kPpK + g * kKSlot + (lane >> 3) * kBlk + (part & 1) * (kBlk / 2);
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
+            const int cr = __shfl_sync(~0u, row, r);
+            if (lane < 24) cp_async16(d + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src + (size_t)max(cr, 0) * rs, cr < 0 ? 0 : 16);
+          }
+          cp_async_commit();
+          if (g > 0) {  // the slot before is there
+            cp_async_wait<1>();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::arrive_operands(tc::mapa(bar(&sh->kfull[g - 1]), 0));
+          }
+        }
+        row = row_of(c, (t + 1) * kPpKeys + part * 32 + lane, t + 1 < t1 ? keys : 0);
+        cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) tc::arrive_operands(tc::mapa(bar(&sh->kfull[kKSlots - 1]), 0));
+      }
+    }
+    for (int i = 0; i < kKSlots && u > 0; ++i)  // the last releases have arrived
+      if (!mbar_wait_bounded(bar(&sh->kempty[i]), (u - 1) & 1, drain_budget(p.budget_ns))) break;
   } else if (warp > 5) {
     // ============================================================ values, by cp.async: a warp fills a slot
     const int slot = warp - 6;
@@ -198,18 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
     for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
       int t0, t1;
       const int keys = span(c, &t0, &t1);
-      auto rows_of = [&](int tile) {  // of this lane's key (-1: none, reads as zeros)
-        const int k = tile * kPpKeys + slot * 32 + lane;
-        if (tile >= t1 || k >= keys) return -1;
-        const int pg = k / p.page;
-        const int blk = p.table[(size_t)c.s * p.table_stride + pg];
-        if (blk < 0 || blk >= p.nblocks) {
-          atomicOr(p.status, kStatusBadSlot);
-          return -1;
-        }
-        return blk * p.page + (k - pg * p.page);
-      };
-      int row = rows_of(t0);
+      int row = row_of(c, t0 * kPpKeys + slot * 32 + lane, t0 < t1 ? keys : 0);
       for (int t = t0; t < t1; ++t, ++u) {
         ok = at_wait_warp(empty, (u & 1) ^ 1, abort, p.budget_ns, p.status);
         if (!ok) break;
@@ -222,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
           cp_async16(d + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src + (size_t)max(cr, 0) * p.lat_rs, cr < 0 ? 0 : 16);
         }
         cp_async_commit();
-        row = rows_of(t + 1);
+        row = row_of(c, (t + 1) * kPpKeys + slot * 32 + lane, t + 1 < t1 ? keys : 0);
         cp_async_wait<0>();
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -294,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       tc::commit2_both(bar(&sh->done));
     }
     __syncwarp();
-  } else {
+  } else if (warp < 4) {
     // ============================================================ queries, softmax, results
     const int r = tid & 63, hf = tid >> 6;  // row of this CTA's 64, half of a tile's keys
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
@@ -310,23 +361,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       if (lane == 0) mbar_arrive(bar(&sh->pair[warp & 1]));
       return at_wait_warp(bar(&sh->pair[warp & 1]), meets++ & 1, abort, p.budget_ns, p.status);
     };
-    auto load_q = [&](const PlanCursor& c) {  // the first five of the nine blocks, or the others
-      const int row = c.j * kPpRows + rank * 64 + r;
-      const bool live = row < c.q.n * H;
-      const int tok = live ? row / H : 0, hd = live ? row - tok * H : 0;
-      const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_lat) + (size_t)(c.q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs);
-      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_pe) + (size_t)(c.q.begin + tok) * p.qp_ts + (size_t)hd * p.qp_hs);
-      const int end = hf ? 9 : 5;
-#pragma unroll 2
-      for (int j = hf ? 5 : 0; j < end; ++j) {
-        const uint4* src = j < 8 ? ql + j * 8 : qp;
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + kPpQ + j * kBlk + r * 128 + ((i ^ (r & 7)) * 16)) = v[i];
+    auto load_q = [&](const PlanCursor& c) {  // a warp takes 16 of the 64 rows, lane = 16-byte unit
+      for (int i = 0; i < 16; ++i) {
+        const int qr = warp * 16 + i, row = c.j * kPpRows + rank * 64 + qr;
+        const bool live = row < c.q.n * H;
+        const int tok = live ? row / H : 0, hd = live ? row - tok * H : 0;
+        const T* ql = static_cast<const T*>(p.q_lat) + (size_t)(c.q.begin + tok) * p.ql_ts + (size_t)hd * p.ql_hs;
+        const T* qp = static_cast<const T*>(p.q_pe) + (size_t)(c.q.begin + tok) * p.qp_ts + (size_t)hd * p.qp_hs;
+        const uint32_t d = sbase + kPpQ + (lane >> 3) * kBlk + qr * 128 + (((lane & 7) ^ (qr & 7)) * 16);
+        cp_async16(d, ql + lane * 8, live ? 16 : 0);
+        cp_async16(d + 4 * kBlk, ql + 256 + lane * 8, live ? 16 : 0);
+        if (lane < 8) cp_async16(d + 8 * kBlk, qp + lane * 8, live ? 16 : 0);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       tc::fence_proxy_async_smem();
       announce(&sh->qready);
     };
@@ -341,7 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       span(c, &t0, &t1);
       if (tid == 0 && rank == 0 && c.hi >= x1) plan_post_join(p, c, kPpRows, w, x0, x1, total, W);
       const int row = c.j * kPpRows + rank * 64 + r;
-      const bool live = row < c.q.n * H;
+      const int rows = min(32, c.q.n * H - (row - lane));  // of this warp's 32
+      const bool live = lane < rows;
       const int limit0 = (live ? c.q.keys_of_row(row, H) : 0) - hf * 64;
       const bool whole = c.lo >= x0 && c.hi <= x1;
       const size_t grow = (size_t)c.q.begin * H + row;
@@ -434,33 +483,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads, 1) paged
       }
       // this thread's columns: 128 hf .. 128 hf + 127 of either half of the output
       const float iv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      T* out = static_cast<T*>(p.out) + (live ? grow : 0) * kRank + hf * 128;
-      float* po = p.part_o + (slot * kPpRows + rank * 64 + r) * kRank + hf * 128;
       if (t0 < t1) {
+        // 32 columns at a time through the weights' place, so that a warp stores whole rows' pieces
+        unsigned char* st = smem + kPpP + warp * 4096;
+        T* out = static_cast<T*>(p.out) + (grow - lane) * kRank + hf * 128;  // (of the warp's first row)
+        float* po = p.part_o + (slot * kPpRows + rank * 64 + (warp & 1) * 32) * kRank + hf * 128;
 #pragma unroll 1
         for (int cc = 0; cc < 256; cc += 32) {
           uint32_t o[32];
           tc::ld32(tl + cc, o);
           tc::wait_ld();
-          if (!live) continue;
           const int col = (cc >> 7) * 256 + (cc & 127);
-          if (whole) {
+          __syncwarp();
+          if (whole) {  // four units of 16 bytes a row
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
+            for (int k = 0; k < 4; ++k) {
               uint32_t q[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                q[j] = E::pack(__uint_as_float(o[k + 2 * j]) * iv, __uint_as_float(o[k + 2 * j + 1]) * iv);
-              *reinterpret_cast<uint4*>(out + col + k) = make_uint4(q[0], q[1], q[2], q[3]);
+                q[j] = E::pack(__uint_as_float(o[8 * k + 2 * j]) * iv, __uint_as_float(o[8 * k + 2 * j + 1]) * iv);
+              *reinterpret_cast<uint4*>(st + lane * 64 + ((k ^ (lane >> 1 & 3)) * 16)) = make_uint4(q[0], q[1], q[2], q[3]);
             }
-          } else {
+            __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(po + col + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const int rr = i * 8 + (lane >> 2), k = lane & 3;
+              if (rr < rows)
+                *reinterpret_cast<uint4*>(out + (size_t)rr * kRank + col + k * 8) = *reinterpret_cast<const uint4*>(st + rr * 64 + ((k ^ (rr >> 1 & 3)) * 16));
+            }
+          } else {  // eight units a row
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(st + lane * 128 + ((k ^ (lane & 7)) * 16)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), k = lane & 7;
+              if (rr < rows)
+                *reinterpret_cast<uint4*>(po + (size_t)rr * kRank + col + k * 4) = *reinterpret_cast<const uint4*>(st + rr * 128 + ((k ^ (rr & 7)) * 16));
+            }
           }
         }
         tc::fence_before_sync();
       } else if (whole && live) {  // no key at all
+        T* out = static_cast<T*>(p.out) + grow * kRank + hf * 128;
         for (int cc = 0; cc < 256; cc += 8)
           *reinterpret_cast<uint4*>(out + (cc >> 7) * 256 + (cc & 127)) = make_uint4(0, 0, 0, 0);
       }
@@ -492,26 +558,35 @@ cudaError_t launch(const PagedParams& p, PagedMaps* m, cudaStream_t stream) {
   PagedMaps::Key key;
   memset(&key, 0, sizeof(key));
   key.lat = p.latent; key.kpe = p.kpe; key.lat_rs = p.lat_rs; key.kpe_rs = p.kpe_rs; key.rows = p.nblocks * p.page;
-  if (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0) {
+  const bool box = p.page % kBoxRows == 0;
+  if (box && (!m->valid || memcmp(&key, &m->key, sizeof(key)) != 0)) {
     m->valid = false;
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, kBox, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tmap_2d(&m->lat, dt, p.latent, kRank, key.rows, (uint64_t)p.lat_rs * 2, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&m->kpe, dt, p.kpe, kRope, key.rows, (uint64_t)p.kpe_rs * 2, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     m->key = key;
     m->valid = true;
   }
   PpArgs a;
   a.lat = m->lat; a.kpe = m->kpe; a.p = p;
-  paged_pair_kernel<T><<<p.workers * 2, kPpThreads, kPpSmem, stream>>>(a);
+  if (box)
+    paged_pair_kernel<T, true><<<p.workers * 2, kPpThreads<true>, kPpSmem, stream>>>(a);
+  else
+    paged_pair_kernel<T, false><<<p.workers * 2, kPpThreads<false>, kPpSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t paged_pair_prepare(bool bf16) {
-  return bf16 ? cudaFuncSetAttribute(paged_pair_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem)
-              : cudaFuncSetAttribute(paged_pair_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+  const void* k[2] = {bf16 ? (const void*)paged_pair_kernel<__nv_bfloat16, true> : (const void*)paged_pair_kernel<__half, true>,
+                      bf16 ? (const void*)paged_pair_kernel<__nv_bfloat16, false> : (const void*)paged_pair_kernel<__half, false>};
+  for (const void* f : k) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t paged_pair_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream) {

@@ -27,8 +27,9 @@ namespace mla {
 
 constexpr int kKeyTile = 64;
 // Width of an item beyond its key tiles (loading its queries, storing its
-// result), in key tiles.
-constexpr int kItemCost = 1;
+// result), in key tiles.  128-row items: about 10 us for 0.95 us a key tile
+// (32 sequences of 100 to 2000 keys, 128 heads: 47 us at cost 1, 40 us at 8).
+__host__ __device__ constexpr int plan_item_cost(int R) { return R == kPagedPairRows ? 8 : 1; }
 constexpr int kPlanThreadsMax = 512;
 
 struct PlanShared {
@@ -84,7 +85,7 @@ __host__ __device__ __forceinline__ Seq plan_seq(const PagedParams& p, int s, in
   q.L = L;
   const long long rows = (long long)q.n * p.heads;
   q.items = (int)((rows + R - 1) / R);
-  q.first = q.last = kItemCost;
+  q.first = q.last = plan_item_cost(R);
   if (q.items > 0) {
     q.first += (q.keys_of_item(0, R, p.heads) + kKeyTile - 1) / kKeyTile;
     q.last += (q.keys_of_item(q.items - 1, R, p.heads) + kKeyTile - 1) / kKeyTile;
@@ -127,11 +128,13 @@ __device__ __forceinline__ long long plan_total(const PagedParams& p, PlanShared
   return ps->base[nt];
 }
 
-// Workers that take part: no range is shorter than kMinRange (with 2, one
-// sequence of 777 tokens took 16.5 us instead of 15.6).
-constexpr int kMinRange = 1;
-__host__ __device__ __forceinline__ int plan_workers(long long total, int W) {
-  const long long w = total / kMinRange;
+// Workers that take part: no range is shorter than this.  16-row items: 2
+// instead of 1 took one sequence of 777 tokens from 15.6 to 16.5 us.  128-row
+// items: one sequence of 4096 keys 30.4 us at 1, 26.7 at 2, 24.8 at 3; eight of
+// 500 to 3000 keys 26.6 us up to 3, 33.8 at 4.
+__host__ __device__ constexpr int plan_min_range(int R) { return R == kPagedPairRows ? 3 : 1; }
+__host__ __device__ __forceinline__ int plan_workers(long long total, int W, int R) {
+  const long long w = total / plan_min_range(R);
   return w < 1 ? 1 : (w < W ? (int)w : W);
 }
 __host__ __device__ __forceinline__ long long plan_worker_begin(long long total, int w, int W) {

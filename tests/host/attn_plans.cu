@@ -57,7 +57,7 @@ static void run(const std::vector<int>& n, const std::vector<int>& L, int H, int
   std::map<std::pair<int, int>, std::vector<Piece>> got;
   std::map<int, int> slots;
   if (total > 0) {
-    const int We = plan_workers(total, W);
+    const int We = plan_workers(total, W, R);
     CHECK(We >= 1 && We <= W);
     for (int w = 0; w < We; ++w) {
       const long long x0 = plan_worker_begin(total, w, We), x1 = plan_worker_begin(total, w + 1, We);
