@@ -219,6 +219,31 @@ def test_paged_ragged_chunks(H, layout):
     paged_case([0, 1, 3, 5, 2, 70, 0, 9], [5, 1, 2, 0, 90, 200, 0, 9], H, 16, "fp16", seed=H + 3, lead=2, tail=3, layout=layout)
 
 
+@pytest.mark.parametrize("H,page", [(40, 64), (128, 32), (128, 64), (200, 96)])
+@pytest.mark.parametrize("layout", ["plain", "combined", "heads"])
+def test_paged_ragged_chunks_of_whole_boxes(H, page, layout):
+    # as above on pages that TMA boxes fit, with sequences of several tiles and chunks of several items
+    paged_case([0, 1, 3, 5, 2, 70, 0, 9], [5, 1, 2, 0, 290, 400, 0, 9], H, page, "bf16", seed=H + page, lead=2, tail=3, layout=layout)
+
+
+@pytest.mark.parametrize("page", [32, 64, 16])
+def test_paged_decode_lengths_around_boxes_and_tiles(page):
+    L = [0, 1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 255, 256, 257, 400]
+    paged_case([1] * len(L), L, 128, page, "fp16", seed=page)
+    paged_case([2] * len(L), L, 48, page, "bf16", seed=page + 1)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_paged_bad_block_reads_as_zeros(page):
+    c = Paged([1, 1, 1], [300, 290, 77], 128, page, "bf16", 8)
+    c.table[1, 1], c.keys[1][page:2 * page] = c.nb, 0
+    c.table[2, 0], c.keys[2][:page] = -1, 0
+    a = B.MLAAttention(config(128, "bf16"), 3)
+    c.run(a)
+    assert a.status() == 10 and a.status() == 0
+    c.check()
+
+
 @pytest.mark.parametrize("H,n,L", [(16, 1, 5000), (128, 1, 5000), (128, 2, 3001), (3, 1, 20000), (24, 3, 4097)])
 def test_paged_long_context_is_split(H, n, L):
     paged_case([n], [L], H, 64, "bf16", seed=L)
@@ -472,6 +497,20 @@ def test_prompt_captured_and_repeated():
     q = torch.cat((qn, qp), -1)[0, :, :333].double().transpose(0, 1)
     ref, _, tol, _ = attend(q, k, v[0, :, :333].double(), 0, SCALE, dt)
     check("out", out[0, :, :333].transpose(0, 1), ref, tol)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_paged_waits_are_bounded(page):
+    """With a wait limit of 1 ns a call may give up: it ends, reports it, and the next handle is right."""
+    c = Paged([1, 2, 1], [3000, 70, 500], 128, page, "bf16", 21)
+    a = B.MLAAttention(config(128, "bf16"), c.T, spin_budget_ns=1)
+    for _ in range(2):
+        c.run(a)
+        assert a.status() in (0, 6) and a.status() == 0
+    b = B.MLAAttention(config(128, "bf16"), c.T)
+    c.run(b)
+    assert b.status() == 0
+    c.check()
 
 
 def test_waits_are_bounded():
