@@ -228,7 +228,7 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   const long long rows_per_seq = (long long)(a.T / a.num_seqs > 0 ? a.T / a.num_seqs : 1) * H;
   // 32 rows or fewer: the kernel built around the key stream (64 sequences of up to 4096 keys with 16 heads: 48 us, a
   // tcgen05 kernel for 128 rows 92 us); more: one pass of the tcgen05 kernel (64 sequences of up to 32768 keys with 128
-  // heads: 245 us, four passes of the other 1344 us)
+  // heads: 250 us, four passes of the other 1344 us)
   const bool tc = rows_per_seq > kPagedMmaRows;
   const int rows = tc ? kPagedPairRows : rows_per_seq <= 16 ? 16 : kPagedMmaRows;
   p.workers = tc ? h->num_sms / 2 : paged_mma_workers(rows, h->num_sms);

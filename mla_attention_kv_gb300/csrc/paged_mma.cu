@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
     const long long a = x0 > c.lo ? x0 : c.lo, b = x1 < c.hi ? x1 : c.hi;
     // this worker's tiles of KT keys
     constexpr int kSub = kKeyTile / KT;
-    const int t0 = c.tile_at(a, tiles) * kSub, t1 = min(c.tile_at(b, tiles) * kSub, (keys + KT - 1) / KT);
+    const int t0 = c.tile_at(a, tiles, R) * kSub, t1 = min(c.tile_at(b, tiles, R) * kSub, (keys + KT - 1) / KT);
     const bool whole = c.lo >= x0 && c.hi <= x1;
     const int s = c.s;
 

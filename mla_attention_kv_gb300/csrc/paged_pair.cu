@@ -31,8 +31,8 @@
 // Both key and value copies by TMA reached 30 bytes per cycle and SM (4500
 // cycles a tile), so the values come by cp.async, on the load/store path.
 // Requests into L2 ahead of the copies changed nothing.  Decode of 64
-// sequences of up to 32768 keys, 128 heads, bf16 (1.15 GB of cache): 245 us,
-// 4.7 TB/s; chunks of up to 512 tokens over 8192 keys: 1.00 ms, 1.45 PFLOP/s.
+// sequences of up to 32768 keys, 128 heads, bf16 (1.15 GB of cache): 250 us,
+// 4.6 TB/s; chunks of up to 512 tokens over 8192 keys: 1.01 ms, 1.44 PFLOP/s.
 //
 // Rescaling the output only when a maximum grew by more than 2^8: as in
 // prompt_tc.cu.
@@ -144,8 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
   auto span = [&](const PlanCursor& c, int* t0, int* t1) {
     const int keys = c.q.keys_of_item(c.j, kPpRows, H);
     const int tiles = (keys + kPpKeys - 1) / kPpKeys;
-    *t0 = c.tile_at(x0 > c.lo ? x0 : c.lo, tiles);
-    *t1 = c.tile_at(x1 < c.hi ? x1 : c.hi, tiles);
+    *t0 = c.tile_at(x0 > c.lo ? x0 : c.lo, tiles, kPpRows);
+    *t1 = c.tile_at(x1 < c.hi ? x1 : c.hi, tiles, kPpRows);
     return keys;
   };
 

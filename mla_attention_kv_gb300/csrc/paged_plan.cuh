@@ -16,7 +16,7 @@
 // first / last being the widths of its first and last item (the causal limit
 // grows along the chunk): exact for one item, an even slope for many.  A
 // position x inside item j is mapped to the key tile
-// (x - F(j)) * tiles / width, by both neighbours alike.
+// (x - F(j) - cost) * tiles / (width - cost), by both neighbours alike.
 #pragma once
 #include <stdint.h>
 
@@ -28,8 +28,12 @@ namespace mla {
 constexpr int kKeyTile = 64;
 // Width of an item beyond its key tiles (loading its queries, storing its
 // result), in key tiles.  128-row items: about 10 us for 0.95 us a key tile
-// (32 sequences of 100 to 2000 keys, 128 heads: 47 us at cost 1, 40 us at 8).
-__host__ __device__ constexpr int plan_item_cost(int R) { return R == kPagedPairRows ? 8 : 1; }
+// (32 sequences of 100 to 2000 keys, 128 heads: 47 us at cost 1, 33 at 10).
+// It stands before the item's first key tile, so that a worker that begins an
+// item pays for it and one that goes on with it does not (4 sequences of 20000
+// to 32768 keys, 2 tokens of 128 heads: 66 us, 71 with the cost spread over the
+// item's tiles).
+__host__ __device__ constexpr int plan_item_cost(int R) { return R == kPagedPairRows ? 10 : 1; }
 constexpr int kPlanThreadsMax = 512;
 
 struct PlanShared {
@@ -199,8 +203,12 @@ struct PlanCursor {
     return true;
   }
   // Key tile that position x of this item (lo <= x <= hi) stands for.
-  __host__ __device__ __forceinline__ int tile_at(long long x, int tiles) const {
-    const long long n = (x - lo) * tiles, d = hi - lo;
+  __host__ __device__ __forceinline__ int tile_at(long long x, int tiles, int R) const {
+    const long long d = hi - lo - plan_item_cost(R);
+    if (d < 1) return x < hi ? 0 : tiles;
+    const long long y = x - lo - plan_item_cost(R);
+    if (y <= 0) return 0;
+    const long long n = y * tiles;
     return n < (1u << 31) ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
   }
 };

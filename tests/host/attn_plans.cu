@@ -71,7 +71,7 @@ static void run(const std::vector<int>& n, const std::vector<int>& L, int H, int
         CHECK(keys >= 0 && keys <= c.q.L);
         const int tiles = (keys + kKeyTile - 1) / kKeyTile;
         const long long a = x0 > c.lo ? x0 : c.lo, b = x1 < c.hi ? x1 : c.hi;
-        Piece pc = {c.tile_at(a, tiles), c.tile_at(b, tiles), w, -1, c.lo >= x0 && c.hi <= x1};
+        Piece pc = {c.tile_at(a, tiles, R), c.tile_at(b, tiles, R), w, -1, c.lo >= x0 && c.hi <= x1};
         CHECK(pc.t0 >= 0 && pc.t0 <= pc.t1 && pc.t1 <= tiles);
         if (!pc.whole) {
           pc.slot = w * 2 + (c.lo < x0 ? 0 : 1);
