@@ -99,11 +99,12 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     fail(e, "cudaMalloc workspace");
     return MLA_ERR_NO_MEMORY;
   }
-  e = cudaMemset(h->ws, 0, 256);
+  e = cudaMemset(h->ws, 0, ml_off);  // (status and records)
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // a first call may come on a stream that does not wait for this one
   if (e != cudaSuccess) {
     cudaFree(h->ws);
     delete h;
-    return fail(e, "cudaMemset workspace");
+    return fail(e, "clear workspace");
   }
   unsigned char* base = static_cast<unsigned char*>(h->ws);
   h->status = reinterpret_cast<unsigned*>(base);

@@ -100,10 +100,8 @@ __global__ void __launch_bounds__(PmCfg<MT>::kThreads, PmCfg<MT>::kCtas) paged_m
   const long long total = plan_total(p, plan, R, blockIdx.x == 0);
   const int W = total > 0 ? plan_workers(total, p.workers, R) : 0;
   const int w = blockIdx.x;
-  if (w >= W) {
-    if (tid == 0) p.joins[w].rows = 0;
-    return;
-  }
+  if (tid == 0) plan_open_join(p, w);
+  if (w >= W) return;
   const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
 
   PlanCursor c;
@@ -356,7 +354,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p,
   const int w1 = blockIdx.x;
   const PagedJoin join = p.joins[w1];
   const int r = blockIdx.y * 8 + warp;
-  if (r >= join.rows) return;
+  if (r >= join.rows || !plan_join_fits(p, join, w1, R)) return;
   const int w2 = join.last_worker;
   const size_t row = (size_t)join.row + r;
   const int n = w2 - w1 + 1;

@@ -103,10 +103,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
   grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = plan_total(p, plan, kPpRows, blockIdx.x == 0);
   const int W = total > 0 ? plan_workers(total, p.workers, kPpRows) : 0;
-  if (w >= W) {
-    if (tid == 0) p.joins[w].rows = 0;
-    return;
-  }
+  if (tid == 0 && rank == 0) plan_open_join(p, w);  // (before any wait)
+  if (w >= W) return;
   const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
   PlanCursor first;
   first.seek(p, plan, kPpRows, x0);

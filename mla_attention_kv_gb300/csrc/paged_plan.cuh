@@ -213,6 +213,20 @@ struct PlanCursor {
   }
 };
 
+// The joining kernel runs whatever becomes of the workers, so a worker's
+// record is empty from before its first wait until plan_post_join: a worker
+// that gives up leaves nothing for it to do, and never what an earlier call
+// of the handle (perhaps a larger one) has left there.  The thread that posts.
+__host__ __device__ __forceinline__ void plan_open_join(const PagedParams& p, int w) { p.joins[w] = PagedJoin{0, 0, 0, 0}; }
+
+// Whether a record of worker w1 stays within this call's rows and workers.
+// Posted ones do, unless the lengths changed while the call ran and its
+// workers saw different ones.
+__host__ __device__ __forceinline__ bool plan_join_fits(const PagedParams& p, const PagedJoin& j, int w1, int R) {
+  return j.row >= 0 && j.rows >= 0 && j.rows <= R && (long long)j.row + j.rows <= (long long)p.T * p.heads &&
+         j.last_worker >= w1 && j.last_worker < p.workers;
+}
+
 // Worker w's record for the joining kernel, made at the last item of its
 // range: the rows of that item if the item begins with it and goes on with
 // others.  One thread.
