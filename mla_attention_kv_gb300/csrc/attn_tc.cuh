@@ -39,6 +39,16 @@ __device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity, vola
   return __all_sync(~0u, at_wait(bar, parity, abort, budget, status));
 }
 
+// How often slot i of a ring of `slots` has been filled after `fills` fills in
+// turn.  A role that gives up leaves a ring at any place; the barriers of a
+// slot filled n > 0 times are then waited on with parity (n - 1) & 1: that of
+// its last fill, whose phase is the current one or has just completed.  (A
+// parity counted in whole rounds can name the phase before it, which is
+// complete, and the wait returns with a copy still in flight.)
+__host__ __device__ constexpr uint32_t ring_uses(uint32_t fills, uint32_t slots, uint32_t i) {
+  return (fills + slots - 1 - i) / slots;
+}
+
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));

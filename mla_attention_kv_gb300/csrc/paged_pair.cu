@@ -162,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
   if (kBox && warp == 4) {
     // ============================================================ keys, by TMA
     const int zero_row = p.nblocks * p.page;  // past the end of the map: reads as zeros
-    uint32_t u = 0;                           // tiles copied
+    uint32_t u = 0, fills = 0;                // tiles, slots filled
     bool ok = true;
     PlanCursor c = first;
     for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
@@ -192,25 +192,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
               tma_load_2d_pair(d + j * kBlk, blk < 8 ? &a.lat : &a.kpe, blk < 8 ? blk * 64 : 0, row, b);
             }
           }
+          ++fills;
         }
         row = next;
       }
     }
-    // every copy has landed, and every release of a slot has arrived, before the CTAs may exit
+    // Every copy has landed, and every release of a slot has arrived, before the CTAs may exit.  After a wait that ran
+    // out the two CTAs may have filled different numbers of slots: a fill that the other CTA has not matched is never
+    // released, and its waits take the whole limit, in which it lands.
     __syncwarp();
     const uint64_t t0 = globaltimer_ns();
     auto drain = [&](uint64_t* b, uint32_t par) {
       const uint64_t spent = globaltimer_ns() - t0, limit = drain_budget(p.budget_ns);
       mbar_wait_bounded(bar(b), par, spent < limit ? limit - spent : 0);
     };
-    for (int i = 0; i < kKSlots && u > 0; ++i) {
-      if (rank == 0) drain(&sh->kfull[i], (u - 1) & 1);
-      drain(&sh->kempty[i], (u - 1) & 1);
+    for (int i = 0; i < kKSlots; ++i) {
+      const uint32_t n = ring_uses(fills, kKSlots, i);
+      if (n == 0) break;
+      if (rank == 0) drain(&sh->kfull[i], (n - 1) & 1);
+      drain(&sh->kempty[i], (n - 1) & 1);
     }
   } else if (!kBox && warp > 9) {
     // ============================================================ keys, by cp.async: 32 of this CTA's 64 to a warp
     const int part = rank * 2 + warp - 10;  // which 32 keys of a tile
-    uint32_t u = 0;
+    uint32_t u = 0, fills = 0;
     bool ok = true;
     PlanCursor c = first;
     for (bool more = true; more && c.lo < x1 && ok; more = c.next(p, kPpRows)) {
@@ -232,6 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
             if (lane < 24) cp_async16(d + r * 128 + (((lane & 7) ^ (r & 7)) * 16), src + (size_t)max(cr, 0) * rs, cr < 0 ? 0 : 16);
           }
           cp_async_commit();
+          ++fills;
           if (g > 0) {  // the slot before is there
             cp_async_wait<1>();
             tc::fence_proxy_async_smem();
@@ -246,8 +252,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
         if (ok && lane == 0) tc::arrive_operands(tc::mapa(bar(&sh->kfull[kKSlots - 1]), 0));
       }
     }
-    for (int i = 0; i < kKSlots && u > 0; ++i)  // the last releases have arrived
-      if (!mbar_wait_bounded(bar(&sh->kempty[i]), (u - 1) & 1, drain_budget(p.budget_ns))) break;
+    for (int i = 0; i < kKSlots; ++i) {  // the last releases have arrived
+      const uint32_t n = ring_uses(fills, kKSlots, i);
+      if (n == 0 || !mbar_wait_bounded(bar(&sh->kempty[i]), (n - 1) & 1, drain_budget(p.budget_ns))) break;
+    }
   } else if (warp > 5) {
     // ============================================================ values, by cp.async: a warp fills a slot
     const int slot = warp - 6;
