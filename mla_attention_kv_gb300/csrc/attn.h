@@ -93,7 +93,7 @@ struct PromptParams {
   const int32_t* cu;  // packed sequences [nseq + 1] over the s tokens of batch 0, or null
   unsigned* status;
   int b, s, nseq, heads, kv_heads, causal;
-  int clusters;  // CTA pairs that share the work
+  int ctas;  // CTAs that share the work
   float scale_log2;
   unsigned long long budget_ns;
 };

@@ -274,7 +274,7 @@ mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cu
   DeviceGuard g(h->device);
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
   p.lse = a.lse; p.cu = a.cu_seqlens; p.status = h->status; p.b = a.b; p.s = a.s; p.nseq = a.cu_seqlens ? a.num_seqs : a.b;
-  p.heads = H; p.kv_heads = KH; p.causal = a.causal; p.clusters = h->num_sms / 2; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
+  p.heads = H; p.kv_heads = KH; p.causal = a.causal; p.ctas = h->num_sms; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   cudaError_t e = prompt_tc_launch(h->cfg.dtype == MLA_BF16, p, &h->prompt_maps, stream);
   if (e != cudaSuccess) return fail(e, "prompt attention launch");
   h->last_launches = 1;

@@ -1,11 +1,11 @@
-// prompt_plan.cuh -- which query block of which sequence and head a cluster
-// of the prompt attention works on.
+// prompt_plan.cuh -- which query block of which sequence and head a CTA of
+// the prompt attention works on.
 //
 // Items are (head, block of query rows of a sequence), head after head, so
-// that the clusters at work share few heads' keys in L2; the blocks of a
+// that the CTAs at work share few heads' keys in L2; the blocks of a
 // sequence are taken from its end, where a causal block has the most keys.
-// Cluster c of C takes items c, 2C - 1 - c, 2C + c, 4C - 1 - c, ...: the
-// direction alternates so that no cluster always gets the longer blocks.
+// CTA c of C takes items c, 2C - 1 - c, 2C + c, 4C - 1 - c, ...: the
+// direction alternates so that no CTA always gets the longer blocks.
 #pragma once
 #include "attn.h"
 #include "common.cuh"
@@ -60,7 +60,7 @@ __device__ __forceinline__ int prompt_plan(const PromptParams& p, PromptPlan* ps
   return ps->base[nt];
 }
 
-// Item of cluster c of C in its k-th round.
+// Item of CTA c of C in its k-th round.
 __device__ __forceinline__ long long prompt_item(int c, int C, int k) {
   return (long long)k * C + ((k & 1) ? C - 1 - c : c);
 }

@@ -9,10 +9,12 @@
 // for their product with the values (the operand type of the MMA), the sum
 // takes them before that.
 //
-// A cluster of two CTAs takes 256 query rows of a head, each CTA 128 of them;
-// both need the same keys and values, so each loads half of every stage and
-// multicasts it to both (L2 would have to deliver 55 bytes per cycle and SM
-// otherwise).
+// A CTA takes 128 query rows of a head and loads their keys and values by
+// itself, 80 KB a tile, mostly from L2 (hit rate 83 %): neighbours take
+// neighbouring blocks of a head, so a tile is wanted by several at about the
+// same time.  Copies shared by a pair of CTAs were worth 1 to 4 % (8192 tokens,
+// 128 heads: 1.86 to 1.89 ms) and would bind the operator to memory of the
+// GPU that it runs on.
 //
 // Tensor memory: scores S0, S1 (128 columns each, by the parity of the key
 // tile; the rounded weights overwrite the first 64 columns of theirs and are
@@ -24,17 +26,18 @@
 // an mbarrier takes a thread about 100 cycles even when the phase is complete,
 // so finer slots cost more than they hide.
 //
-// What bounds it (one prompt of 8192, 128 heads, causal, bf16: 1.88 ms, 1.46
-// PFLOP/s): about 1810 cycles per tile and 13000 per item around its tiles,
-// the tensor pipe busy 58 % of the time.  A tile's way is scores, softmax,
-// weights announced, output, with two tiles in flight.  Measured and slower:
-// the pair on the 2-SM MMA (half the shared-memory traffic, but every
-// announcement crosses the CTAs) 1.99 ms; four softmax warps per 32 rows
-// 2.10 ms; tiles of 64 keys, four in flight, 2.10 ms.
+// What bounds it (one prompt of 8192, 128 heads, causal, bf16: 1.91 to 1.93
+// ms, 1.43 PFLOP/s): 0.97 us per tile (about 1900 cycles), 1.8 us more per item
+// and 17 us per call (fitted to non-causal prompts of 512 to 4096 tokens), the tensor
+// pipe busy 60 % of the time.  A tile's way is scores, softmax, weights
+// announced, output, with two tiles in flight.  Measured and slower: pairs of
+// CTAs on the 2-SM MMA (half the shared-memory traffic, but every announcement
+// crosses the CTAs) 1.99 ms; and, with pairs that shared their copies, four
+// softmax warps per 32 rows 2.10 ms; tiles of 64 keys, four in flight, 2.10 ms.
 //
 // MMA order: scores of tile i + 1, then output of tile i, so the softmax of
 // a tile runs under the scores of the next and the output of the previous.
-// The clusters are persistent: copies and scores of the next item begin while
+// The CTAs are persistent: copies and scores of the next item begin while
 // the last one's result is stored.
 //
 // The output is rescaled only when a row's maximum has grown by more than 2^8
@@ -59,7 +62,6 @@ namespace {
 
 constexpr int kPtThreads = kPromptPlanThreads;
 constexpr int kPtTile = 128;   // query rows per CTA, keys per tile
-constexpr int kPtRows = 256;   // query rows per cluster
 constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kBlock = 16384;  // 128 keys x 64 columns
 constexpr uint32_t kKBytes = 3 * kBlock, kVBytes = 2 * kBlock;
@@ -87,7 +89,7 @@ struct PtArgs {
 };
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
+__global__ void __launch_bounds__(kPtThreads, 1)
     prompt_tc_kernel(const __grid_constant__ PtArgs a) {
   using E = Elem<T>;
   const PromptParams& p = a.p;
@@ -98,39 +100,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   volatile int* abort = &sh->abort;
   auto bar = [](uint64_t* b) { return smem_u32(b); };
-  const int rank = blockIdx.x & 1;  // (clusters are pairs of neighbours along x)
 
-  // the items of this cluster: key tiles n of this CTA's 128 rows, nt of the pair (the second CTA may have none)
-  const int blocks = prompt_plan(p, &sh->plan, kPtRows, blockIdx.x == 0);
-  const int cluster = blockIdx.x >> 1;
+  // the items of this CTA, with n key tiles each (n > 0: an item has a row, and a row sees a key)
+  const int blocks = prompt_plan(p, &sh->plan, kPtTile, blockIdx.x == 0);
+  const int cta = blockIdx.x;
   const long long items = (long long)blocks * p.heads;
-  if (cluster >= items) return;
+  if (cta >= items) return;
   struct Item {
     PromptPlace pl;
-    int n, nt;
+    int n;
   };
   auto item_at = [&](long long x) {
     Item it;
-    it.pl = prompt_place(p, &sh->plan, x, blocks, kPtRows);
-    auto tiles_of = [&](int w) {
-      const int r0 = it.pl.row0 + w * kPtTile;
-      if (r0 >= it.pl.len) return 0;
-      const int end = p.causal ? min(it.pl.len, r0 + kPtTile) : it.pl.len;
-      return (end + kPtTile - 1) / kPtTile;
-    };
-    it.n = tiles_of(rank);
-    it.nt = max(tiles_of(0), tiles_of(1));
+    it.pl = prompt_place(p, &sh->plan, x, blocks, kPtTile);
+    const int end = p.causal ? min(it.pl.len, it.pl.row0 + kPtTile) : it.pl.len;
+    it.n = (end + kPtTile - 1) / kPtTile;
     return it;
   };
 
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(bar(&sh->kfull[i]), 1);
-      mbar_init(bar(&sh->kempty[i]), 2);  // the MMA warps of both CTAs
+      mbar_init(bar(&sh->kempty[i]), 1);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(bar(&sh->vfull[i]), 1);
-      mbar_init(bar(&sh->vempty[i]), 2);
+      mbar_init(bar(&sh->vempty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&sh->sfull[i]), 1);
@@ -148,7 +143,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   if (warp == 9) tc::tmem_alloc(smem_u32(&sh->tmem), 512);
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();  // both CTAs' barriers are initialised before any copy or commit reaches them
   tc::fence_after_sync();
   const uint32_t tmem = uniform(sh->tmem);
 
@@ -158,39 +152,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       int nk = 0, nv = 0;  // stages filled
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const long long x = prompt_item(cluster, p.clusters, k);
+        const long long x = prompt_item(cta, p.ctas, k);
         if (x >= items) break;
         const Item it = item_at(x);
-        const int hk = it.pl.head / (p.heads / p.kv_heads), t0 = it.pl.begin + rank * 64;
-        // this CTA's 64 rows of every block go to both CTAs
+        const int hk = it.pl.head / (p.heads / p.kv_heads), t0 = it.pl.begin;
         auto keys = [&](int i) {
-          const uint32_t s = nk % kKStages, b = bar(&sh->kfull[s]), d = sbase + s * kKBytes + rank * (kBlock / 2);
+          const uint32_t s = nk % kKStages, b = bar(&sh->kfull[s]), d = sbase + s * kKBytes;
           ok = ok && at_wait(bar(&sh->kempty[s]), ((nk / kKStages) & 1) ^ 1, abort, p.budget_ns, p.status);
           if (!ok) return;
           const int tok = t0 + i * kPtTile;
           mbar_arrive_expect_tx(b, kKBytes);
-          tma_load_4d_multicast(d, &a.kn, 0, tok, hk, it.pl.batch, b, 3);
-          tma_load_4d_multicast(d + kBlock, &a.kn, 64, tok, hk, it.pl.batch, b, 3);
-          tma_load_4d_multicast(d + 2 * kBlock, &a.kp, 0, tok, 0, it.pl.batch, b, 3);
+          tma_load_4d(d, &a.kn, 0, tok, hk, it.pl.batch, b);
+          tma_load_4d(d + kBlock, &a.kn, 64, tok, hk, it.pl.batch, b);
+          tma_load_4d(d + 2 * kBlock, &a.kp, 0, tok, 0, it.pl.batch, b);
           ++nk;
         };
         auto values = [&](int i) {
-          const uint32_t s = nv % kVStages, b = bar(&sh->vfull[s]), d = sbase + kPtV + s * kVBytes + rank * (kBlock / 2);
+          const uint32_t s = nv % kVStages, b = bar(&sh->vfull[s]), d = sbase + kPtV + s * kVBytes;
           ok = ok && at_wait(bar(&sh->vempty[s]), ((nv / kVStages) & 1) ^ 1, abort, p.budget_ns, p.status);
           if (!ok) return;
           const int tok = t0 + i * kPtTile;
           mbar_arrive_expect_tx(b, kVBytes);
-          tma_load_4d_multicast(d, &a.v, 0, tok, hk, it.pl.batch, b, 3);
-          tma_load_4d_multicast(d + kBlock, &a.v, 64, tok, hk, it.pl.batch, b, 3);
+          tma_load_4d(d, &a.v, 0, tok, hk, it.pl.batch, b);
+          tma_load_4d(d + kBlock, &a.v, 64, tok, hk, it.pl.batch, b);
           ++nv;
         };
         keys(0);
-        for (int i = 0; i < it.nt && ok; ++i) {
-          if (i + 1 < it.nt) keys(i + 1);
+        for (int i = 0; i < it.n && ok; ++i) {
+          if (i + 1 < it.n) keys(i + 1);
           values(i);
         }
       }
-      // every copy into this CTA, and every release of a stage by the peer, has landed before the cluster may exit
+      // every copy has landed, and every release of a stage has arrived, before the CTA may exit
       const uint64_t t0 = globaltimer_ns();
       auto drain = [&](uint64_t* b, int use, int stages) {
         const uint64_t spent = globaltimer_ns() - t0, limit = drain_budget(p.budget_ns);
@@ -219,61 +212,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         return ok;
       };
       uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stage and phase of the rings
-      uint32_t g_qk = 0, g_pv = 0, mine = 0;    // tiles done, items with rows
-      auto qk = [&](bool own) {  // S = Q K^T (past this CTA's last tile: release the stage only)
+      uint32_t g_qk = 0, g_pv = 0, mine = 0;    // tiles done, items
+      auto qk = [&]() {  // S = Q K^T
         if (!wait(&sh->kfull[ks], kp)) return;
-        if (own) {
-          const uint64_t bd = dk + ks * (kKBytes >> 4);
-          const uint32_t d = tmem + (g_qk & 1) * 128;
+        const uint64_t bd = dk + ks * (kKBytes >> 4);
+        const uint32_t d = tmem + (g_qk & 1) * 128;
 #pragma unroll 1
-          for (int c = 0; c < 3; ++c)
+        for (int c = 0; c < 3; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_f16_ts(d, tmem + kTmQ + c * 32 + k * 8, bd + c * (kBlock >> 4) + 2 * k, id_qk, c > 0 || k > 0);
-          tc::commit(bar(&sh->sfull[g_qk & 1]));
-          ++g_qk;
-        }
-        tc::commit_multicast(bar(&sh->kempty[ks]), 3);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f16_ts(d, tmem + kTmQ + c * 32 + k * 8, bd + c * (kBlock >> 4) + 2 * k, id_qk, c > 0 || k > 0);
+        tc::commit(bar(&sh->sfull[g_qk & 1]));
+        ++g_qk;
+        tc::commit(bar(&sh->kempty[ks]));
         if (++ks == kKStages) {
           ks = 0;
           kp ^= 1;
         }
       };
-      auto pv = [&](bool own, bool first, bool last) {  // O (+)= P V
+      auto pv = [&](bool first, bool last) {  // O (+)= P V
         if (!wait(&sh->vfull[vs], vp)) return;
-        if (own) {
-          // (the item before this one has been read from O)
-          if (first && mine > 0 && !wait(&sh->ofree, (mine - 1) & 1)) return;
-          if (!wait(&sh->pfull[g_pv & 1], (g_pv >> 1) & 1)) return;
-          tc::fence_after_sync();
-          const uint64_t bd = dv + vs * (kVBytes >> 4);
-          const uint32_t pa = tmem + (g_pv & 1) * 128;
+        // (the item before this one has been read from O)
+        if (first && mine > 0 && !wait(&sh->ofree, (mine - 1) & 1)) return;
+        if (!wait(&sh->pfull[g_pv & 1], (g_pv >> 1) & 1)) return;
+        tc::fence_after_sync();
+        const uint64_t bd = dv + vs * (kVBytes >> 4);
+        const uint32_t pa = tmem + (g_pv & 1) * 128;
 #pragma unroll 2
-          for (int k = 0; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, !first || k > 0);
-          tc::commit(bar(&sh->pvdone));
-          if (last) tc::commit(bar(&sh->olast));
-          ++g_pv;
-        }
-        tc::commit_multicast(bar(&sh->vempty[vs]), 3);
+        for (int k = 0; k < 8; ++k) tc::mma_f16_ts(tmem + kTmO, pa + k * 8, bd + k * 128, id_pv, !first || k > 0);
+        tc::commit(bar(&sh->pvdone));
+        if (last) tc::commit(bar(&sh->olast));
+        ++g_pv;
+        tc::commit(bar(&sh->vempty[vs]));
         if (++vs == kVStages) {
           vs = 0;
           vp ^= 1;
         }
       };
       for (int k = 0; ok; ++k) {
-        const long long x = prompt_item(cluster, p.clusters, k);
+        const long long x = prompt_item(cta, p.ctas, k);
         if (x >= items) break;
         const Item it = item_at(x);
-        if (it.n > 0) {
-          if (!wait(&sh->qready, mine & 1)) break;
-          tc::fence_after_sync();
+        if (!wait(&sh->qready, mine & 1)) break;
+        tc::fence_after_sync();
+        qk();
+        for (int i = 0; i < it.n && ok; ++i) {
+          if (i + 1 < it.n) qk();
+          if (ok) pv(i == 0, i == it.n - 1);
         }
-        qk(it.n > 0);
-        for (int i = 0; i < it.nt && ok; ++i) {
-          if (i + 1 < it.nt) qk(i + 1 < it.n);
-          if (ok) pv(i < it.n, i == 0, i == it.n - 1);
-        }
-        mine += it.n > 0;
+        ++mine;
       }
       // every MMA issued so far has completed before TMEM is released
       tc::commit(bar(&sh->done));
@@ -292,12 +279,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       const int u = hf * 12 + i;
       const bool pe = u >= 16;
       const PromptTensor& t = pe ? p.q_pe : p.q_nope;
-      const int qi = it.pl.row0 + rank * kPtTile + r;
+      const int qi = it.pl.row0 + r;
       const int tok = it.pl.begin + (qi < it.pl.len ? qi : 0);
       return reinterpret_cast<const uint4*>(static_cast<const T*>(t.ptr) + (size_t)it.pl.batch * t.sb + (size_t)it.pl.head * t.sh + (size_t)tok * t.st) + (pe ? u - 16 : u);
     };
     auto load_q = [&](const Item& it) {
-      const bool live = it.pl.row0 + rank * kPtTile + r < it.pl.len;
+      const bool live = it.pl.row0 + r < it.pl.len;
       uint4 v[12];
 #pragma unroll
       for (int i = 0; i < 12; ++i) v[i] = live ? *q_unit(it, i) : make_uint4(0, 0, 0, 0);
@@ -314,21 +301,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (lane == 0) mbar_arrive(bar(&sh->pair[q]));
       return at_wait_warp(bar(&sh->pair[q]), meets++ & 1, abort, p.budget_ns, p.status);
     };
-    uint32_t g = 0, gv = 0, mine = 0;  // tiles of this CTA, tiles of the pair, items with rows
-    Item it = item_at(prompt_item(cluster, p.clusters, 0));
-    if (it.n > 0) load_q(it);
+    uint32_t g = 0, mine = 0;  // tiles, items done
+    Item it = item_at(prompt_item(cta, p.ctas, 0));
+    load_q(it);
     for (int round = 0; ok; ++round) {
-      const long long xn = prompt_item(cluster, p.clusters, round + 1);
+      const long long xn = prompt_item(cta, p.ctas, round + 1);
       const bool more = xn < items;
       Item nx = it;
       if (more) {
         nx = item_at(xn);
-        if (nx.n > 0)
-          for (int i = 0; i < 12; i += 4)  // the next queries' lines into L2
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(q_unit(nx, i)));
+        for (int i = 0; i < 12; i += 4)  // the next queries' lines into L2
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q_unit(nx, i)));
       }
       const int n = it.n;
-      const int qi = it.pl.row0 + rank * kPtTile + r;  // query's token in its sequence
+      const int qi = it.pl.row0 + r;  // query's token in its sequence
       const bool live = qi < it.pl.len;
       float m = -INFINITY;  // maximum the weights are relative to (raw score units)
       float l = 0.f;        // sum over this thread's keys
@@ -398,8 +384,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         const int valid = it.pl.len - i * kPtTile;
         if (valid < kPtTile) {
           // value rows past the sequence's end: whole 128-byte rows, so the swizzle does not matter
-          const uint32_t use = gv + i, vs = use % kVStages;
-          if (!at_wait_warp(bar(&sh->vfull[vs]), (use / kVStages) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
+          const uint32_t vs = g % kVStages;
+          if (!at_wait_warp(bar(&sh->vfull[vs]), (g / kVStages) & 1, abort, p.budget_ns, p.status)) { ok = false; break; }
           for (int x = tid; x < (kPtTile - valid) * 16; x += 256)
             *reinterpret_cast<uint4*>(smem + kPtV + vs * kVBytes + ((x >> 3) & 1) * kBlock + (valid + x / 16) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           tc::fence_proxy_async_smem();
@@ -412,10 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         l += (a0 + a1) + (b0 + b1);
       }
       if (!ok) break;
-      gv += it.nt;
       // the next item's queries go in while the last output MMA runs (all score MMAs of this one are done)
-      if (more && nx.n > 0) load_q(nx);
-      if (n > 0) {
+      if (more) load_q(nx);
+      {
         const uint32_t par = meets & 1;
         sh->row[par][hf][r] = l;
         // (a barrier of its own: a parity says which of two neighbouring phases is done, and this warp has not followed
@@ -454,7 +439,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
-  tc::cluster_sync();  // the peer's copies and commits into this CTA are done
 }
 
 template <typename T>
@@ -471,7 +455,7 @@ cudaError_t launch(const PromptParams& p, PromptMaps* m, cudaStream_t stream) {
     const CUtensorMapDataType dt = Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     for (int i = 0; i < 3; ++i) {
       const PromptTensor& t = *src[i];
-      if (!encode_tmap_4d_rows(&m->map[i], dt, t.ptr, width[i], p.s, heads[i], p.b, t.st, heads[i] > 1 ? t.sh : width[i], t.sb, kPtTile / 2))
+      if (!encode_tmap_4d_rows(&m->map[i], dt, t.ptr, width[i], p.s, heads[i], p.b, t.st, heads[i] > 1 ? t.sh : width[i], t.sb, kPtTile))
         return cudaErrorInvalidValue;
     }
     m->key = key;
@@ -480,9 +464,9 @@ cudaError_t launch(const PromptParams& p, PromptMaps* m, cudaStream_t stream) {
   PtArgs a;
   a.kn = m->map[0]; a.kp = m->map[1]; a.v = m->map[2];
   a.p = p;
-  const long long items = (long long)prompt_blocks(p, kPtRows) * p.heads;
-  if (items < a.p.clusters) a.p.clusters = (int)items;
-  prompt_tc_kernel<T><<<2 * a.p.clusters, kPtThreads, kPtSmem, stream>>>(a);
+  const long long items = (long long)prompt_blocks(p, kPtTile) * p.heads;
+  if (items < a.p.ctas) a.p.ctas = (int)items;
+  prompt_tc_kernel<T><<<a.p.ctas, kPtThreads, kPtSmem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -34,14 +34,13 @@ bool encode_tmap_4d_rows(CUtensorMap* map, CUtensorMapDataType dtype, const void
                          uint32_t box1);
 
 #ifdef __CUDACC__
-// Tiled 4-D load of one box into the shared memory of every CTA in `mask` (at one offset),
-// its bytes counted on the barrier at `bar`'s offset in each of them.
-__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                                      int w, uint32_t bar, uint16_t mask) {
+// Tiled 4-D load of one box; completion is counted in bytes on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "h"(mask)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 // Tiled 2-D load of one box into shared memory; completion is counted in
