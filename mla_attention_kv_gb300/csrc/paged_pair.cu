@@ -340,7 +340,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPpThreads<kBox>, 1)
         int t0, t1;
         span(c, &t0, &t1);
         if (t0 >= t1) continue;
-        if (!wait(&sh->qready, item++ & 1)) break;
+        ok = item == 0 ? at_wait_poll<true>(bar(&sh->qready), 0, abort, p.budget_ns, p.status) : wait(&sh->qready, item & 1);
+        if (!ok) break;
+        ++item;
         tc::fence_after_sync();
         qk();
         for (int t = t0; t < t1 && ok; ++t) {

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const uint32_t id_pv = tc::idesc_f16(E::kBf16, 128, 128, false, true);
       const uint64_t dk = tc::sdesc_sw128(sbase, 16, 1024);             // K-major: keys
       const uint64_t dv = tc::sdesc_sw128(sbase + kPtV, kBlock, 1024);  // MN-major: values
-      bool ok = true;
+      bool ok = at_wait_poll(bar(&sh->qready), 0, abort, p.budget_ns, p.status);
       auto wait = [&](uint64_t* b, uint32_t par) {
         ok = ok && at_wait(bar(b), par, abort, p.budget_ns, p.status);
         return ok;

@@ -6,7 +6,8 @@ import torch
 from mla_attention_kv_gb300 import binding as B
 from mla_attention_kv_gb300 import build as BLD
 
-from test_attn_gpu import Paged, config
+from attn_ref import attend, check
+from test_attn_gpu import SCALE, Paged, config, gen, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -34,7 +35,7 @@ def test_a_call_that_gives_up_writes_only_its_output(page):
     big.run(a)
     assert a.status() == 0
     small.run(a)
-    assert a.status() in (0, 6) and a.status() == 0
+    assert a.status() == 6 and a.status() == 0
     assert (out[small.T:] == 7.0).all() and (lse[small.T:] == 7.0).all()
     big.out.fill_(0)
     big.run(a)
@@ -44,3 +45,48 @@ def test_a_call_that_gives_up_writes_only_its_output(page):
     small.run(b)
     assert b.status() == 0
     small.check()
+
+
+@pytest.mark.parametrize("H,page", [(128, 16), (128, 64), (48, 32)])
+@pytest.mark.parametrize("n", [1, 40])
+def test_paged_limit_is_kept_and_reported(H, page, n):
+    """A limit of 1 ns runs out in every call of the pair kernel (the MMA thread has to wait for the queries at least),
+    the status says so once, and a handle with the usual limit is right afterwards."""
+    c = Paged([n] * 8, [3000, 70, 500, 40, 41, 999, 64, 1280], H, page, "bf16", 21)
+    a = B.MLAAttention(config(H, "bf16"), c.T, spin_budget_ns=1)
+    for _ in range(2):
+        c.run(a)
+        assert a.status() == 6 and a.status() == 0
+    b = B.MLAAttention(config(H, "bf16"), c.T)
+    c.run(b)
+    assert b.status() == 0
+    c.check()
+
+
+def test_prompt_limit_is_kept_and_reported():
+    g = gen(1)
+    x, p = rnd(g, 1, 4, 900, 128, dtype=torch.bfloat16), rnd(g, 1, 4, 900, 64, dtype=torch.bfloat16)
+    q, v = rnd(g, 1, 4, 900, 128, dtype=torch.bfloat16), rnd(g, 1, 4, 900, 128, dtype=torch.bfloat16)
+    guard = torch.full((1, 4, 1200, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[:, :, :900]
+    a = B.MLAAttention(config(4, "bf16"), 900, spin_budget_ns=1)
+    for causal in (True, False):
+        a.run_prompt(q, p, x, p[:, :1], v, out, causal=causal)
+        assert a.status() == 6 and a.status() == 0
+    b = B.MLAAttention(config(4, "bf16"), 900)
+    b.run_prompt(q, p, x, p[:, :1], v, out)
+    assert b.status() == 0
+    assert (guard[:, :, 900:] == 7.0).all()
+    k = torch.cat((x, p[:, :1].expand(1, 4, 900, 64)), -1)[0].double()
+    qq = torch.cat((q, p), -1)[0].double().transpose(0, 1)
+    ref, _, tol, _ = attend(qq, k, v[0].double(), 0, SCALE, torch.bfloat16)
+    check("out", out[0].transpose(0, 1), ref, tol)
+
+
+def test_a_limit_of_milliseconds_is_not_run_out_by_ordinary_waits():
+    """20 ms: far over any wait of a call of a few hundred microseconds, far under the default."""
+    c = Paged([1] * 8, [3000, 70, 500, 40, 41, 999, 64, 1280], 128, 64, "bf16", 22)
+    a = B.MLAAttention(config(128, "bf16"), c.T, spin_budget_ns=20_000_000)
+    c.run(a)
+    assert a.status() == 0
+    c.check()
