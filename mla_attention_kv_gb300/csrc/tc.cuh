@@ -144,11 +144,14 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cl_addr) {
 }
 // Arrive on an mbarrier of the cluster for shared-memory operands of a pair MMA
 // that this CTA's threads have written and passed through
-// fence.proxy.async: they are read by this SM's own tensor core, so the
-// release need not reach beyond the CTA.  (At cluster scope it waits for
-// everything else the SM has under way: 2000 cycles beside copies and MMAs.)
+// fence.proxy.async.  The release reaches the waiting thread of the other CTA,
+// but orders shared memory alone: an arrive.release.cluster waits for
+// everything else the SM has under way, 2000 cycles beside copies and MMAs.
 __device__ __forceinline__ void arrive_operands(uint32_t cl_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr)
+      : "memory");
 }
 // Relaxed arrive at cluster scope: for releasing tensor memory, whose reads
 // are complete once tcgen05.wait::ld has returned (nothing else to order --

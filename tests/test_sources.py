@@ -17,3 +17,9 @@ def test_no_bulk_copy_multicasts():
         for m in re.finditer(r"cp\.async\.bulk[^;]*", text):
             assert "multicast" not in m.group(0), (os.path.basename(f), m.group(0))
         assert "tma_load_4d_multicast" not in text
+
+
+def test_arrivals_at_another_cta_are_released_to_it():
+    """A release of CTA scope does not reach a waiter in another CTA of the cluster."""
+    for f in glob.glob(os.path.join(ROOT, "mla_attention_kv_gb300", "csrc", "*")):
+        assert "arrive.release.cta.shared::cluster" not in open(f).read(), os.path.basename(f)
