@@ -45,6 +45,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // overlapping (the stride of a dimension of size 1 is not read).
 bool stride_ok(int stride, int width, bool used) { return !used || (stride >= width && stride % 8 == 0); }
 
+// Reads and clears the status word in one step (the second word keeps what was
+// read): calls that overlap on another stream may set bits meanwhile.
+__global__ void take_status_kernel(unsigned* status) { status[1] = atomicExch(status, 0u); }
+
 // Makes the handle's device current for the length of a call.
 struct DeviceGuard {
   int before = -1;
@@ -139,12 +143,11 @@ mla_status mla_attn_status(mla_attn* h, cudaStream_t stream) {
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return fail(e, "cudaStreamSynchronize");
   unsigned st = 0;
-  e = cudaMemcpy(&st, h->status, sizeof(unsigned), cudaMemcpyDeviceToHost);
+  take_status_kernel<<<1, 1, 0, stream>>>(h->status);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, h->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return fail(e, "read status");
-  if (st) {
-    e = cudaMemset(h->status, 0, 256);
-    if (e != cudaSuccess) return fail(e, "clear status");
-  }
   if (st & kStatusBadPosition) return MLA_ERR_BAD_POSITION;
   if (st & kStatusTimeout) return MLA_ERR_DEVICE_TIMEOUT;
   if (st & kStatusBadSlot) return MLA_ERR_BAD_SLOT;

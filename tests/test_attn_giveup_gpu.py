@@ -83,6 +83,28 @@ def test_prompt_limit_is_kept_and_reported():
     check("out", out[0].transpose(0, 1), ref, tol)
 
 
+def test_status_reads_one_stream_and_loses_nothing():
+    """The status call waits for its own stream alone, and clears what it reads before it returns: every bad slot of a
+    side stream is reported once, while the default stream is busy."""
+    a = B.MLAAttention(config(2, "fp16"), 1)
+    kv = torch.randn(1, 576, device="cuda").half()
+    c = a.alloc_latent_caches(1, 4)
+    bad = torch.tensor([4], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a.append_latent(kv[:, :512], kv[:, 512:], None, None, None, None, bad, **c, stream=side)
+    assert a.status(side) == 10  # (kernels are loaded)
+    torch.cuda._sleep(2_000_000_000)  # about a second
+    busy = torch.cuda.Event()
+    busy.record()
+    for _ in range(50):
+        a.append_latent(kv[:, :512], kv[:, 512:], None, None, None, None, bad, **c, stream=side)
+        assert a.status(side) == 10
+    assert a.status(side) == 0
+    assert not busy.query()
+    torch.cuda.synchronize()
+
+
 def test_a_limit_of_milliseconds_is_not_run_out_by_ordinary_waits():
     """20 ms: far over any wait of a call of a few hundred microseconds, far under the default."""
     c = Paged([1] * 8, [3000, 70, 500, 40, 41, 999, 64, 1280], 128, 64, "bf16", 22)
