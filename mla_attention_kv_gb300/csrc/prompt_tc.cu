@@ -41,15 +41,15 @@
 // the last one's result is stored.
 //
 // The output is rescaled only when a row's maximum has grown by more than 2^8
-// since the last time (weights are then at most 2^8: the sums stay exact to
-// fp32 and 2^8 * 128 keys is far inside fp16's range): rare after the first
-// tiles.
+// since the last time: rare after the first tiles.  A weight is then at most
+// 2^8 (fp16 holds up to 65504), and the sums of weights and products are fp32.
 //
 // Warps: 0-7 queries, softmax, results (a row belongs to two threads, 64 keys
 // of a tile each: warps q and q + 4), 8 TMA, 9 MMA.  Value rows past the
 // sequence's end (tokens of no or another sequence, which may hold anything)
 // are zeroed in shared memory by the softmax warps before the MMA reads them;
-// scores of such keys are masked.
+// scores of such keys are masked.  Keys that only later tokens of the sequence
+// see are multiplied by a weight of 0, so their values have to be finite.
 #include <string.h>
 
 #include "attn.h"
