@@ -494,8 +494,8 @@ typedef struct mla_attn_paged_args {
  * product with the latents.  Results do not depend on timing.
  * Two launches.  A block index outside [0, num_blocks) reads as a block of
  * zeros and is reported (MLA_ERR_BAD_SLOT); a length below 0 or past
- * table_stride * page_size and offsets outside [0, T] are clamped and
- * reported (MLA_ERR_BAD_LENGTH).  Errors: MLA_ERR_INVALID_ARG (also T %
+ * table_stride * page_size or 2^31 - 256, and offsets outside [0, T], are
+ * clamped and reported (MLA_ERR_BAD_LENGTH).  Errors: MLA_ERR_INVALID_ARG (also T %
  * num_seqs != 0 without cu_q), MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED,
  * MLA_ERR_CUDA. */
 mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cudaStream_t stream);

@@ -35,6 +35,8 @@ constexpr int kKeyTile = 64;
 // item's tiles).
 __host__ __device__ constexpr int plan_item_cost(int R) { return R == kPagedPairRows ? 10 : 1; }
 constexpr int kPlanThreadsMax = 512;
+// Longest sequence: a tile beyond its last one still has key numbers of 31 bits.
+constexpr int kMaxKeys = 0x7fffff00;
 
 struct PlanShared {
   int threads;
@@ -82,7 +84,7 @@ __host__ __device__ __forceinline__ Seq plan_seq(const PagedParams& p, int s, in
     q.begin = s * p.n_uniform;
     q.n = p.n_uniform;
   }
-  const long long cap = (long long)p.table_stride * p.page;
+  const long long width = (long long)p.table_stride * p.page, cap = width < kMaxKeys ? width : kMaxKeys;
   int L = p.kv_lens[s];
   if (L < 0) { bad = true; L = 0; }
   if (L > cap) { bad = true; L = (int)cap; }

@@ -1,5 +1,5 @@
-"""The attention's abort paths on the host (no GPU): compiles and runs the
-programs of tests/host that model them (see their headers)."""
+"""The attention's abort paths and limits on the host (no GPU): compiles and
+runs the programs of tests/host that model them (see their headers)."""
 import os
 import shutil
 import subprocess
@@ -9,7 +9,7 @@ import pytest
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
-@pytest.mark.parametrize("name", ["attn_joins", "attn_rings"])
+@pytest.mark.parametrize("name", ["attn_joins", "attn_rings", "attn_limits"])
 def test_host_model(name, tmp_path):
     nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(nvcc):
