@@ -26,8 +26,8 @@
 // an mbarrier takes a thread about 100 cycles even when the phase is complete,
 // so finer slots cost more than they hide.
 //
-// What bounds it (one prompt of 8192, 128 heads, causal, bf16: 1.91 to 1.93
-// ms, 1.43 PFLOP/s): 0.97 us per tile (about 1900 cycles), 1.8 us more per item
+// What bounds it (one prompt of 8192, 128 heads, causal, bf16: 1.91 to 1.95
+// ms, 1.42 PFLOP/s): 0.97 us per tile (about 1900 cycles), 1.8 us more per item
 // and 17 us per call (fitted to non-causal prompts of 512 to 4096 tokens), the tensor
 // pipe busy 60 % of the time.  A tile's way is scores, softmax, weights
 // announced, output, with two tiles in flight.  Measured and slower: pairs of

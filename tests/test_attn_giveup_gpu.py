@@ -112,3 +112,32 @@ def test_a_limit_of_milliseconds_is_not_run_out_by_ordinary_waits():
     c.run(a)
     assert a.status() == 0
     c.check()
+
+
+def test_appends_and_prompts_of_one_handle_overlap():
+    """They use only the status word of the workspace, so calls of one handle may run on several streams at once."""
+    g = gen(8)
+    bf = torch.bfloat16
+    a = B.MLAAttention(config(4, "bf16"), 900)
+    ins = [[rnd(g, 1, h, 900, d, dtype=bf) for h, d in ((4, 128), (4, 64), (4, 128), (1, 64), (4, 128))] for _ in range(3)]
+    outs = [torch.zeros_like(x[0]) for x in ins]
+    want = []
+    for x in ins:
+        o = torch.zeros_like(x[0])
+        a.run_prompt(*x, o)
+        want.append(o)
+    kv = rnd(g, 900, 576, dtype=bf)
+    slots = torch.randperm(912, generator=g, device="cuda")[:900].to(torch.int32)
+    caches = [a.alloc_latent_caches(57, 16) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x, o, c in zip(streams, ins, outs, caches):
+            a.run_prompt(*x, o, stream=s)
+            a.append_latent(kv[:, :512], kv[:, 512:], None, None, None, None, slots, **c, stream=s)
+    torch.cuda.synchronize()
+    assert a.status() == 0
+    for o, w, c in zip(outs, want, caches):
+        assert torch.equal(o, w)
+        assert torch.equal(c["latent_cache"].view(-1, 512)[slots.long()], kv[:, :512])
+        assert torch.equal(c["kpe_cache"].view(-1, 64)[slots.long()], kv[:, 512:])
