@@ -81,7 +81,8 @@ typedef enum mla_status {
   MLA_ERR_NO_MEMORY = 8,       /* workspace allocation failed in create                   */
   MLA_ERR_WRONG_MODE = 9,      /* run of one quant mode on a handle made for the other    */
   MLA_ERR_BAD_SLOT = 10,       /* a paged-cache slot past the cache was seen (row dropped)*/
-  MLA_ERR_BAD_LENGTH = 11      /* a sequence length or offset out of range was seen       */
+  MLA_ERR_BAD_LENGTH = 11,     /* a sequence length or offset out of range was seen       */
+  MLA_ERR_NO_PAGES = 12        /* a page plan had too few free pages for a sequence       */
 } mla_status;
 
 typedef enum mla_dtype { MLA_F16 = 0, MLA_BF16 = 1 } mla_dtype;
@@ -397,8 +398,8 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out);
 mla_status mla_attn_destroy(mla_attn* h);
 
 /* Synchronise `stream`, read and clear the handle's device status word:
- * MLA_OK, MLA_ERR_BAD_POSITION, MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_BAD_SLOT or
- * MLA_ERR_BAD_LENGTH (in that order of precedence). */
+ * MLA_OK, MLA_ERR_BAD_POSITION, MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_BAD_SLOT,
+ * MLA_ERR_BAD_LENGTH or MLA_ERR_NO_PAGES (in that order of precedence). */
 mla_status mla_attn_status(mla_attn* h, cudaStream_t stream);
 
 /* Number of kernels the last call on this handle enqueued (-1: null handle). */
@@ -537,6 +538,138 @@ typedef struct mla_attn_prompt_args {
  * are clamped and reported (MLA_ERR_BAD_LENGTH).  Errors as above; cu_seqlens
  * with b > 1 is MLA_ERR_INVALID_ARG. */
 mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cudaStream_t stream);
+
+typedef struct mla_attn_paged_kv_args {
+  const void* q_nope;          /* [T, H, 128]                  */
+  const void* q_pe;            /* [T, H, 64]                   */
+  const int32_t* cu_q;         /* [num_seqs + 1] or NULL       */
+  const int32_t* kv_lens;      /* [num_seqs]                   */
+  const int32_t* block_table;  /* [num_seqs, table_stride]     */
+  const void* k_cache;         /* [num_blocks, KH, page_size, 128] */
+  const void* v_cache;         /* [num_blocks, KH, page_size, 128] */
+  const void* kpe_cache;       /* [num_blocks, 1, page_size, 64]   */
+  const float* k_scale;        /* [KH * 128], or NULL          */
+  const float* v_scale;        /* [KH * 128], or NULL          */
+  const float* kpe_scale;      /* [64], or NULL                */
+  void* out;                   /* [T, H, 128], dense           */
+  float* lse;                  /* [T, H], dense, or NULL       */
+  long long k_block_stride, k_head_stride;
+  long long v_block_stride, v_head_stride;
+  long long kpe_block_stride;
+  int num_seqs, T;
+  int table_stride;
+  int page_size, num_blocks;
+  int k_row_stride, v_row_stride, kpe_row_stride;
+  int q_nope_token_stride, q_nope_head_stride;
+  int q_pe_token_stride, q_pe_head_stride;
+} mla_attn_paged_kv_args;
+
+/* Attention of the newest tokens of num_seqs sequences over the paged
+ * up-projected caches that mla_kv_prolog_run_paged writes, or over int8 codes
+ * as mla_kv_prolog_run_c8 makes them (its dense [b, H, s, 128] outputs are a
+ * cache of b blocks with pages of s rows):
+ *   q_nope [T, H, 128], q_pe [T, H, 64]  dtype (strided; q_pe rotated)
+ *   k_cache, v_cache  a block's rows per KV head, KH = num_kv_heads; query
+ *            head h reads KV head h / (H / KH).  dtype; with scales int8
+ *            codes that stand for code * scale of their channel
+ *   kpe_cache  the rotated key parts, which the heads share; alike
+ *   k_scale, v_scale, kpe_scale  all three (int8 caches), or none
+ *   cu_q, kv_lens, block_table as for mla_attn_paged_run
+ *   out      [T, H, 128] dtype, dense;  lse [T, H] f32, dense, or NULL
+ * Row i of n sees the cached tokens j <= L - n + i: out = sum_j p_j v_j with
+ * p = softmax(scale * (q_nope . k_j + q_pe . kpe_j)), lse = ln sum_j exp(...).
+ * Strides are in elements, multiples of 16 bytes; rows are contiguous, blocks,
+ * heads and rows may lie in any order.  What mla_attn_paged_run says of rows
+ * without keys, of rows of no sequence, of cache rows past L and of finite
+ * rows below it, and of precision holds here too (int8: the softmax weights
+ * are rounded to fp16, the scaled queries enter with 22 bits); results do not
+ * depend on timing.  A block index outside [0, num_blocks) reads as zeros
+ * and is reported (MLA_ERR_BAD_SLOT); lengths and offsets out of range are
+ * clamped and reported (MLA_ERR_BAD_LENGTH).  Two launches.  Made for few
+ * query rows per KV head (n * H / KH up to 16; more rows read the cache once
+ * for each 16 of them, 8 with int8).  Errors: MLA_ERR_INVALID_ARG (also T %
+ * num_seqs != 0 without cu_q, bad strides, some of the scales only),
+ * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args, cudaStream_t stream);
+
+typedef struct mla_page_plan_args {
+  const int32_t* new_lens;     /* [num_seqs]                   */
+  const int32_t* ended;        /* [num_seqs] or NULL           */
+  const int32_t* kv_lens;      /* [num_seqs]                   */
+  int32_t* block_table;        /* [num_seqs, table_stride]     */
+  int32_t* free_blocks;        /* [num_blocks]                 */
+  const int32_t* free_count;   /* [1]                          */
+  int32_t* kv_lens_out;        /* [num_seqs]                   */
+  int32_t* free_count_out;     /* [1]                          */
+  int32_t* cu_q;               /* [num_seqs + 1]               */
+  int32_t* slot_mapping;       /* [T]                          */
+  int32_t* positions;          /* [T]                          */
+  int num_seqs, T;
+  int table_stride;
+  int page_size, num_blocks;
+} mla_page_plan_args;
+
+/* Plan one step of a paged cache on the device: what mla_latent_append (or
+ * mla_kv_prolog_run_paged) and the paged attentions read, from the requests'
+ * lengths.  Sequence i has kv_lens[i] tokens in the cache and brings
+ * new_lens[i] >= 0 new ones (0: it idles); the token rows of a step are
+ * packed in sequence order.
+ *   free_blocks [num_blocks] int32: a stack, entries 0 .. free_count - 1 are
+ *            blocks that no sequence holds, the next one handed out last
+ *   ended    [num_seqs] int32: where not 0, the sequence's
+ *            ceil(kv_lens / page_size) pages go back to the stack first (in
+ *            sequence and page order) and its length becomes 0; with new
+ *            tokens, a new sequence begins in its place
+ *   block_table, free_blocks  updated in place; entries that a sequence does
+ *            not use keep what they hold
+ *   kv_lens_out  length after the step, new tokens included (may be kv_lens)
+ *   free_count_out  (may be free_count)
+ *   cu_q     sequence i owns token rows cu_q[i] .. cu_q[i + 1] - 1
+ *   slot_mapping, positions  of each row: block * page_size + offset, and the
+ *            row's position in its sequence; rows from cu_q[num_seqs] to T
+ *            are padding (slot -1, position 0), so a captured step can keep T
+ * New pages are taken from the top of the stack in sequence order.  A
+ * sequence whose pages are not all there gets none (nor do later ones that
+ * need any): its length stays, its rows have slot -1 and position 0, and
+ * MLA_ERR_NO_PAGES is reported by mla_attn_status.  The same holds, with
+ * MLA_ERR_BAD_LENGTH, for a sequence that would pass table_stride *
+ * page_size or 2^31 - 256 tokens, or row T.  Lengths and a count out of
+ * range are clamped, and pages past the stack's end dropped
+ * (MLA_ERR_BAD_LENGTH); a row whose block is not in [0, num_blocks) gets
+ * slot -1 (MLA_ERR_BAD_SLOT).  T may be smaller than max_tokens; of the
+ * handle only its status word is used.  One launch.  Other than as stated the arrays
+ * must not overlap.  Errors: MLA_ERR_INVALID_ARG (also num_blocks *
+ * page_size > INT_MAX, num_seqs > 2^30), MLA_ERR_TOO_MANY_TOKENS,
+ * MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point next to the int8 building blocks: rows and weights in
+ * e4m3 (4 exponent, 3 mantissa bits, largest value 448) with fp32 scales for
+ * blocks of 128, the form in which the DeepSeek-V3 / R1 checkpoints are
+ * published: a row has a scale for each 128 of its columns, a weight one for
+ * each block of 128 x 128. */
+typedef struct mla_fp8_quant_args {
+  const void* x;      /* [T, K] dtype                            */
+  const void* gamma;  /* [K] dtype, or NULL                      */
+  void* q;            /* [T, K] e4m3                             */
+  float* scale;       /* [ceil(K / 128), T], dense               */
+  int T, K;
+  int x_stride;       /* elements between rows, multiple of 8    */
+  int q_stride;       /* bytes between rows, multiple of 16      */
+  int dtype;          /* mla_dtype of x and gamma                */
+  float eps;          /* RMSNorm epsilon; used with gamma        */
+} mla_fp8_quant_args;
+
+/* Quantise rows to e4m3.  y = x, or with gamma y = x / sqrt(mean(x^2) + eps)
+ * * gamma (fp32).  Per row and block of 128 columns (the last one may be
+ * shorter): scale = max(max |y| / 448, 2^-126), q = e4m3(y * (1 / scale)) to
+ * nearest even, so y is about q * scale.  Rows have to be finite (a NaN gives
+ * a NaN code and does not enter its block's scale; an infinity makes the
+ * scale infinite).  Runs on the current device, one launch.  Errors:
+ * MLA_ERR_INVALID_ARG (also bad strides), MLA_ERR_UNSUPPORTED (K not a
+ * multiple of 16), MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+mla_status mla_fp8_quant_rows(const mla_fp8_quant_args* args, cudaStream_t stream);
 
 /* Text of a status code (static storage), the text of the last CUDA error
  * seen by this library on the calling thread, and the ABI version. */

@@ -19,7 +19,8 @@ MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
                 3: "MLA_ERR_TOO_MANY_TOKENS", 4: "MLA_ERR_MISALIGNED", 5: "MLA_ERR_CUDA",
                 6: "MLA_ERR_DEVICE_TIMEOUT", 7: "MLA_ERR_BAD_POSITION", 8: "MLA_ERR_NO_MEMORY",
-                9: "MLA_ERR_WRONG_MODE", 10: "MLA_ERR_BAD_SLOT", 11: "MLA_ERR_BAD_LENGTH"}
+                9: "MLA_ERR_WRONG_MODE", 10: "MLA_ERR_BAD_SLOT", 11: "MLA_ERR_BAD_LENGTH",
+                12: "MLA_ERR_NO_PAGES"}
 PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_DECODE_GRID = 0, 1, 2, 3
 MLA_F16, MLA_BF16 = 0, 1
 QUANT_NONE, QUANT_W8A8 = 0, 1
@@ -33,7 +34,8 @@ EXPORTED = ["mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
             "mla_kv_prolog_prepare_weights", "mla_kv_prolog_run_latent", "mla_kv_prolog_run_paged",
             "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold", "mla_prolog_w8a8_capture",
             "mla_kv_prolog_last_cluster_launches", "mla_attn_create", "mla_attn_destroy", "mla_attn_status",
-            "mla_attn_last_launches", "mla_latent_append", "mla_attn_paged_run", "mla_attn_prompt_run"]
+            "mla_attn_last_launches", "mla_latent_append", "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan",
+            "mla_fp8_quant_rows", "mla_attn_paged_kv_run"]
 
 
 class MLAError(RuntimeError):
@@ -100,7 +102,8 @@ def load(path: str | None = None):
     L.mla_attn_destroy.argtypes = [H]
     L.mla_attn_status.argtypes = [H, P]
     L.mla_attn_last_launches.argtypes = [H]
-    for fn in (L.mla_latent_append, L.mla_attn_paged_run, L.mla_attn_prompt_run):
+    L.mla_fp8_quant_rows.argtypes = [P, P]
+    for fn in (L.mla_latent_append, L.mla_attn_paged_run, L.mla_attn_prompt_run, L.mla_page_plan, L.mla_attn_paged_kv_run):
         fn.argtypes = [H, P, P]
     for fn in ("mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
                "mla_kv_prolog_status", "mla_kv_prolog_destroy", "mla_kv_prolog_set_path",
@@ -110,7 +113,8 @@ def load(path: str | None = None):
                "mla_kv_prolog_run_paged", "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold",
                "mla_prolog_w8a8_capture", "mla_kv_prolog_last_cluster_launches", "mla_attn_create",
                "mla_attn_destroy", "mla_attn_status", "mla_attn_last_launches", "mla_latent_append",
-               "mla_attn_paged_run", "mla_attn_prompt_run"):
+               "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan", "mla_fp8_quant_rows",
+               "mla_attn_paged_kv_run"):
         getattr(L, fn).restype = ctypes.c_int
     L.mla_status_string.argtypes = [ctypes.c_int]
     L.mla_status_string.restype = ctypes.c_char_p
@@ -426,14 +430,16 @@ def mla_attn_destroy(h):
 
 
 def mla_attn_status(h, stream=None) -> int:
-    """Raw status code (0 = ok, 6 = timeout, 7 = bad position, 10 = bad slot, 11 = bad length)."""
+    """Raw status code (0 = ok, 6 = timeout, 7 = bad position, 10 = bad slot, 11 = bad length, 12 = no pages)."""
     return load().mla_attn_status(h, _stream(stream))
 
 
-# mla_latent_append_args, mla_attn_paged_args, mla_attn_prompt_args: pointers, then ints
+# mla_latent_append_args, mla_attn_paged_args, mla_attn_prompt_args, mla_page_plan_args: pointers, then ints
 _APPEND_ARGS = struct.Struct("@11Q11i4x")
 _PAGED_ARGS = struct.Struct("@9Q11i4x")
 _PROMPT_ARGS = struct.Struct("@8Q21i4x")
+_PLAN_ARGS = struct.Struct("@11Q5i4x")
+_PAGED_KV_ARGS = struct.Struct("@13Q5q12i")  # mla_attn_paged_kv_args: pointers, 64-bit strides, ints
 
 
 class MLAAttention:
@@ -613,6 +619,138 @@ class MLAAttention:
         if code:
             _check(code, "mla_attn_prompt_run")
         return out
+
+
+    def _kv_cache(self, t, dtype, shape, name):
+        """Block, head and row stride of a cache [num_blocks, heads, page_size, width] whose rows are contiguous."""
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
+            self._on_device(t, dtype, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        bs, hs, rs, es = t.stride()
+        if es != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        if rs > _INT_MAX:
+            if shape[2] > 1:
+                raise ValueError(f"{name}: row strides must be below 2^31 elements")
+            rs = shape[3]  # (a single row has no stride of its own)
+        return bs, hs, rs
+
+    def run_paged_kv(self, q_nope, q_pe, kv_lens, block_table, k_cache, v_cache, kpe_cache, out, cu_q=None, lse=None,
+                     scales=None, stream=None):
+        """Attention of the newest tokens over the paged caches of the prolog's outputs: q_nope [T, H, 128], q_pe
+        [T, H, 64], k_cache and v_cache [blocks, KH, page, 128], kpe_cache [blocks, 1, page, 64] -> out [T, H, 128] and
+        lse [T, H] (float32, optional); kv_lens, block_table, cu_q as for run_paged.  scales: int8 caches with the
+        float32 scales scales["k"] [KH * 128], scales["v"] [KH * 128], scales["kpe"] [64] of run_c8."""
+        H, KH, nope, rope, vd, i32, f32 = self.heads, self.kv_heads, self.nope, self.rope, self.vdim, torch.int32, torch.float32
+        T, n = q_nope.shape[0], kv_lens.shape[0]
+        if block_table.dim() != 2 or k_cache.dim() != 4:
+            raise ValueError("block_table must have shape [num_seqs, blocks], k_cache [num_blocks, heads, page_size, 128]")
+        nb, _, page, _ = k_cache.shape
+        width = block_table.shape[1]
+        q0, q1, _ = self._rows(q_nope, (T, H, nope), "q_nope")
+        p0, p1, _ = self._rows(q_pe, (T, H, rope), "q_pe")
+        dt = self.dtype if scales is None else torch.int8
+        k0, k1, k2 = self._kv_cache(k_cache, dt, (nb, KH, page, nope), "k_cache")
+        v0, v1, v2 = self._kv_cache(v_cache, dt, (nb, KH, page, vd), "v_cache")
+        e0, _, e2 = self._kv_cache(kpe_cache, dt, (nb, 1, page, rope), "kpe_cache")
+        sk = sv = se = 0
+        if scales is not None:
+            sk = self._flat(scales["k"], f32, KH * nope, 'scales["k"]')
+            sv = self._flat(scales["v"], f32, KH * vd, 'scales["v"]')
+            se = self._flat(scales["kpe"], f32, rope, 'scales["kpe"]')
+        code = self._lib.mla_attn_paged_kv_run(self.h, _PAGED_KV_ARGS.pack(
+            q_nope.data_ptr(), q_pe.data_ptr(), 0 if cu_q is None else self._flat(cu_q, i32, n + 1, "cu_q"),
+            self._flat(kv_lens, i32, n, "kv_lens"), self._flat(block_table, i32, n * width, "block_table"),
+            k_cache.data_ptr(), v_cache.data_ptr(), kpe_cache.data_ptr(), sk, sv, se,
+            self._flat(out, self.dtype, T * H * vd, "out"), 0 if lse is None else self._flat(lse, f32, T * H, "lse"),
+            k0, k1, v0, v1, e0, n, T, width, page, nb, k2, v2, e2, q0, q1, p0, p1), self._stream(stream))
+        if code:
+            _check(code, "mla_attn_paged_kv_run")
+        return out
+
+    def plan_pages(self, new_lens, kv_lens, block_table, free_blocks, free_count, page_size, cu_q, slot_mapping, positions,
+                   kv_lens_out=None, free_count_out=None, ended=None, stream=None):
+        """One step's plan of a paged cache, all int32: new_lens and kv_lens [n], block_table [n, blocks] and the stack
+        free_blocks [num_blocks] (both updated), free_count [1], ended [n] or None -> cu_q [n + 1], slot_mapping [T],
+        positions [T], kv_lens_out [n] and free_count_out [1] (None: in place)."""
+        i32 = torch.int32
+        n, T, nb = new_lens.shape[0], slot_mapping.shape[0], free_blocks.shape[0]
+        if block_table.dim() != 2:
+            raise ValueError("block_table must have shape [num_seqs, blocks]")
+        width = block_table.shape[1]
+        lens, count = self._flat(kv_lens, i32, n, "kv_lens"), self._flat(free_count, i32, 1, "free_count")
+        code = self._lib.mla_page_plan(self.h, _PLAN_ARGS.pack(
+            self._flat(new_lens, i32, n, "new_lens"), 0 if ended is None else self._flat(ended, i32, n, "ended"), lens,
+            self._flat(block_table, i32, n * width, "block_table"), self._flat(free_blocks, i32, nb, "free_blocks"), count,
+            lens if kv_lens_out is None else self._flat(kv_lens_out, i32, n, "kv_lens_out"),
+            count if free_count_out is None else self._flat(free_count_out, i32, 1, "free_count_out"),
+            self._flat(cu_q, i32, n + 1, "cu_q"), self._flat(slot_mapping, i32, T, "slot_mapping"),
+            self._flat(positions, i32, T, "positions"), n, T, width, page_size, nb), self._stream(stream))
+        if code:
+            _check(code, "mla_page_plan")
+        return slot_mapping
+
+
+# ------------------------------------------------------------------ 8-bit floating point
+FP8_BLOCK = 128  # columns (and weight rows) that share a scale
+_FP8_ROWS_ARGS = struct.Struct("@4Q5if")
+_DTYPES = {torch.float16: MLA_F16, torch.bfloat16: MLA_BF16}
+
+
+def _fp8_rows(t, dtype, shape, name):
+    """Row stride of a [rows, cols] CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if shape[0] <= 1:
+        return shape[1]
+    if rows > _INT_MAX:
+        raise ValueError(f"{name}: strides must be below 2^31 elements")
+    return rows
+
+
+def mla_fp8_quant_rows(x, q, scale, gamma=None, eps=1e-6, stream=None):
+    """Rows x [T, K] (fp16 or bf16, RMSNorm with gamma [K] first unless None) to e4m3 codes q [T, K]
+    (torch.float8_e4m3fn) and scales [ceil(K / 128), T]: x ~ q * scale."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise TypeError("x must be an fp16 or bf16 tensor")
+    if x.dim() != 2:
+        raise ValueError("x must have shape [rows, columns]")
+    T, K = x.shape
+    xs = _fp8_rows(x, x.dtype, (T, K), "x")
+    qs = _fp8_rows(q, torch.float8_e4m3fn, (T, K), "q")
+    if scale.shape != (-(-K // FP8_BLOCK), T):
+        raise ValueError(f"scale must have shape {(-(-K // FP8_BLOCK), T)}, got {tuple(scale.shape)}")
+    sp = _dev(scale, torch.float32, "scale")
+    gp = 0
+    if gamma is not None:
+        if gamma.shape != (K,):
+            raise ValueError(f"gamma must have shape {(K,)}, got {tuple(gamma.shape)}")
+        gp = _dev(gamma, x.dtype, "gamma")
+    dev = x.get_device()
+    for t in (q, scale, gamma):
+        if t is not None and t.get_device() != dev:
+            raise TypeError(f"all tensors must be on CUDA device {dev}")
+    args = _FP8_ROWS_ARGS.pack(x.data_ptr(), gp, q.data_ptr(), sp, T, K, xs, qs, _DTYPES[x.dtype], eps)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        code = load().mla_fp8_quant_rows(args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = load().mla_fp8_quant_rows(args, stream)
+    if code:
+        _check(code, "mla_fp8_quant_rows")
+    return q
 
 
 def to_device(inp: dict, device="cuda") -> dict:

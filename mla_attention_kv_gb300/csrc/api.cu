@@ -133,6 +133,7 @@ const char* mla_status_string(mla_status s) {
     case MLA_ERR_WRONG_MODE: return "run does not match the handle's quant mode";
     case MLA_ERR_BAD_SLOT: return "a cache slot past num_blocks * page_size was seen (row dropped)";
     case MLA_ERR_BAD_LENGTH: return "a sequence length or offset out of range was seen (clamped)";
+    case MLA_ERR_NO_PAGES: return "too few free pages for a sequence (its rows have no slot)";
   }
   return "unknown status";
 }

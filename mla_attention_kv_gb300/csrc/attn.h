@@ -33,6 +33,26 @@ struct AppendParams {
 };
 cudaError_t append_launch(bool bf16, const AppendParams& p, cudaStream_t stream);
 
+// ---------------------------------------------------------------- page plan
+// Longest sequence of a plan: its page numbers times the page size stay below 2^31.
+constexpr int kMaxSeqTokens = 0x7fffff00;
+struct PagePlanParams {
+  const int32_t* new_lens;
+  const int32_t* ended;  // or null
+  const int32_t* kv_lens;
+  int32_t* table;
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* kv_lens_out;     // may be kv_lens
+  int32_t* free_count_out;  // may be free_count
+  int32_t* cu_q;
+  int32_t* slots;
+  int32_t* positions;
+  unsigned* status;
+  int nseq, T, table_stride, page, nblocks;
+};
+cudaError_t page_plan_launch(const PagePlanParams& p, cudaStream_t stream);
+
 // ---------------------------------------------------------------- paged attention
 // An item that worker i began and others went on with (rows = 0: none).
 struct PagedJoin {
@@ -81,6 +101,29 @@ cudaError_t paged_pair_prepare(bool bf16);
 cudaError_t paged_pair_launch(bool bf16, const PagedParams& p, PagedMaps* maps, cudaStream_t stream);
 // Joins the partial results of items split over workers.
 cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged K/V attention
+struct PagedKvParams {
+  PagedParams plan;  // sequences, lengths, table, workspace, out and lse; heads: query heads per KV head
+  const void* q_nope;
+  const void* q_pe;
+  const void* k;  // [block, KV head, row, 128] by strides (elements)
+  const void* v;
+  const void* kpe;  // [block, row, 64]
+  const float* k_scale;  // int8 caches: scale per channel [KV heads * 128], [KV heads * 128], [64]
+  const float* v_scale;
+  const float* kpe_scale;
+  long long k_bs, k_hs, v_bs, v_hs, kpe_bs;
+  int k_rs, v_rs, kpe_rs;
+  int qn_ts, qn_hs, qp_ts, qp_hs;
+  int kv_heads;
+};
+constexpr int kKvWarps = 8;  // workers per CTA
+constexpr int kKvRows = 16;  // query rows of an item
+constexpr int kKvRowsI8 = 8;
+inline int paged_kv_workers(int num_sms) { return num_sms * kKvWarps; }
+cudaError_t paged_kv_prepare(bool bf16);
+cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- prompt attention
 struct PromptTensor {

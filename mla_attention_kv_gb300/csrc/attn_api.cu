@@ -93,11 +93,15 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     delete h;
     return fail(e, "device query");
   }
-  // workspace: [status, 256 bytes] | a join record per worker | two partial results per worker
+  // workspace: [status, 256 bytes] | a join record per worker | two partial results per worker (512 columns wide for the
+  // latent cache, 128 for the K/V caches, whose workers are more)
   const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedPairRows;
-  const size_t rows = rows_mma > rows_tc ? rows_mma : rows_tc;
-  const size_t join_off = 256, ml_off = join_off + (((size_t)h->num_sms * 2 * sizeof(PagedJoin) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
-  e = cudaMalloc(&h->ws, o_off + rows * kRank * sizeof(float));
+  const size_t rows_lat = rows_mma > rows_tc ? rows_mma : rows_tc, rows_kv = (size_t)paged_kv_workers(h->num_sms) * 2 * kKvRows;
+  const size_t rows = rows_lat > rows_kv ? rows_lat : rows_kv;
+  const size_t values = rows_lat * kRank > rows_kv * kV ? rows_lat * kRank : rows_kv * kV;
+  const size_t workers = (size_t)(paged_kv_workers(h->num_sms) > h->num_sms * 2 ? paged_kv_workers(h->num_sms) : h->num_sms * 2);
+  const size_t join_off = 256, ml_off = join_off + ((workers * sizeof(PagedJoin) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+  e = cudaMalloc(&h->ws, o_off + values * sizeof(float));
   if (e != cudaSuccess) {
     delete h;
     fail(e, "cudaMalloc workspace");
@@ -120,6 +124,7 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   e = paged_mma_prepare(bf16);
   if (e == cudaSuccess) e = paged_pair_prepare(bf16);
   if (e == cudaSuccess) e = prompt_tc_prepare(bf16);
+  if (e == cudaSuccess) e = paged_kv_prepare(bf16);
   if (e != cudaSuccess) {
     cudaFree(h->ws);
     delete h;
@@ -152,6 +157,7 @@ mla_status mla_attn_status(mla_attn* h, cudaStream_t stream) {
   if (st & kStatusTimeout) return MLA_ERR_DEVICE_TIMEOUT;
   if (st & kStatusBadSlot) return MLA_ERR_BAD_SLOT;
   if (st & kStatusBadLength) return MLA_ERR_BAD_LENGTH;
+  if (st & kStatusNoPages) return MLA_ERR_NO_PAGES;
   return MLA_OK;
 }
 
@@ -244,6 +250,53 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
   return MLA_OK;
 }
 
+mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_attn_paged_kv_args& a = *args;
+  if (a.num_seqs < 0 || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
+      (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  if (a.num_seqs == 0 || a.T == 0) return MLA_OK;
+  if (!a.cu_q && a.T % a.num_seqs != 0) return MLA_ERR_INVALID_ARG;
+  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  const int H = h->cfg.num_heads, KH = h->cfg.num_kv_heads;
+  if (!a.q_nope || !a.q_pe || !a.kv_lens || !a.block_table || !a.k_cache || !a.v_cache || !a.kpe_cache || !a.out ||
+      !a.k_scale != !a.v_scale || !a.k_scale != !a.kpe_scale)
+    return MLA_ERR_INVALID_ARG;
+  const bool i8 = a.k_scale != nullptr;
+  const int unit = i8 ? 16 : 8;  // elements in 16 bytes of a cache
+  auto cache_ok = [&](long long stride, int width, bool used) { return !used || (stride >= width && stride % unit == 0); };
+  if (!stride_ok(a.q_nope_token_stride, kNope, a.T > 1) || !stride_ok(a.q_nope_head_stride, kNope, H > 1) ||
+      !stride_ok(a.q_pe_token_stride, kRope, a.T > 1) || !stride_ok(a.q_pe_head_stride, kRope, H > 1) ||
+      !cache_ok(a.k_block_stride, kNope, a.num_blocks > 1) || !cache_ok(a.k_head_stride, kNope, KH > 1) ||
+      !cache_ok(a.k_row_stride, kNope, a.page_size > 1) || !cache_ok(a.v_block_stride, kV, a.num_blocks > 1) ||
+      !cache_ok(a.v_head_stride, kV, KH > 1) || !cache_ok(a.v_row_stride, kV, a.page_size > 1) ||
+      !cache_ok(a.kpe_block_stride, kRope, a.num_blocks > 1) || !cache_ok(a.kpe_row_stride, kRope, a.page_size > 1))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.q_nope, a.q_pe, a.cu_q, a.kv_lens, a.block_table, a.k_cache, a.v_cache, a.kpe_cache,
+                        a.k_scale, a.v_scale, a.kpe_scale, a.out, a.lse};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  PagedKvParams p = {};
+  PagedParams& s = p.plan;
+  s.cu_q = a.cu_q; s.kv_lens = a.kv_lens; s.table = a.block_table; s.out = a.out; s.lse = a.lse; s.part_o = h->part_o;
+  s.part_ml = h->part_ml; s.joins = h->joins; s.status = h->status; s.table_stride = a.table_stride; s.page = a.page_size;
+  s.nblocks = a.num_blocks; s.nseq = a.num_seqs; s.T = a.T; s.heads = H / KH; s.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs;
+  s.workers = paged_kv_workers(h->num_sms); s.scale_log2 = h->scale_log2;
+  p.q_nope = a.q_nope; p.q_pe = a.q_pe; p.k = a.k_cache; p.v = a.v_cache; p.kpe = a.kpe_cache; p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale; p.kpe_scale = a.kpe_scale; p.k_bs = a.k_block_stride; p.k_hs = a.k_head_stride;
+  p.v_bs = a.v_block_stride; p.v_hs = a.v_head_stride; p.kpe_bs = a.kpe_block_stride; p.k_rs = a.k_row_stride;
+  p.v_rs = a.v_row_stride; p.kpe_rs = a.kpe_row_stride; p.qn_ts = a.q_nope_token_stride; p.qn_hs = a.q_nope_head_stride;
+  p.qp_ts = a.q_pe_token_stride; p.qp_hs = a.q_pe_head_stride; p.kv_heads = KH;
+  cudaError_t e = paged_kv_launch(h->cfg.dtype == MLA_BF16, i8, p, stream);
+  if (e != cudaSuccess) return fail(e, "paged K/V attention launch");
+  h->last_launches = 2;
+  return MLA_OK;
+}
+
 mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cudaStream_t stream) {
   if (!h || !args) return MLA_ERR_INVALID_ARG;
   const mla_attn_prompt_args& a = *args;
@@ -280,6 +333,34 @@ mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cu
   p.heads = H; p.kv_heads = KH; p.causal = a.causal; p.ctas = h->num_sms; p.scale_log2 = h->scale_log2; p.budget_ns = h->budget_ns;
   cudaError_t e = prompt_tc_launch(h->cfg.dtype == MLA_BF16, p, &h->prompt_maps, stream);
   if (e != cudaSuccess) return fail(e, "prompt attention launch");
+  h->last_launches = 1;
+  return MLA_OK;
+}
+
+mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_page_plan_args& a = *args;
+  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
+      (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  if (!a.free_blocks || !a.free_count || !a.free_count_out || !a.cu_q || (a.T > 0 && (!a.slot_mapping || !a.positions)) ||
+      (a.num_seqs > 0 && (!a.new_lens || !a.kv_lens || !a.kv_lens_out || (a.table_stride > 0 && !a.block_table))))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.new_lens, a.ended, a.kv_lens, a.block_table, a.free_blocks, a.free_count, a.kv_lens_out,
+                        a.free_count_out, a.cu_q, a.slot_mapping, a.positions};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  PagePlanParams p = {};
+  p.new_lens = a.new_lens; p.ended = a.ended; p.kv_lens = a.kv_lens; p.table = a.block_table; p.free_blocks = a.free_blocks;
+  p.free_count = a.free_count; p.kv_lens_out = a.kv_lens_out; p.free_count_out = a.free_count_out; p.cu_q = a.cu_q;
+  p.slots = a.slot_mapping; p.positions = a.positions; p.status = h->status; p.nseq = a.num_seqs; p.T = a.T;
+  p.table_stride = a.table_stride; p.page = a.page_size; p.nblocks = a.num_blocks;
+  cudaError_t e = page_plan_launch(p, stream);
+  if (e != cudaSuccess) return fail(e, "page plan launch");
   h->last_launches = 1;
   return MLA_OK;
 }

@@ -12,7 +12,7 @@ namespace mla {
 void set_error_text(const char* what);
 
 // Device status bits (kept in the handle's workspace).
-enum : unsigned { kStatusBadPosition = 1u, kStatusTimeout = 2u, kStatusBadSlot = 4u, kStatusBadLength = 8u };
+enum : unsigned { kStatusBadPosition = 1u, kStatusTimeout = 2u, kStatusBadSlot = 4u, kStatusBadLength = 8u, kStatusNoPages = 16u };
 
 // Output placement of token row t (shared by the decode and prefill
 // kernels): the dense layout [b, X, s, d] (outer = bi, inner = si, count =
