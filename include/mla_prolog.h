@@ -671,6 +671,60 @@ typedef struct mla_fp8_quant_args {
  * multiple of 16), MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_fp8_quant_rows(const mla_fp8_quant_args* args, cudaStream_t stream);
 
+typedef struct mla_fp8_linear_config {
+  int in_features;  /* K, multiple of 16                               */
+  int out_features; /* N, multiple of 8                                */
+  int dtype;        /* mla_dtype of x, gamma and out                   */
+  int max_tokens;   /* largest T of any run (sizes the workspace)      */
+  unsigned long long spin_budget_ns; /* device wait limit; 0 selects 1 s */
+} mla_fp8_linear_config;
+
+typedef struct mla_fp8_linear_s mla_fp8_linear;
+
+/* A linear layer with an e4m3 weight.
+ *   weight        [N, K] e4m3, dense ([out, in], as checkpoints store it)
+ *   weight_scale  [ceil(N / 128), ceil(K / 128)] f32, dense
+ * Both stay the caller's and are read by every run; the handle owns the
+ * workspace of quantised rows and a status word.  One handle serves one
+ * stream at a time, and one host thread (runs given codes use only its
+ * status word and may overlap on the device).  Errors:
+ * MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (K or N), MLA_ERR_MISALIGNED,
+ * MLA_ERR_NO_MEMORY, MLA_ERR_CUDA. */
+mla_status mla_fp8_linear_create(const mla_fp8_linear_config* cfg, const void* weight,
+                                 const float* weight_scale, mla_fp8_linear** out);
+mla_status mla_fp8_linear_destroy(mla_fp8_linear* h);
+
+/* Synchronise `stream`, read and clear the status word: MLA_OK or
+ * MLA_ERR_DEVICE_TIMEOUT. */
+mla_status mla_fp8_linear_status(mla_fp8_linear* h, cudaStream_t stream);
+
+/* Number of kernels the last run enqueued (-1: null handle). */
+int mla_fp8_linear_last_launches(mla_fp8_linear* h);
+
+typedef struct mla_fp8_linear_args {
+  const void* x;         /* [T, K] dtype, or NULL                   */
+  const void* gamma;     /* [K] dtype, or NULL; with x only         */
+  const void* x_q;       /* [T, K] e4m3, when x is NULL             */
+  const float* x_scale;  /* [ceil(K / 128), T], with x_q            */
+  void* out;             /* [T, N] dtype                            */
+  int T;
+  int x_stride;          /* elements, multiple of 8                 */
+  int x_q_stride;        /* bytes, multiple of 16                   */
+  int out_stride;        /* elements, multiple of 8                 */
+  float eps;             /* RMSNorm epsilon; used with gamma        */
+} mla_fp8_linear_args;
+
+/* out[t][n] = sum over blocks b of 128 columns: x_scale[b][t] *
+ * weight_scale[n / 128][b] * sum_{k in b} x_q[t][k] weight[n][k], for rows
+ * that mla_fp8_quant_rows has made (x_q, x_scale), or for rows x that the
+ * call quantises itself first, after an RMSNorm with gamma or as they are
+ * (two launches).  A block's sum is the tensor core's fp32 sum of exact
+ * products; the blocks are scaled and added in fp32 and rounded once.
+ * Results do not depend on timing.  Errors: MLA_ERR_INVALID_ARG (also both or
+ * neither of x and x_q, bad strides), MLA_ERR_TOO_MANY_TOKENS,
+ * MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+mla_status mla_fp8_linear_run(mla_fp8_linear* h, const mla_fp8_linear_args* args, cudaStream_t stream);
+
 /* Text of a status code (static storage), the text of the last CUDA error
  * seen by this library on the calling thread, and the ABI version. */
 const char* mla_status_string(mla_status s);

@@ -35,7 +35,9 @@ EXPORTED = ["mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
             "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold", "mla_prolog_w8a8_capture",
             "mla_kv_prolog_last_cluster_launches", "mla_attn_create", "mla_attn_destroy", "mla_attn_status",
             "mla_attn_last_launches", "mla_latent_append", "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan",
-            "mla_fp8_quant_rows", "mla_attn_paged_kv_run"]
+            "mla_fp8_quant_rows", "mla_attn_paged_kv_run",
+            "mla_fp8_linear_create", "mla_fp8_linear_destroy", "mla_fp8_linear_status", "mla_fp8_linear_last_launches",
+            "mla_fp8_linear_run"]
 
 
 class MLAError(RuntimeError):
@@ -59,6 +61,11 @@ class AttnConfig(ctypes.Structure):
                 ("nope_dim", ctypes.c_int), ("v_dim", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("max_tokens", ctypes.c_int),
                 ("max_pos", ctypes.c_int), ("spin_budget_ns", ctypes.c_ulonglong)]
+
+
+class Fp8LinearConfig(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int), ("out_features", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("spin_budget_ns", ctypes.c_ulonglong)]
 
 
 _lib = None
@@ -103,6 +110,11 @@ def load(path: str | None = None):
     L.mla_attn_status.argtypes = [H, P]
     L.mla_attn_last_launches.argtypes = [H]
     L.mla_fp8_quant_rows.argtypes = [P, P]
+    L.mla_fp8_linear_create.argtypes = [ctypes.POINTER(Fp8LinearConfig), P, P, ctypes.POINTER(ctypes.c_void_p)]
+    L.mla_fp8_linear_destroy.argtypes = [H]
+    L.mla_fp8_linear_status.argtypes = [H, P]
+    L.mla_fp8_linear_last_launches.argtypes = [H]
+    L.mla_fp8_linear_run.argtypes = [H, P, P]
     for fn in (L.mla_latent_append, L.mla_attn_paged_run, L.mla_attn_prompt_run, L.mla_page_plan, L.mla_attn_paged_kv_run):
         fn.argtypes = [H, P, P]
     for fn in ("mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
@@ -114,7 +126,8 @@ def load(path: str | None = None):
                "mla_prolog_w8a8_capture", "mla_kv_prolog_last_cluster_launches", "mla_attn_create",
                "mla_attn_destroy", "mla_attn_status", "mla_attn_last_launches", "mla_latent_append",
                "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan", "mla_fp8_quant_rows",
-               "mla_attn_paged_kv_run"):
+               "mla_attn_paged_kv_run", "mla_fp8_linear_create", "mla_fp8_linear_destroy", "mla_fp8_linear_status",
+               "mla_fp8_linear_last_launches", "mla_fp8_linear_run"):
         getattr(L, fn).restype = ctypes.c_int
     L.mla_status_string.argtypes = [ctypes.c_int]
     L.mla_status_string.restype = ctypes.c_char_p
@@ -751,6 +764,95 @@ def mla_fp8_quant_rows(x, q, scale, gamma=None, eps=1e-6, stream=None):
     if code:
         _check(code, "mla_fp8_quant_rows")
     return q
+
+
+_FP8_LINEAR_ARGS = struct.Struct("@5Q4if4x")
+
+
+class MLAFp8Linear:
+    """Linear layer with an e4m3 weight [N, K] (torch.float8_e4m3fn) and a scale for each 128 x 128 block of it,
+    [ceil(N / 128), ceil(K / 128)] float32 (one library handle).  dtype: "fp16" or "bf16" of rows and results."""
+
+    def __init__(self, weight, weight_scale, dtype: str, max_tokens: int, spin_budget_ns: int = 0):
+        self.h = None
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+            raise TypeError("weight must be a tensor of shape [out_features, in_features]")
+        self.N, self.K = weight.shape
+        wp, sp = _dev(weight, torch.float8_e4m3fn, "weight"), _dev(weight_scale, torch.float32, "weight_scale")
+        self.blocks = -(-self.K // FP8_BLOCK)
+        if weight_scale.shape != (-(-self.N // FP8_BLOCK), self.blocks):
+            raise ValueError(f"weight_scale must have shape {(-(-self.N // FP8_BLOCK), self.blocks)}, got {tuple(weight_scale.shape)}")
+        if weight_scale.get_device() != weight.get_device():
+            raise TypeError("weight and weight_scale must be on one device")
+        self.weight, self.weight_scale = weight, weight_scale  # (read by every run)
+        self.device = weight.get_device()
+        self.dtype = _tdt(dict(dtype=dtype))
+        self.max_tokens = max_tokens
+        self._lib = load()
+        c = Fp8LinearConfig(self.K, self.N, _DTYPES[self.dtype], max_tokens, spin_budget_ns)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(self._lib.mla_fp8_linear_create(ctypes.byref(c), wp, sp, ctypes.byref(h)), "mla_fp8_linear_create")
+        self.h = h
+
+    def close(self):
+        if self.h is not None:
+            _check(load().mla_fp8_linear_destroy(self.h), "mla_fp8_linear_destroy")
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def last_launches(self) -> int:
+        return load().mla_fp8_linear_last_launches(self.h)
+
+    def status(self, stream=None) -> int:
+        """Raw status code (0 = ok, 6 = timeout)."""
+        return load().mla_fp8_linear_status(self.h, self._stream(stream))
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _rows(self, t, dtype, shape, name):
+        st = _fp8_rows(t, dtype, shape, name)
+        if t.get_device() != self.device:
+            raise TypeError(f"{name} must be on CUDA device {self.device}")
+        return st
+
+    def _dense(self, t, dtype, shape, name):
+        p = _dev(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != self.device:
+            raise TypeError(f"{name} must be on CUDA device {self.device}")
+        return p
+
+    def run(self, out, x=None, x_q=None, x_scale=None, gamma=None, eps=1e-6, stream=None):
+        """out [T, N] of rows x [T, K] (quantised by the call, after an RMSNorm with gamma [K] unless None), or of the
+        codes x_q [T, K] and scales x_scale [ceil(K / 128), T] of mla_fp8_quant_rows."""
+        if (x is None) == (x_q is None) or (x_q is None) != (x_scale is None) or (x is None and gamma is not None):
+            raise ValueError("give x (and gamma), or x_q and x_scale")
+        T = (x_q if x is None else x).shape[0]
+        os_ = self._rows(out, self.dtype, (T, self.N), "out")
+        xp = gp = qp = sp = xs = qs = 0
+        if x is not None:
+            xs, xp = self._rows(x, self.dtype, (T, self.K), "x"), x.data_ptr()
+            if gamma is not None:
+                gp = self._dense(gamma, self.dtype, (self.K,), "gamma")
+        else:
+            qs, qp = self._rows(x_q, torch.float8_e4m3fn, (T, self.K), "x_q"), x_q.data_ptr()
+            sp = self._dense(x_scale, torch.float32, (self.blocks, T), "x_scale")
+        code = self._lib.mla_fp8_linear_run(self.h, _FP8_LINEAR_ARGS.pack(
+            xp, gp, qp, sp, out.data_ptr(), T, xs, qs, os_, eps), self._stream(stream))
+        if code:
+            _check(code, "mla_fp8_linear_run")
+        return out
 
 
 def to_device(inp: dict, device="cuda") -> dict:

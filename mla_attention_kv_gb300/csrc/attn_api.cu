@@ -4,12 +4,12 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <new>
 
 #include "../../include/mla_prolog.h"
+#include "api_util.cuh"
 #include "attn.h"
 
 using namespace mla;
@@ -32,38 +32,9 @@ struct mla_attn_s {
 
 namespace {
 
-mla_status fail(cudaError_t e, const char* what) {
-  char text[256];
-  snprintf(text, sizeof(text), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
-  set_error_text(text);
-  return MLA_ERR_CUDA;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // A stride between rows of `width` elements: whole 16-byte units, rows not
 // overlapping (the stride of a dimension of size 1 is not read).
 bool stride_ok(int stride, int width, bool used) { return !used || (stride >= width && stride % 8 == 0); }
-
-// Reads and clears the status word in one step (the second word keeps what was
-// read): calls that overlap on another stream may set bits meanwhile.
-__global__ void take_status_kernel(unsigned* status) { status[1] = atomicExch(status, 0u); }
-
-// Makes the handle's device current for the length of a call.
-struct DeviceGuard {
-  int before = -1;
-  cudaError_t err;
-  explicit DeviceGuard(int device) {
-    err = cudaGetDevice(&before);
-    if (err == cudaSuccess && before != device)
-      err = cudaSetDevice(device);
-    else
-      before = -1;
-  }
-  ~DeviceGuard() {
-    if (before >= 0) cudaSetDevice(before);
-  }
-};
 
 }  // namespace
 
@@ -145,13 +116,8 @@ mla_status mla_attn_status(mla_attn* h, cudaStream_t stream) {
   if (!h) return MLA_ERR_INVALID_ARG;
   DeviceGuard g(h->device);
   if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return fail(e, "cudaStreamSynchronize");
   unsigned st = 0;
-  take_status_kernel<<<1, 1, 0, stream>>>(h->status);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, h->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  const cudaError_t e = take_status(h->status, &st, stream);
   if (e != cudaSuccess) return fail(e, "read status");
   if (st & kStatusBadPosition) return MLA_ERR_BAD_POSITION;
   if (st & kStatusTimeout) return MLA_ERR_DEVICE_TIMEOUT;

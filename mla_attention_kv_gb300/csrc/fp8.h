@@ -23,4 +23,36 @@ struct Fp8RowsParams {
 };
 cudaError_t fp8_rows_launch(bool bf16, const Fp8RowsParams& p, cudaStream_t stream);
 
+// ---------------------------------------------------------------- linear layer
+struct Fp8LinearParams {
+  const float* x_scale;  // [blocks of K, T]
+  const float* w_scale;  // [blocks of N, blocks of K]
+  void* out;             // [T, N], row stride out_stride (elements)
+  unsigned* status;
+  int T, K, N, out_stride;
+  int dependent;  // launched while the kernel that makes the rows runs
+  unsigned long long budget_ns;
+};
+// Tensor maps of the weight (boxes of 128 rows) and of the last call's rows.
+struct Fp8Maps {
+  CUtensorMap w;
+  struct Key {
+    const void* x;
+    int T, stride, box;
+  } key;
+  bool valid;
+  CUtensorMap x;
+};
+// Few rows: weights as the 128-row operand, the K blocks split over a cluster.
+constexpr int kFp8NarrowMax = 128;  // token rows of a tile
+cudaError_t fp8_narrow_prepare();
+cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+                              cudaStream_t stream);
+// Many rows: 256 x 256 tiles on the 2-SM MMA.
+cudaError_t fp8_pair_prepare();
+cudaError_t fp8_pair_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+                            cudaStream_t stream);
+// The map of rows xq [T, K] with boxes of `box` rows, made anew if it is another than the last one.
+bool fp8_row_map(Fp8Maps* maps, const void* xq, int T, int K, int stride, int box);
+
 }  // namespace mla

@@ -1,5 +1,5 @@
 """Refusals of the serving-step operators on the host (no GPU): page plan,
-paged K/V attention, e4m3 rows.  Every bad argument is answered before
+paged K/V attention, e4m3 rows and linear layer.  Every bad argument is answered before
 any CUDA call.  Fake addresses: nothing is dereferenced."""
 import ctypes
 import os
@@ -40,8 +40,9 @@ KV = dict(qn=fake(), qp=fake(), cu=0, lens=fake(), table=fake(), k=fake(), v=fak
           k_bs=16 * 16 * 128, k_hs=16 * 128, v_bs=16 * 16 * 128, v_hs=16 * 128, e_bs=16 * 64, n=2, T=2, ts=4, page=16, nb=8, k_rs=128,
           v_rs=128, e_rs=64, qn_t=16 * 128, qn_h=128, qp_t=16 * 64, qp_h=64)
 ROWS = dict(x=fake(), gamma=0, q=fake(), scale=fake(), T=4, K=256, xs=256, qs=256, dtype=0, eps=1e-6)
-STRUCTS = dict(mla_page_plan_args=B._PLAN_ARGS, mla_attn_paged_kv_args=B._PAGED_KV_ARGS, mla_fp8_quant_args=B._FP8_ROWS_ARGS)
-BASES = dict(mla_page_plan_args=PLAN, mla_attn_paged_kv_args=KV, mla_fp8_quant_args=ROWS)
+LINEAR = dict(x=fake(), gamma=0, xq=0, xsc=0, out=fake(), T=4, xs=256, qs=0, os=264, eps=1e-6)
+STRUCTS = dict(mla_fp8_linear_args=B._FP8_LINEAR_ARGS, mla_page_plan_args=B._PLAN_ARGS, mla_attn_paged_kv_args=B._PAGED_KV_ARGS, mla_fp8_quant_args=B._FP8_ROWS_ARGS)
+BASES = dict(mla_fp8_linear_args=LINEAR, mla_page_plan_args=PLAN, mla_attn_paged_kv_args=KV, mla_fp8_quant_args=ROWS)
 
 
 def packed(struct, base, **over):
@@ -84,11 +85,57 @@ def test_fp8_rows_refusals(L, over, code):
     assert L.mla_fp8_quant_rows(packed(B._FP8_ROWS_ARGS, ROWS, **over), None) == code, over
 
 
+def linear_cfg(**over):
+    c = dict(in_features=256, out_features=264, dtype=B.MLA_F16, max_tokens=16, spin_budget_ns=0)
+    c.update(over)
+    return B.Fp8LinearConfig(**c)
+
+
+@pytest.mark.parametrize("over,w,s,code", [
+    (dict(in_features=0), 16, 16, 1), (dict(out_features=-8), 16, 16, 1), (dict(max_tokens=0), 16, 16, 1), (dict(dtype=2), 16, 16, 1),
+    (dict(), 0, 16, 1), (dict(), 16, 0, 1), (dict(in_features=264), 16, 16, 2), (dict(out_features=260), 16, 16, 2),
+    (dict(), 24, 16, 4), (dict(), 16, 20, 4),
+])
+def test_linear_create_refusals(L, over, w, s, code):
+    h = P()
+    assert L.mla_fp8_linear_create(ctypes.byref(linear_cfg(**over)), w or None, s or None, ctypes.byref(h)) == code
+    assert not h.value
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(T=-1), 1), (dict(T=17), 3), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(out=0), 1), (dict(os=256), 1), (dict(os=268), 1),
+    (dict(x=0), 1), (dict(xq=fake()), 1), (dict(xsc=fake()), 1), (dict(xs=248), 1), (dict(xs=260), 1),
+    (dict(x=0, xq=fake(), qs=256), 1), (dict(x=0, xsc=fake(), qs=256), 1), (dict(x=0, xq=fake(), xsc=fake(), qs=264), 1),
+    (dict(x=0, xq=fake(), xsc=fake(), qs=240), 1), (dict(x=0, xq=fake(), xsc=fake(), qs=256, gamma=fake()), 1),
+    (dict(x=0x5000008), 4), (dict(gamma=0x5000008), 4), (dict(out=0x5000004), 4), (dict(x=0, xq=0x5000008, xsc=fake(), qs=256), 4),
+    (dict(x=0, xq=fake(), xsc=0x5000004, qs=256), 4), (dict(T=0, x=0, out=0), 0),
+])
+def test_linear_refusals(L, over, code):
+    mem = (ctypes.c_char * 1024)()  # a handle struct built on the host: the checks read its configuration only
+    c = linear_cfg()
+    ctypes.memmove(mem, ctypes.byref(c), ctypes.sizeof(c))
+    assert L.mla_fp8_linear_run(ctypes.cast(mem, P), packed(B._FP8_LINEAR_ARGS, LINEAR, **over), None) == code, over
+
+
+def test_linear_config_layout_matches_the_header(tmp_path):
+    src = open(os.path.join(ROOT, "include", "mla_prolog.h")).read()
+    body = re.search(r"typedef struct mla_fp8_linear_config \{(.*?)\} mla_fp8_linear_config;", src, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    fields = [re.match(r"\s*(.*?)\s+(\w+)$", f.strip()).groups() for f in body.split(";") if f.strip()]
+    of = {"int": ctypes.c_int, "unsigned long long": ctypes.c_ulonglong}
+    assert [(n, of[t]) for t, n in fields] == list(B.Fp8LinearConfig._fields_)
+
+
 def test_null_arguments(L):
     h = FakeHandle().ptr
     assert L.mla_page_plan(None, packed(B._PLAN_ARGS, PLAN), None) == 1 and L.mla_page_plan(h, None, None) == 1
     assert L.mla_attn_paged_kv_run(None, packed(B._PAGED_KV_ARGS, KV), None) == 1 and L.mla_attn_paged_kv_run(h, None, None) == 1
     assert L.mla_fp8_quant_rows(None, None) == 1
+    out = P()
+    assert L.mla_fp8_linear_create(None, 16, 16, ctypes.byref(out)) == 1
+    assert L.mla_fp8_linear_create(ctypes.byref(linear_cfg()), 16, 16, None) == 1
+    assert L.mla_fp8_linear_destroy(None) == 1 and L.mla_fp8_linear_status(None, None) == 1
+    assert L.mla_fp8_linear_last_launches(None) == -1 and L.mla_fp8_linear_run(None, packed(B._FP8_LINEAR_ARGS, LINEAR), None) == 1
     assert b"page" in L.mla_status_string(12)
 
 
@@ -132,5 +179,7 @@ def test_binding_rejects_host_tensors():
     x = torch.zeros(2, 256, dtype=torch.float16)
     with pytest.raises(TypeError):
         B.mla_fp8_quant_rows(x, x.to(torch.float8_e4m3fn), torch.zeros(2, 2))
+    with pytest.raises(TypeError):
+        B.MLAFp8Linear(x.to(torch.float8_e4m3fn), torch.zeros(1, 2), "fp16", 4)
     with pytest.raises(TypeError):
         B.mla_fp8_quant_rows(x.float(), x.to(torch.float8_e4m3fn), torch.zeros(2, 2))
