@@ -33,7 +33,7 @@ struct Fp8LinearParams {
   int dependent;  // launched while the kernel that makes the rows runs
   unsigned long long budget_ns;
 };
-// Tensor maps of the weight (boxes of 128 rows) and of the last call's rows.
+// Tensor maps of the weight (boxes of 128 rows), and of the last call's rows and results.
 struct Fp8Maps {
   CUtensorMap w;
   struct Key {
@@ -42,15 +42,21 @@ struct Fp8Maps {
   } key;
   bool valid;
   CUtensorMap x;
+  struct OutKey {
+    const void* out;
+    int T, stride;
+  } out_key;
+  bool out_valid;
+  CUtensorMap out;
 };
 // Few rows: weights as the 128-row operand, the K blocks split over a cluster.
 constexpr int kFp8NarrowMax = 128;  // token rows of a tile
 cudaError_t fp8_narrow_prepare();
 cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
                               cudaStream_t stream);
-// Many rows: 256 x 256 tiles on the 2-SM MMA.
-cudaError_t fp8_pair_prepare();
-cudaError_t fp8_pair_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+// Many rows: persistent CTAs on tiles of 128 rows x 256 weight rows.
+cudaError_t fp8_wide_prepare();
+cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
                             cudaStream_t stream);
 // The map of rows xq [T, K] with boxes of `box` rows, made anew if it is another than the last one.
 bool fp8_row_map(Fp8Maps* maps, const void* xq, int T, int K, int stride, int box);

@@ -93,7 +93,7 @@ mla_status mla_fp8_linear_create(const mla_fp8_linear_config* cfg, const void* w
   e = cudaMemset(h->ws, 0, 256);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // a first call may come on a stream that does not wait for this one
   if (e == cudaSuccess) e = fp8_narrow_prepare();
-  if (e == cudaSuccess) e = fp8_pair_prepare();
+  if (e == cudaSuccess) e = fp8_wide_prepare();
   if (e != cudaSuccess) {
     cudaFree(h->ws);
     delete h;
@@ -165,7 +165,7 @@ mla_status mla_fp8_linear_run(mla_fp8_linear* h, const mla_fp8_linear_args* args
   p.w_scale = h->w_scale; p.out = a.out; p.status = h->status; p.T = a.T; p.K = K; p.N = N;
   p.out_stride = a.T > 1 ? a.out_stride : N; p.budget_ns = h->budget_ns;
   e = a.T <= kFp8NarrowMax ? fp8_narrow_launch(bf16, p, xq, xq_stride, &h->maps, h->num_sms, stream)
-                           : fp8_pair_launch(bf16, p, xq, xq_stride, &h->maps, h->num_sms, stream);
+                           : fp8_wide_launch(bf16, p, xq, xq_stride, &h->maps, h->num_sms, stream);
   if (e != cudaSuccess) return fail(e, "fp8 linear launch");
   ++h->last_launches;
   return MLA_OK;
