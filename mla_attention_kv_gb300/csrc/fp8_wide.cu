@@ -49,7 +49,7 @@ static_assert(sizeof(WdShared) <= 512, "barrier block");
 struct WdArgs {
   CUtensorMap w, x, out;
   Fp8LinearParams p;
-  int nm, nn, m_fast;
+  int nm, nn, group;
 };
 
 template <typename T>
@@ -64,9 +64,12 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
   volatile int* abort = &sh->abort;
   auto bar = [](uint64_t* b) { return smem_u32(b); };
   const int blocks = (p.K + kFp8Block - 1) / kFp8Block, tiles = a.nm * a.nn;
-  // tile u: token tiles or weight tiles fastest
-  auto tile_m = [&](int u) { return a.m_fast ? u % a.nm : u / a.nn; };
-  auto tile_n = [&](int u) { return a.m_fast ? u / a.nm : u % a.nn; };
+  // tile u: groups of token tiles in turn; within a group, its token tiles fastest
+  auto tile_at = [&](int u, int& m, int& n) {
+    const int per = a.group * a.nn, g = u / per, r = u - g * per, w = min(a.group, a.nm - g * a.group);
+    n = r / w;
+    m = g * a.group + r - n * w;
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWdStages; ++i) {
@@ -95,7 +98,10 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
       uint32_t s = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
-        const int m0 = tile_m(u) * 128, n0 = tile_n(u) * 256;
+        int m0, n0;
+        tile_at(u, m0, n0);
+        m0 *= 128;
+        n0 *= 256;
         for (int b = 0; b < blocks; ++b, ++s) {
           const uint32_t st = s % kWdStages;
           ok = at_wait(bar(&sh->empty[st]), ((s / kWdStages) & 1) ^ 1, abort, p.budget_ns, p.status);
@@ -158,7 +164,9 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
     bool ok = true;
     grid_dep_wait();
     for (int u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
-      const int row0 = tile_m(u) * 128 + q * 32, t = row0 + lane, nblk = tile_n(u) * 2 + h;
+      int tm, tn;
+      tile_at(u, tm, tn);
+      const int row0 = tm * 128 + q * 32, t = row0 + lane, nblk = tn * 2 + h;
       const float* xs = p.x_scale + (t < p.T ? t : 0);
       const float* ws = p.w_scale + (nblk * 128 < p.N ? (size_t)nblk * blocks : 0);
       uint64_t acc[32];
@@ -234,8 +242,11 @@ cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, c
   a.w = maps.w; a.x = maps.x; a.out = maps.out; a.p = p;
   a.nm = (p.T + 127) / 128;
   a.nn = (p.N + 255) / 256;
-  // the operand that is smaller stays in L2 while the other streams past it
-  a.m_fast = (long long)p.T < (long long)p.N;
+  // A group's rows (16 MB at most) stay in L2 while the weights stream past them; more than 64 tiles leave too few weight
+  // tiles at work at a time.  8192 x 1536 -> 24576: 241 us in one group of 64, 254 in groups of 24; 16384 x 7168 -> 2112:
+  // 211 in groups of 24, 261 in one of 128; 16384 x 512 -> 32768: 281 in groups of 64, 323 in one of 128.
+  const long long fit = (1ll << 24) / (128ll * p.K);
+  a.group = fit < 8 ? 8 : fit > 64 ? 64 : (int)fit;
   const long long tiles = (long long)a.nm * a.nn;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(tiles < num_sms ? (int)tiles : num_sms);
