@@ -4,15 +4,15 @@
 //
 // with blocks of 128 along K.  The weights are read once and used by few
 // rows: bound by their bytes (by latency for one row).  So the weights are
-// the MMA's 128-row operand and the tokens its columns (16 to 128): a tile is
+// the MMA's 128-row operand and the tokens its columns (16 to 64): a tile is
 // 128 weight rows, which share one weight scale per block, and its K blocks
 // are split over the CTAs of a cluster, whose parts are summed through
 // distributed shared memory in a fixed order (no workspace, no second
 // launch).  The tensor core's sum of a block stays in tensor memory until the
-// epilogue scales it and adds it to fp32 registers: one weight row and all
-// tokens of the tile per thread.
+// epilogue scales it and adds it to fp32 registers: one weight row and up to
+// 32 tokens per thread.
 //
-// Warps: 0 TMA, 1 tensor memory and MMA, 2-5 epilogue.  Behind the row
+// Warps: 0 TMA, 1 tensor memory and MMA, 2-5 (or 2-9) epilogue.  Behind the row
 // quantisation the kernel is launched early: its first weight tiles are under
 // way while that one still runs.
 #include <string.h>
@@ -24,15 +24,17 @@
 namespace mla {
 namespace {
 
-constexpr int kNwThreads = 192;
 constexpr uint32_t kWTile = 128 * 128;
 
 template <int TN>
 struct NwCfg {
+  static constexpr int kCols = TN < 32 ? TN : 32;      // token columns of an epilogue warp
+  static constexpr int kEpi = 4 * TN / kCols;          // epilogue warps
+  static constexpr int kThreads = 64 + kEpi * 32;
   static constexpr uint32_t kStage = kWTile + TN * 128;
-  static constexpr int kStages = TN == 128 ? 3 : TN == 64 ? 4 : 5;  // two CTAs per SM
-  static constexpr uint32_t kScale = kStages * kStage;             // [4 warps][2][TN] fp32
-  static constexpr uint32_t kBar = kScale + 4 * 2 * TN * 4;
+  static constexpr int kStages = TN == 64 ? 4 : 5;     // two CTAs per SM
+  static constexpr uint32_t kScale = kStages * kStage;  // [warp][2][kCols] fp32
+  static constexpr uint32_t kBar = kScale + kEpi * 2 * kCols * 4;
   static constexpr uint32_t kSmem = kBar + 256 + 1024;  // + alignment slack
   static constexpr uint32_t kTmem = 2 * TN < 32 ? 32 : 2 * TN;
   static_assert(TN * 128 * 4 <= kStages * kStage, "the sums take the stages' place");
@@ -51,8 +53,14 @@ struct NwArgs {
   Fp8LinearParams p;
 };
 
+__device__ __forceinline__ float ld_scale(const float* p) {  // (volatile: requested where it stands)
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 template <typename T, int TN>
-__global__ void __launch_bounds__(kNwThreads, 2) fp8_narrow_kernel(const __grid_constant__ NwArgs a) {
+__global__ void __launch_bounds__(NwCfg<TN>::kThreads, 2) fp8_narrow_kernel(const __grid_constant__ NwArgs a) {
   using E = Elem<T>;
   using S = NwCfg<TN>;
   const Fp8LinearParams& p = a.p;
@@ -77,7 +85,7 @@ __global__ void __launch_bounds__(kNwThreads, 2) fp8_narrow_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&sh->tfull[i]), 1);
-      mbar_init(bar(&sh->tempty[i]), 4);
+      mbar_init(bar(&sh->tempty[i]), S::kEpi);
     }
     mbar_init(bar(&sh->done), 1);
     sh->abort = 0;
@@ -89,7 +97,8 @@ __global__ void __launch_bounds__(kNwThreads, 2) fp8_narrow_kernel(const __grid_
   tc::fence_after_sync();
   const uint32_t tmem = uniform(sh->tmem);
 
-  float2 acc[TN / 2];  // (epilogue warps)
+  constexpr int kCols = S::kCols;
+  uint64_t acc[kCols / 2];  // (epilogue warps)
   if (warp == 0) {
     // ============================================================ TMA
     if (lane == 0) {
@@ -140,56 +149,51 @@ __global__ void __launch_bounds__(kNwThreads, 2) fp8_narrow_kernel(const __grid_
     __syncwarp();
   } else {
     // ============================================================ epilogue: scaled sums
-    const int e = warp - 2;
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    float* sc = reinterpret_cast<float*>(smem + S::kScale) + e * 2 * TN;
-    constexpr int kMine = (TN + 31) / 32;
+    const int e = warp - 2, c0 = (e >> 2) * kCols;  // this warp's token columns
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+    float* sc = reinterpret_cast<float*>(smem + S::kScale) + e * 2 * kCols;
 #pragma unroll
-    for (int j = 0; j < TN / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
     grid_dep_wait();
-    auto scales = [&](int i, float* s) {  // of K block b0 + i: this lane's tokens
-      const float w = i < nb ? __ldg(p.w_scale + (size_t)nt * blocks + b0 + i) : 0.f;
-#pragma unroll
-      for (int u = 0; u < kMine; ++u) {
-        const int t = t0 + u * 32 + lane;
-        s[u] = i < nb && (TN >= 32 || lane < TN) && t < p.T ? w * __ldg(p.x_scale + (size_t)(b0 + i) * p.T + t) : 0.f;
-      }
-    };
-    float next[kMine];
-    scales(0, next);
+    // the scales of K block b0 + i for this lane's token, requested two blocks ahead and multiplied when they are used
+    const int t = t0 + c0 + lane;
+    const bool mine = lane < kCols && t < p.T;
+    const float* xs = p.x_scale + (size_t)b0 * p.T + (mine ? t : 0);
+    const float* ws = p.w_scale + (size_t)nt * blocks + b0;
+    float x1 = mine ? ld_scale(xs) : 0.f, w1 = ld_scale(ws), x2 = 0.f, w2 = 0.f;
+    if (nb > 1) {
+      x2 = mine ? ld_scale(xs + p.T) : 0.f;
+      w2 = ld_scale(ws + 1);
+    }
     for (int i = 0; i < nb; ++i) {
       const int buf = i & 1;
-      float* s = sc + buf * TN;
-#pragma unroll
-      for (int u = 0; u < kMine; ++u)
-        if (TN >= 32 || lane < TN) s[u * 32 + lane] = next[u];
-      scales(i + 1, next);
+      float* s = sc + buf * kCols;
+      if (lane < kCols) s[lane] = x1 * w1;
+      x1 = x2;
+      w1 = w2;
+      if (i + 2 < nb) {
+        x2 = mine ? ld_scale(xs + (size_t)(i + 2) * p.T) : 0.f;
+        w2 = ld_scale(ws + i + 2);
+      }
       __syncwarp();
-      if (!at_wait_warp(bar(&sh->tfull[buf]), (i >> 1) & 1, abort, p.budget_ns, p.status)) break;
+      if (!__all_sync(~0u, mbar_try_wait(bar(&sh->tfull[buf]), (i >> 1) & 1)) &&
+          !at_wait_warp(bar(&sh->tfull[buf]), (i >> 1) & 1, abort, p.budget_ns, p.status))
+        break;
       tc::fence_after_sync();
-      constexpr int kCols = TN < 32 ? 16 : 32;
+      uint32_t v[kCols];
+      if constexpr (kCols == 16)
+        tc::ld16(tl + buf * TN, v);
+      else
+        tc::ld32(tl + buf * TN, v);
+      tc::wait_ld();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh->tempty[buf]));
 #pragma unroll
-      for (int c = 0; c < TN; c += kCols) {
-        uint32_t v[kCols];
-        if constexpr (kCols == 16)
-          tc::ld16(tl + buf * TN + c, v);
-        else
-          tc::ld32(tl + buf * TN + c, v);
-        tc::wait_ld();
-        if (c + kCols == TN) {  // the last columns are in registers
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(&sh->tempty[buf]));
-        }
-#pragma unroll
-        for (int k = 0; k < kCols; k += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(s + c + k);
-          float2* d = acc + (c + k) / 2;
-          d[0].x = fmaf(__uint_as_float(v[k]), f.x, d[0].x);
-          d[0].y = fmaf(__uint_as_float(v[k + 1]), f.y, d[0].y);
-          d[1].x = fmaf(__uint_as_float(v[k + 2]), f.z, d[1].x);
-          d[1].y = fmaf(__uint_as_float(v[k + 3]), f.w, d[1].y);
-        }
+      for (int k = 0; k < kCols; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(s + k);
+        acc[k / 2] = f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2_pack(f.x, f.y), acc[k / 2]);
+        acc[k / 2 + 1] = f2_fma(f2_pack(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), f2_pack(f.z, f.w), acc[k / 2 + 1]);
       }
     }
   }
@@ -197,18 +201,20 @@ __global__ void __launch_bounds__(kNwThreads, 2) fp8_narrow_kernel(const __grid_
   // ---- sums over the cluster: [token][weight row] in the stages' place
   __syncthreads();  // (all MMAs and copies are through)
   if (warp >= 2) {
-    float* red = reinterpret_cast<float*>(smem) + (warp & 3) * 32 + lane;
+    float* red = reinterpret_cast<float*>(smem) + (warp - 2) / 4 * kCols * 128 + (warp & 3) * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < TN / 2; ++j) {
-      red[(2 * j) * 128] = acc[j].x;
-      red[(2 * j + 1) * 128] = acc[j].y;
+    for (int j = 0; j < kCols / 2; ++j) {
+      float y0, y1;
+      f2_unpack(acc[j], y0, y1);
+      red[(2 * j) * 128] = y0;
+      red[(2 * j + 1) * 128] = y1;
     }
   }
   if (split > 1) tc::cluster_sync(); else __syncthreads();
   if (warp >= 2) {
     const int live = min(TN, p.T - t0);
     const int n = nt * 128 + lane * 4;
-    for (int j = live * rank / split + warp - 2; j < live * (rank + 1) / split; j += 4) {
+    for (int j = live * rank / split + warp - 2; j < live * (rank + 1) / split; j += S::kEpi) {
       const uint32_t at = sbase + (j * 128 + lane * 4) * 4;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int r = 0; r < split; ++r) {
@@ -238,12 +244,10 @@ template <typename T, int TN>
 cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, cudaStream_t stream) {
   NwArgs a;
   a.w = maps.w; a.x = maps.x; a.p = p;
-  const int blocks = (p.K + kFp8Block - 1) / kFp8Block, nt = (p.N + 127) / 128, tt = (p.T + TN - 1) / TN;
-  int split = 1;
-  while (split < 8 && 2 * split <= blocks && (long long)nt * tt * split * 2 <= 2 * num_sms) split *= 2;
+  const int nt = (p.N + 127) / 128, tt = (p.T + TN - 1) / TN, split = fp8_narrow_split(p, num_sms, nullptr);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(split, nt, tt);
-  c.blockDim = dim3(kNwThreads);
+  c.blockDim = dim3(NwCfg<TN>::kThreads);
   c.dynamicSmemBytes = NwCfg<TN>::kSmem;
   c.stream = stream;
   cudaLaunchAttribute at[2] = {};
@@ -257,15 +261,16 @@ cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, c
   return cudaLaunchKernelEx(&c, fp8_narrow_kernel<T, TN>, a);
 }
 
+int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
 template <typename T>
 cudaError_t launch_tn(const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms, cudaStream_t stream) {
-  const int tn = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
+  const int tn = tile_tokens(p.T);
   if (!fp8_row_map(maps, xq, p.T, p.K, xq_stride, tn)) return cudaErrorInvalidValue;
   switch (tn) {
     case 16: return launch<T, 16>(p, *maps, num_sms, stream);
     case 32: return launch<T, 32>(p, *maps, num_sms, stream);
-    case 64: return launch<T, 64>(p, *maps, num_sms, stream);
-    default: return launch<T, 128>(p, *maps, num_sms, stream);
+    default: return launch<T, 64>(p, *maps, num_sms, stream);
   }
 }
 
@@ -278,11 +283,30 @@ cudaError_t prepare() {
   cudaError_t e = prepare_one<T, 16>();
   if (e == cudaSuccess) e = prepare_one<T, 32>();
   if (e == cudaSuccess) e = prepare_one<T, 64>();
-  if (e == cudaSuccess) e = prepare_one<T, 128>();
   return e;
 }
 
 }  // namespace
+
+// CTAs of a cluster that share a tile's K blocks: as many as leave two blocks
+// each and two CTAs per SM in all, up to 8, or 4 for tiles of 64 tokens, whose
+// sums are larger (64 x 7168 -> 2112: 10.0 us on 4, 11.3 on 8; one row 8.2 on 4,
+// 7.4 on 8).  Cost: the blocks that an SM takes in turn, in units of about 0.15
+// us: one for a block of up to 32 tokens, two for 64, three for a block of the
+// other kernel's tile (1 x 1536 -> 24576: 9.5 us here, 12.6 there, cost 24, 36).  256 x 7168 -> 2112: 14.2 us here, 29.4 there (cost 56, 168);
+// 128 x 1536 -> 24576: 19.6 and 12.4 (72, 36); 256 x 16384 -> 7168: 72 and 63
+// (512, 384); 512 x 2048 -> 576: 7.8 and 10.1 (16, 48).
+int fp8_narrow_split(const Fp8LinearParams& p, int num_sms, int* cost) {
+  const int tn = tile_tokens(p.T), most = tn == 64 ? 4 : 8;
+  const long long blocks = (p.K + kFp8Block - 1) / kFp8Block, tiles = (long long)((p.N + 127) / 128) * ((p.T + tn - 1) / tn);
+  int split = 1;
+  while (split < most && 2 * split <= blocks && tiles * split * 2 <= 2 * num_sms) split *= 2;
+  if (cost) {
+    const long long c = (tiles * split + num_sms - 1) / num_sms * ((blocks + split - 1) / split) * (tn == 64 ? 2 : 1);
+    *cost = c < 0x7fffffff ? (int)c : 0x7fffffff;
+  }
+  return split;
+}
 
 bool fp8_row_map(Fp8Maps* maps, const void* xq, int T, int K, int stride, int box) {
   Fp8Maps::Key key;

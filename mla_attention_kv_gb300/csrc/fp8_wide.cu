@@ -15,8 +15,8 @@
 // the 2-SM MMA, which would halve the weight traffic but sends commits and
 // releases across the pair, about 1000 cycles each way.
 //
-// Warps: 0 TMA, 1 tensor memory and MMA, 4-11 epilogue (2 and 3 only give
-// their registers).
+// Warps: 0 TMA, 1 tensor memory, 1 and 2 MMA, 4-19 epilogue (3 only gives its
+// registers).
 #include <string.h>
 
 #include "attn_tc.cuh"
@@ -40,7 +40,7 @@ constexpr int kWdBufs = 4;  // of 128 tensor memory columns
 constexpr int kWdRoleRegs = 32, kWdEpiRegs = 112;
 
 struct WdShared {
-  uint64_t full[kWdStages], empty[kWdStages], tfull[kWdBufs], tempty[kWdBufs], done;
+  uint64_t full[kWdStages], empty[kWdStages], tfull[kWdBufs], tempty[kWdBufs], done[2];
   uint32_t tmem;
   int abort;
 };
@@ -74,13 +74,13 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWdStages; ++i) {
       mbar_init(bar(&sh->full[i]), 1);
-      mbar_init(bar(&sh->empty[i]), 1);
+      mbar_init(bar(&sh->empty[i]), 2);  // both MMA warps
     }
     for (int i = 0; i < kWdBufs; ++i) {
       mbar_init(bar(&sh->tfull[i]), 1);
       mbar_init(bar(&sh->tempty[i]), kWdEpi / 2);
     }
-    mbar_init(bar(&sh->done), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(&sh->done[i]), 1);
     sh->abort = 0;
     fence_mbar_init();
   }
@@ -119,37 +119,33 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ============================================================ MMA
+  } else if (warp < 3) {
+    // ============================================================ MMA: a warp for each weight block of the tile
     if (tc::elect_one()) {
+      const int h = warp - 1;
       constexpr uint32_t idesc = tc::idesc_e4m3(128, 128);
-      const uint64_t dx = tc::sdesc_sw128(sbase, 16, 1024), dw = tc::sdesc_sw128(sbase + 16384, 16, 1024);
+      const uint64_t dx = tc::sdesc_sw128(sbase, 16, 1024), dw = tc::sdesc_sw128(sbase + 16384 + h * 16384, 16, 1024);
       uint32_t s = 0, st = 0, par = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
 #pragma unroll 1
         for (int b = 0; b < blocks; ++b, ++s) {
-          ok = s == 0 ? at_wait_poll(bar(&sh->full[st]), 0, abort, p.budget_ns, p.status)
-                      : at_wait(bar(&sh->full[st]), par, abort, p.budget_ns, p.status);
+          const uint32_t buf = (s & 1) * 2 + h;
+          ok = (s == 0 ? at_wait_poll(bar(&sh->full[st]), 0, abort, p.budget_ns, p.status)
+                       : at_wait(bar(&sh->full[st]), par, abort, p.budget_ns, p.status)) &&
+               at_wait(bar(&sh->tempty[buf]), ((s >> 1) & 1) ^ 1, abort, p.budget_ns, p.status);
           if (!ok) break;
+          tc::fence_after_sync();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t buf = (s & 1) * 2 + h;
-            ok = ok && at_wait(bar(&sh->tempty[buf]), ((s >> 1) & 1) ^ 1, abort, p.budget_ns, p.status);
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_f8(tmem + buf * 128, dx + st * (kWdStage >> 4) + 2 * k, dw + st * (kWdStage >> 4) + h * 1024 + 2 * k, idesc, k > 0);
-            tc::commit(bar(&sh->tfull[buf]));
-          }
-          if (!ok) break;
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f8(tmem + buf * 128, dx + st * (kWdStage >> 4) + 2 * k, dw + st * (kWdStage >> 4) + 2 * k, idesc, k > 0);
+          tc::commit(bar(&sh->tfull[buf]));
           tc::commit(bar(&sh->empty[st]));
           if (++st == kWdStages) st = 0, par ^= 1;
         }
       }
-      tc::commit(bar(&sh->done));
-      mbar_wait_bounded(bar(&sh->done), 0, drain_budget(p.budget_ns));  // every MMA issued has completed
+      tc::commit(bar(&sh->done[h]));
+      mbar_wait_bounded(bar(&sh->done[h]), 0, drain_budget(p.budget_ns));  // every MMA issued has completed
     }
     __syncwarp();
   } else if (warp >= 4) {
