@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t kv_half2(uint32_t biased, uint32_t selector)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <typename T, bool kI8>
+// kWhole: pages are multiples of a stage, so that a stage lies in one page.
+template <typename T, bool kI8, bool kWhole>
 __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_constant__ PagedKvParams p) {
   using E = Elem<T>;
   using S = KvCfg<kI8>;
@@ -103,40 +104,83 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
     const bool whole = c.lo >= x0 && c.hi <= x1;
     if (lane == 0 && c.hi >= x1) kv_post_join(p, c, R, w, x0, x1, total, W);
 
-    // ---- stages: lane r looks up row r's page, two stages ahead of its use
+    // ---- stages.  A place is looked up two stages ahead of its use.
     struct Place { int blk, off; };
-    auto place_of = [&](int t) {
-      const int k = t * S::Keys + lane;
-      if (t >= t1 || lane >= S::Keys || k >= keys) return Place{0, -1};
-      const int pg = (int)((unsigned)k / (unsigned)p.plan.page);
-      return Place{p.plan.table[(size_t)c.s * p.plan.table_stride + pg], k - pg * p.plan.page};
-    };
-    auto load = [&](int t, Place pl) {
+    const unsigned char* kb = static_cast<const unsigned char*>(p.k) + c.head * p.k_hs * S::E;
+    const unsigned char* vb = static_cast<const unsigned char*>(p.v) + c.head * p.v_hs * S::E;
+    const unsigned char* pb = static_cast<const unsigned char*>(p.kpe);
+    const int32_t* table = p.plan.table + (size_t)c.s * p.plan.table_stride;
+    auto bad_block = [&](Place& pl) {
       if (pl.off >= 0 && (pl.blk < 0 || pl.blk >= p.plan.nblocks)) {
         atomicOr(p.plan.status, kStatusBadSlot);
         pl.off = -1;
       }
-      const uint32_t st = ring + (t % kStages) * kStageBytes;
-      const unsigned char* kb = static_cast<const unsigned char*>(p.k) + c.head * p.k_hs * S::E;
-      const unsigned char* vb = static_cast<const unsigned char*>(p.v) + c.head * p.v_hs * S::E;
-      constexpr int kRowsAt = 32 / S::CK;
-#pragma unroll
-      for (int i = 0; i < S::Keys / kRowsAt; ++i) {
-        const int r = i * kRowsAt + lane / S::CK, ch = lane % S::CK;
-        const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
-        const bool ok = off >= 0;
-        const long long kx = ok ? blk * p.k_bs + (long long)off * p.k_rs : 0, vx = ok ? blk * p.v_bs + (long long)off * p.v_rs : 0;
-        cp_async16(st + kv_at<S::CK>(r, ch), kb + kx * S::E + ch * 16, ok ? 16 : 0);
-        cp_async16(st + kVOff + kv_at<S::CK>(r, ch), vb + vx * S::E + ch * 16, ok ? 16 : 0);
+    };
+    constexpr int kRowsAt = 32 / S::CK, kPeRowsAt = 32 / S::CP;
+    // (kWhole) the next stage to look up: its page and its first row there
+    int npg = 0, noff = 0;
+    if (kWhole) {
+      npg = (int)((unsigned)(t0 * S::Keys) / (unsigned)p.plan.page);
+      noff = t0 * S::Keys - npg * p.plan.page;
+    }
+    auto place_of = [&](int t) {
+      if constexpr (kWhole) {  // all lanes alike
+        const Place pl = t < t1 ? Place{table[npg], noff} : Place{0, -1};
+        noff += S::Keys;
+        if (noff == p.plan.page) noff = 0, ++npg;
+        return pl;
+      } else {  // lane r looks up row r
+        const int k = t * S::Keys + lane;
+        if (t >= t1 || lane >= S::Keys || k >= keys) return Place{0, -1};
+        const int pg = (int)((unsigned)k / (unsigned)p.plan.page);
+        return Place{table[pg], k - pg * p.plan.page};
       }
-      constexpr int kPeRowsAt = 32 / S::CP;
+    };
+    auto load = [&](int t, Place pl) {
+      bad_block(pl);
+      const uint32_t st = ring + (t % kStages) * kStageBytes;
+      if constexpr (kWhole) {
+        const int rows = pl.off < 0 ? 0 : keys - t * S::Keys;  // of the stage, that there are
+        const long long blk = pl.off < 0 ? 0 : pl.blk, off = pl.off < 0 ? 0 : pl.off;
+        const int r0 = lane / S::CK, e0 = lane / S::CP;
+        const unsigned char* ks = kb + (blk * p.k_bs + (off + r0) * p.k_rs) * S::E + lane % S::CK * 16;
+        const unsigned char* vs = vb + (blk * p.v_bs + (off + r0) * p.v_rs) * S::E + lane % S::CK * 16;
+        const unsigned char* ps = pb + (blk * p.kpe_bs + (off + e0) * p.kpe_rs) * S::E + lane % S::CP * 16;
+        const long long kstep = (long long)kRowsAt * p.k_rs * S::E, vstep = (long long)kRowsAt * p.v_rs * S::E,
+                        pstep = (long long)kPeRowsAt * p.kpe_rs * S::E;
 #pragma unroll
-      for (int i = 0; i < S::Keys / kPeRowsAt; ++i) {
-        const int r = i * kPeRowsAt + lane / S::CP, ch = lane % S::CP;
-        const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
-        const bool ok = off >= 0;
-        const long long x = ok ? blk * p.kpe_bs + (long long)off * p.kpe_rs : 0;
-        cp_async16(st + kPeOff + kv_at<S::CP>(r, ch), static_cast<const unsigned char*>(p.kpe) + x * S::E + ch * 16, ok ? 16 : 0);
+        for (int i = 0; i < S::Keys / kRowsAt; ++i) {
+          const int r = i * kRowsAt + r0, n = r < rows ? 16 : 0;
+          const uint32_t d = st + kv_at<S::CK>(r, lane % S::CK);
+          cp_async16(d, ks, n);
+          cp_async16(d + kVOff, vs, n);
+          ks += kstep;
+          vs += vstep;
+        }
+#pragma unroll
+        for (int i = 0; i < S::Keys / kPeRowsAt; ++i) {
+          const int r = i * kPeRowsAt + e0;
+          cp_async16(st + kPeOff + kv_at<S::CP>(r, lane % S::CP), ps, r < rows ? 16 : 0);
+          ps += pstep;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::Keys / kRowsAt; ++i) {
+          const int r = i * kRowsAt + lane / S::CK, ch = lane % S::CK;
+          const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
+          const bool ok = off >= 0;
+          const long long kx = ok ? blk * p.k_bs + (long long)off * p.k_rs : 0, vx = ok ? blk * p.v_bs + (long long)off * p.v_rs : 0;
+          cp_async16(st + kv_at<S::CK>(r, ch), kb + kx * S::E + ch * 16, ok ? 16 : 0);
+          cp_async16(st + kVOff + kv_at<S::CK>(r, ch), vb + vx * S::E + ch * 16, ok ? 16 : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < S::Keys / kPeRowsAt; ++i) {
+          const int r = i * kPeRowsAt + lane / S::CP, ch = lane % S::CP;
+          const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
+          const bool ok = off >= 0;
+          const long long x = ok ? blk * p.kpe_bs + (long long)off * p.kpe_rs : 0;
+          cp_async16(st + kPeOff + kv_at<S::CP>(r, ch), pb + x * S::E + ch * 16, ok ? 16 : 0);
+        }
       }
     };
     {
@@ -461,7 +505,11 @@ __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constan
 
 template <typename T, bool kI8>
 cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
-  paged_kv_kernel<T, kI8><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
+  const bool whole = p.plan.page % KvCfg<kI8>::Keys == 0;
+  if (whole)
+    paged_kv_kernel<T, kI8, true><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
+  else
+    paged_kv_kernel<T, kI8, false><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr int R = KvCfg<kI8>::R;
@@ -482,9 +530,13 @@ cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(paged_kv_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_kv_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+  const void* k[4] = {(const void*)paged_kv_kernel<T, false, false>, (const void*)paged_kv_kernel<T, false, true>,
+                      (const void*)paged_kv_kernel<T, true, false>, (const void*)paged_kv_kernel<T, true, true>};
+  for (const void* f : k) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
