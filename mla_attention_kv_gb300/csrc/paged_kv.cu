@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t kv_half2(uint32_t biased, uint32_t selector)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// kWhole: pages are multiples of a stage, so that a stage lies in one page.
+// kWhole: pages are multiples of 16 rows, so that each 16 rows of a stage lie
+// in one page.
 template <typename T, bool kI8, bool kWhole>
 __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_constant__ PagedKvParams p) {
   using E = Elem<T>;
@@ -105,69 +106,82 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
     if (lane == 0 && c.hi >= x1) kv_post_join(p, c, R, w, x0, x1, total, W);
 
     // ---- stages.  A place is looked up two stages ahead of its use.
-    struct Place { int blk, off; };
+    constexpr int kParts = kWhole ? S::Keys / 16 : 1;  // of a stage that lie in one page each
+    struct Place { int blk[kParts], off[kParts]; };
     const unsigned char* kb = static_cast<const unsigned char*>(p.k) + c.head * p.k_hs * S::E;
     const unsigned char* vb = static_cast<const unsigned char*>(p.v) + c.head * p.v_hs * S::E;
     const unsigned char* pb = static_cast<const unsigned char*>(p.kpe);
     const int32_t* table = p.plan.table + (size_t)c.s * p.plan.table_stride;
-    auto bad_block = [&](Place& pl) {
-      if (pl.off >= 0 && (pl.blk < 0 || pl.blk >= p.plan.nblocks)) {
-        atomicOr(p.plan.status, kStatusBadSlot);
-        pl.off = -1;
-      }
+    auto check = [&](Place& pl) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        if (pl.off[i] >= 0 && (pl.blk[i] < 0 || pl.blk[i] >= p.plan.nblocks)) {
+          atomicOr(p.plan.status, kStatusBadSlot);
+          pl.off[i] = -1;
+        }
     };
     constexpr int kRowsAt = 32 / S::CK, kPeRowsAt = 32 / S::CP;
-    // (kWhole) the next stage to look up: its page and its first row there
+    // (kWhole) the next 16 rows to look up: their page and the first row there
     int npg = 0, noff = 0;
     if (kWhole) {
       npg = (int)((unsigned)(t0 * S::Keys) / (unsigned)p.plan.page);
       noff = t0 * S::Keys - npg * p.plan.page;
     }
     auto place_of = [&](int t) {
+      Place pl;
       if constexpr (kWhole) {  // all lanes alike
-        const Place pl = t < t1 ? Place{table[npg], noff} : Place{0, -1};
-        noff += S::Keys;
-        if (noff == p.plan.page) noff = 0, ++npg;
-        return pl;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const bool ok = t < t1 && t * S::Keys + 16 * i < keys;
+          pl.blk[i] = ok ? table[npg] : 0;
+          pl.off[i] = ok ? noff : -1;
+          noff += 16;
+          if (noff == p.plan.page) noff = 0, ++npg;
+        }
       } else {  // lane r looks up row r
         const int k = t * S::Keys + lane;
-        if (t >= t1 || lane >= S::Keys || k >= keys) return Place{0, -1};
-        const int pg = (int)((unsigned)k / (unsigned)p.plan.page);
-        return Place{table[pg], k - pg * p.plan.page};
+        const bool ok = t < t1 && lane < S::Keys && k < keys;
+        const int pg = ok ? (int)((unsigned)k / (unsigned)p.plan.page) : 0;
+        pl.blk[0] = ok ? table[pg] : 0;
+        pl.off[0] = ok ? k - pg * p.plan.page : -1;
       }
+      return pl;
     };
     auto load = [&](int t, Place pl) {
-      bad_block(pl);
+      check(pl);
       const uint32_t st = ring + (t % kStages) * kStageBytes;
       if constexpr (kWhole) {
-        const int rows = pl.off < 0 ? 0 : keys - t * S::Keys;  // of the stage, that there are
-        const long long blk = pl.off < 0 ? 0 : pl.blk, off = pl.off < 0 ? 0 : pl.off;
         const int r0 = lane / S::CK, e0 = lane / S::CP;
-        const unsigned char* ks = kb + (blk * p.k_bs + (off + r0) * p.k_rs) * S::E + lane % S::CK * 16;
-        const unsigned char* vs = vb + (blk * p.v_bs + (off + r0) * p.v_rs) * S::E + lane % S::CK * 16;
-        const unsigned char* ps = pb + (blk * p.kpe_bs + (off + e0) * p.kpe_rs) * S::E + lane % S::CP * 16;
         const long long kstep = (long long)kRowsAt * p.k_rs * S::E, vstep = (long long)kRowsAt * p.v_rs * S::E,
                         pstep = (long long)kPeRowsAt * p.kpe_rs * S::E;
 #pragma unroll
-        for (int i = 0; i < S::Keys / kRowsAt; ++i) {
-          const int r = i * kRowsAt + r0, n = r < rows ? 16 : 0;
-          const uint32_t d = st + kv_at<S::CK>(r, lane % S::CK);
-          cp_async16(d, ks, n);
-          cp_async16(d + kVOff, vs, n);
-          ks += kstep;
-          vs += vstep;
-        }
+        for (int h = 0; h < kParts; ++h) {
+          const int rows = pl.off[h] < 0 ? 0 : keys - t * S::Keys - 16 * h;  // that there are
+          const long long blk = pl.off[h] < 0 ? 0 : pl.blk[h], off = pl.off[h] < 0 ? 0 : pl.off[h];
+          const unsigned char* ks = kb + (blk * p.k_bs + (off + r0) * p.k_rs) * S::E + lane % S::CK * 16;
+          const unsigned char* vs = vb + (blk * p.v_bs + (off + r0) * p.v_rs) * S::E + lane % S::CK * 16;
+          const unsigned char* ps = pb + (blk * p.kpe_bs + (off + e0) * p.kpe_rs) * S::E + lane % S::CP * 16;
 #pragma unroll
-        for (int i = 0; i < S::Keys / kPeRowsAt; ++i) {
-          const int r = i * kPeRowsAt + e0;
-          cp_async16(st + kPeOff + kv_at<S::CP>(r, lane % S::CP), ps, r < rows ? 16 : 0);
-          ps += pstep;
+          for (int i = 0; i < 16 / kRowsAt; ++i) {
+            const int r = i * kRowsAt + r0, n = r < rows ? 16 : 0;
+            const uint32_t d = st + kv_at<S::CK>(16 * h + r, lane % S::CK);
+            cp_async16(d, ks, n);
+            cp_async16(d + kVOff, vs, n);
+            ks += kstep;
+            vs += vstep;
+          }
+#pragma unroll
+          for (int i = 0; i < 16 / kPeRowsAt; ++i) {
+            const int r = i * kPeRowsAt + e0;
+            cp_async16(st + kPeOff + kv_at<S::CP>(16 * h + r, lane % S::CP), ps, r < rows ? 16 : 0);
+            ps += pstep;
+          }
         }
       } else {
 #pragma unroll
         for (int i = 0; i < S::Keys / kRowsAt; ++i) {
           const int r = i * kRowsAt + lane / S::CK, ch = lane % S::CK;
-          const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
+          const int blk = __shfl_sync(~0u, pl.blk[0], r), off = __shfl_sync(~0u, pl.off[0], r);
           const bool ok = off >= 0;
           const long long kx = ok ? blk * p.k_bs + (long long)off * p.k_rs : 0, vx = ok ? blk * p.v_bs + (long long)off * p.v_rs : 0;
           cp_async16(st + kv_at<S::CK>(r, ch), kb + kx * S::E + ch * 16, ok ? 16 : 0);
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < S::Keys / kPeRowsAt; ++i) {
           const int r = i * kPeRowsAt + lane / S::CP, ch = lane % S::CP;
-          const int blk = __shfl_sync(~0u, pl.blk, r), off = __shfl_sync(~0u, pl.off, r);
+          const int blk = __shfl_sync(~0u, pl.blk[0], r), off = __shfl_sync(~0u, pl.off[0], r);
           const bool ok = off >= 0;
           const long long x = ok ? blk * p.kpe_bs + (long long)off * p.kpe_rs : 0;
           cp_async16(st + kPeOff + kv_at<S::CP>(r, ch), pb + x * S::E + ch * 16, ok ? 16 : 0);
@@ -440,72 +454,88 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------- joining
-// One warp per row of an item that worker w1 began and others went on with:
-// with weights u_i = 2^(m_i - m) of its pieces,
+// The rows of an item that worker w1 began and others went on with: with
+// weights u_i = 2^(m_i - m) of its pieces,
 //   l = sum u_i l_i,  out = sum u_i o_i / l,  lse = (m + log2 l) * ln 2.
-// `rows` is the most rows an item of the call has, R the rows of a slot.
+// `per` warps (1, 2, 4, 8 or 16) share a record's rows, a warp taking one row at a
+// time with 16 pieces in flight.  Bound by latency, so the grid is what fits
+// on the GPU at once: with a block for each eight possible rows 12 sequences
+// with 12 rows per head took 47 us instead of 39.
+constexpr int kJoinFlight = 16;
 template <typename T>
-__global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constant__ PagedKvParams p, int rows, int R) {
+__global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constant__ PagedKvParams p, int per, int R) {
   using E = Elem<T>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = p.plan.heads, H = G * p.kv_heads;
   grid_dep_wait();  // (every block waits, so that this kernel never ends before the one that makes the pieces)
-  const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int w1 = x / rows, r = x - w1 * rows;
-  if (w1 >= p.plan.workers) return;
-  const PagedJoin j = p.plan.joins[w1];
-  const int G = p.plan.heads, H = G * p.kv_heads, w2 = j.last_worker;
-  if (r >= j.rows || j.rows > R || j.row < 0 || (long long)j.row + j.rows > (long long)p.plan.T * G || j.pad < 0 ||
-      j.pad >= p.kv_heads || w2 < w1 || w2 >= p.plan.workers)
-    return;
-  const int tok = (j.row + r) / G;
-  const size_t orow = (size_t)tok * H + j.pad * G + (j.row + r) - tok * G;
-  const int n = w2 - w1 + 1;
-  auto slot = [&](int i) { return (size_t)(w1 + i) * 2 + (i == 0 ? 1 : 0); };
-  auto ml = [&](int i) { return i < n ? reinterpret_cast<const float2*>(p.plan.part_ml)[slot(i) * R + r] : make_float2(-INFINITY, 0.f); };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const float2 a = ml(i);
-    if (a.y != 0.f) m = fmaxf(m, a.x);
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const float2 a = ml(i0 + lane);
-    const float f = a.y == 0.f ? 0.f : exp2f(a.x - m);
-    l += f * a.y;
-    const int end = min(32, n - i0);
-    for (int j0 = 0; j0 < end; j0 += 8) {
-      float4 y[8];
-      float u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        u[k] = __shfl_sync(~0u, f, (j0 + k) & 31);
-        if (j0 + k >= end) u[k] = 0.f;
-        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u[k] != 0.f) y[k] = reinterpret_cast<const float4*>(p.plan.part_o + (slot(i0 + j0 + k) * R + r) * kV)[lane];
+  // (neighbouring records to a group: a long item leaves one record in many, at even distances)
+  const int groups = gridDim.x * 8 / per, each = (p.plan.workers + groups - 1) / groups, first = (blockIdx.x * 8 + warp) / per * each;
+  for (int c0 = 0; c0 < each; c0 += 32) {
+   // (a lane looks at a record: most of them are empty)
+   const int mine = first + c0 + lane;
+   PagedJoin rec = {0, 0, 0, 0};
+   if (c0 + lane < each && mine < p.plan.workers) rec = p.plan.joins[mine];
+   const bool fits = rec.rows > 0 && rec.rows <= R && rec.row >= 0 && (long long)rec.row + rec.rows <= (long long)p.plan.T * G &&
+                     rec.pad >= 0 && rec.pad < p.kv_heads && rec.last_worker >= mine && rec.last_worker < p.plan.workers;
+   for (uint32_t left = __ballot_sync(~0u, fits); left; left &= left - 1) {
+    const int from = __ffs(left) - 1, w1 = first + c0 + from;
+    const PagedJoin j = {__shfl_sync(~0u, rec.row, from), __shfl_sync(~0u, rec.rows, from), __shfl_sync(~0u, rec.last_worker, from),
+                         __shfl_sync(~0u, rec.pad, from)};
+    const int n = j.last_worker - w1 + 1;
+    auto slot = [&](int i) { return (size_t)(w1 + i) * 2 + (i == 0 ? 1 : 0); };
+    for (int r = (blockIdx.x * 8 + warp) % per; r < j.rows; r += per) {
+      const int tok = (j.row + r) / G;
+      const size_t orow = (size_t)tok * H + j.pad * G + (j.row + r) - tok * G;
+      auto ml = [&](int i) { return i < n ? reinterpret_cast<const float2*>(p.plan.part_ml)[slot(i) * R + r] : make_float2(-INFINITY, 0.f); };
+      float m = -INFINITY;
+      for (int i = lane; i < n; i += 32) {
+        const float2 a = ml(i);
+        if (a.y != 0.f) m = fmaxf(m, a.x);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        o.x += u[k] * y[k].x;
-        o.y += u[k] * y[k].y;
-        o.z += u[k] * y[k].z;
-        o.w += u[k] * y[k].w;
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const float2 a = ml(i0 + lane);
+        const float f = a.y == 0.f ? 0.f : exp2f(a.x - m);
+        l += f * a.y;
+        const int end = min(32, n - i0);
+        for (int j0 = 0; j0 < end; j0 += kJoinFlight) {
+          float4 y[kJoinFlight];
+          float u[kJoinFlight];
+#pragma unroll
+          for (int k = 0; k < kJoinFlight; ++k) {
+            // (all loads are made, those past the end of the last piece: under a condition each would wait for the one
+            // before.  A piece without keys has zeros.)
+            const int i = min(j0 + k, end - 1);
+            u[k] = __shfl_sync(~0u, f, i);
+            if (j0 + k >= end) u[k] = 0.f;
+            y[k] = reinterpret_cast<const float4*>(p.plan.part_o + (slot(i0 + i) * R + r) * kV)[lane];
+          }
+#pragma unroll
+          for (int k = 0; k < kJoinFlight; ++k) {
+            o.x += u[k] * y[k].x;
+            o.y += u[k] * y[k].y;
+            o.z += u[k] * y[k].z;
+            o.w += u[k] * y[k].w;
+          }
+        }
       }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+      const float iv = l == 0.f ? 0.f : 1.f / l;
+      reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
+          make_uint2(E::pack(o.x * iv, o.y * iv), E::pack(o.z * iv, o.w * iv));
+      if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+   }
   }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  const float iv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
-      make_uint2(E::pack(o.x * iv, o.y * iv), E::pack(o.z * iv, o.w * iv));
-  if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T, bool kI8>
 cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
-  const bool whole = p.plan.page % KvCfg<kI8>::Keys == 0;
+  const bool whole = p.plan.page % 16 == 0;
   if (whole)
     paged_kv_kernel<T, kI8, true><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
   else
@@ -513,11 +543,12 @@ cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr int R = KvCfg<kI8>::R;
-  // (every item of a call with as many tokens in each sequence has at most these rows)
-  const long long per = (long long)p.plan.n_uniform * p.plan.heads;
-  const int rows = !p.plan.cu_q && per < R ? (int)per : R;
+  // rows of an item (with ragged chunks the average, which is all the host knows)
+  const long long rows = (long long)(p.plan.T / p.plan.nseq > 0 ? p.plan.T / p.plan.nseq : 1) * p.plan.heads;
+  const int per = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 || R == 8 ? 8 : 16;
+  const int blocks = (p.plan.workers * per + 15) / 8, most = p.plan.workers / kKvWarps * 2;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((p.plan.workers * rows + 7) / 8);
+  c.gridDim = dim3((blocks < most ? blocks : most) & ~1);  // (16 warps are two blocks)
   c.blockDim = dim3(256);
   c.stream = stream;
   cudaLaunchAttribute at = {};
@@ -525,7 +556,7 @@ cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_kv_join_kernel<T>, p, rows, R);
+  return cudaLaunchKernelEx(&c, paged_kv_join_kernel<T>, p, per, R);
 }
 
 template <typename T>
