@@ -118,12 +118,11 @@ struct PagedKvParams {
   int qn_ts, qn_hs, qp_ts, qp_hs;
   int kv_heads;
 };
-constexpr int kKvWarps = 8;  // workers per CTA
-constexpr int kKvRows = 16;  // query rows of an item
-constexpr int kKvRowsI8 = 8;
+constexpr int kKvWarps = 8;                 // workers per CTA
+constexpr int kKvRows = 16, kKvRowsT = 8;   // query rows of an item, and in the kernel for few rows
 inline int paged_kv_workers(int num_sms) { return num_sms * kKvWarps; }
 cudaError_t paged_kv_prepare(bool bf16);
-cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, cudaStream_t stream);
+cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- prompt attention
 struct PromptTensor {

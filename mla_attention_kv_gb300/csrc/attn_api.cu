@@ -251,13 +251,13 @@ mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args
   s.cu_q = a.cu_q; s.kv_lens = a.kv_lens; s.table = a.block_table; s.out = a.out; s.lse = a.lse; s.part_o = h->part_o;
   s.part_ml = h->part_ml; s.joins = h->joins; s.status = h->status; s.table_stride = a.table_stride; s.page = a.page_size;
   s.nblocks = a.num_blocks; s.nseq = a.num_seqs; s.T = a.T; s.heads = H / KH; s.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs;
-  s.workers = paged_kv_workers(h->num_sms); s.scale_log2 = h->scale_log2;
+  s.scale_log2 = h->scale_log2;
   p.q_nope = a.q_nope; p.q_pe = a.q_pe; p.k = a.k_cache; p.v = a.v_cache; p.kpe = a.kpe_cache; p.k_scale = a.k_scale;
   p.v_scale = a.v_scale; p.kpe_scale = a.kpe_scale; p.k_bs = a.k_block_stride; p.k_hs = a.k_head_stride;
   p.v_bs = a.v_block_stride; p.v_hs = a.v_head_stride; p.kpe_bs = a.kpe_block_stride; p.k_rs = a.k_row_stride;
   p.v_rs = a.v_row_stride; p.kpe_rs = a.kpe_row_stride; p.qn_ts = a.q_nope_token_stride; p.qn_hs = a.q_nope_head_stride;
   p.qp_ts = a.q_pe_token_stride; p.qp_hs = a.q_pe_head_stride; p.kv_heads = KH;
-  cudaError_t e = paged_kv_launch(h->cfg.dtype == MLA_BF16, i8, p, stream);
+  cudaError_t e = paged_kv_launch(h->cfg.dtype == MLA_BF16, i8, p, h->num_sms, stream);
   if (e != cudaSuccess) return fail(e, "paged K/V attention launch");
   h->last_launches = 2;
   return MLA_OK;

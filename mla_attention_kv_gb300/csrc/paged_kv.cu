@@ -18,17 +18,24 @@
 // with its own share of the keys, its own ring of stages filled by 16-byte
 // cp.async (any page size; a page may end anywhere in a stage) and its own
 // running softmax: nothing in the loop waits for another warp.  The products
-// run on mma.sync with 16 query rows (a stage's chain of loads, not the
-// tensor cores' rate, is what a warp waits for).
+// run on mma.sync, in one of two forms:
+//   up to 8 rows: S^T = K Q^T and O^T = V^T P^T, keys and value columns being
+//     the 16 rows of an operand and the query rows its 8 columns.  P^T turns
+//     from result to operand by a transposing move.  Half the products of the
+//     other form, and 32 registers of output instead of 64;
+//   up to 16 rows (16-bit caches): S = Q K^T and O = P V.
+// Eight warps per SM: eleven, which the first form has room for, bring more
+// pieces to join and no more bandwidth (64 sequences of up to 4096 keys, 16
+// heads: 182 us and 181).
 //
 // int8: codes become fp16 exactly (byte ^ 0x80 as the low byte of 1024 + u,
 // minus 1152).  The scaled queries are split in two fp16 parts, high and low,
-// that take rows 0-7 and 8-15 of the same operand, so the products see them
-// to about 2^-22 at no cost; an item then has 8 rows.  A thread's four
-// consecutive codes of a key are four columns of one k-step in an order of
-// its own, and the queries are laid out in the same order.
+// multiplied one after the other into the same sums, so the products see them
+// to about 2^-22.  A thread's four consecutive codes of a key are four columns
+// of one k-step in an order of its own, and the queries are laid out in the
+// same order.
 #include "attn.h"
-#include "common.cuh"
+#include "attn_tc.cuh"
 #include "paged_kv_plan.cuh"
 
 namespace mla {
@@ -42,13 +49,15 @@ constexpr int kKvThreads = kKvWarps * 32;
 constexpr int kKvSmem = kKvWarps * kWarpBytes + (int)sizeof(PlanShared);
 static_assert(kKvSmem <= 227 * 1024, "shared memory");
 
-template <bool kI8>
+// kT: up to 8 query rows per item.
+template <bool kI8, bool kT>
 struct KvCfg {
-  static constexpr int R = kI8 ? kKvRowsI8 : kKvRows;
+  static constexpr int R = kT ? kKvRowsT : kKvRows;
   static constexpr int E = kI8 ? 1 : 2;        // bytes per value
   static constexpr int Keys = kI8 ? 32 : 16;   // per stage
   static constexpr int CK = kNope * E / 16;    // 16-byte chunks of a key (and value) row
   static constexpr int CP = kRope * E / 16;    // of a rotated part
+  static_assert(R * kV * 4 <= kWarpBytes, "results pass through the ring");
 };
 
 // Where chunk c of row r lies within a block of rows of 8 or 16 chunks (keys,
@@ -68,12 +77,20 @@ __device__ __forceinline__ uint32_t kv_half2(uint32_t biased, uint32_t selector)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The 8 x 8 matrix of 16-bit values that a warp holds (lane = row * 4 + pair), transposed.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // kWhole: pages are multiples of 16 rows, so that each 16 rows of a stage lie
 // in one page.
-template <typename T, bool kI8, bool kWhole>
+template <typename T, bool kI8, bool kT, bool kWhole>
 __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_constant__ PagedKvParams p) {
   using E = Elem<T>;
-  using S = KvCfg<kI8>;
+  using S = KvCfg<kI8, kT>;
+  static_assert(kT || !kI8, "int8: 8 rows");
   constexpr int R = S::R;
   constexpr bool kBf16 = !kI8 && E::kBf16;  // (codes are multiplied as fp16)
   extern __shared__ __align__(128) unsigned char smem[];
@@ -209,16 +226,16 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
     }
 
     // ---- queries, as operand fragments (rows past the item's end are zero)
-    uint32_t qf[12][4];
-    float row_scale = p.plan.scale_log2;
     auto q_row = [&](int r, const T*& qn, const T*& qp) {
       const int tok = (row0 + r) / G, hd = c.head * G + (row0 + r) - tok * G;
       qn = static_cast<const T*>(p.q_nope) + (long long)(sq.begin + tok) * p.qn_ts + (long long)hd * p.qn_hs;
       qp = static_cast<const T*>(p.q_pe) + (long long)(sq.begin + tok) * p.qp_ts + (long long)hd * p.qp_hs;
     };
+    uint32_t qf[12][kT && !kI8 ? 2 : 4];
+    float row_scale[2] = {p.plan.scale_log2, p.plan.scale_log2};
     if constexpr (!kI8) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < (kT ? 1 : 2); ++hf) {
         const int r = g + hf * 8;
         const bool ok = r < live;
         const T *qn = nullptr, *qp = nullptr;
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
         for (int k = 0; k < 12; ++k) {
           const T* src = k < 8 ? qn + k * 16 : qp + (k - 8) * 16;
           qf[k][hf] = ok ? *reinterpret_cast<const uint32_t*>(src + 2 * q4) : 0;
-          qf[k][2 + hf] = ok ? *reinterpret_cast<const uint32_t*>(src + 8 + 2 * q4) : 0;
+          qf[k][(kT ? 1 : 2) + hf] = ok ? *reinterpret_cast<const uint32_t*>(src + 8 + 2 * q4) : 0;
         }
       }
     } else {
@@ -252,8 +269,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
       const int up = mx > 0.f && mx < INFINITY ? min(13 - ilogbf(mx), 100) : 0;
-      const float f = scalbnf(1.f, up);
-      row_scale *= scalbnf(1.f, -up);
+      const float f = scalbnf(1.f, up), down = p.plan.scale_log2 * scalbnf(1.f, -up);
+      row_scale[0] = __shfl_sync(~0u, down, 8 * q4);  // rows 2 q4 and 2 q4 + 1 (lane 4 r holds row r)
+      row_scale[1] = __shfl_sync(~0u, down, 8 * q4 + 4);
 #pragma unroll
       for (int k = 0; k < 12; ++k)
 #pragma unroll
@@ -262,136 +280,164 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
           const __half2 hi = __floats2half2_rn(y0, y1);
           const float2 hf = __half22float2(hi);
           const __half2 lo = __floats2half2_rn(y0 - hf.x, y1 - hf.y);
-          qf[k][2 * i] = *reinterpret_cast<const uint32_t*>(&hi);
-          qf[k][2 * i + 1] = *reinterpret_cast<const uint32_t*>(&lo);
+          qf[k][i] = *reinterpret_cast<const uint32_t*>(&hi);
+          qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&lo);
         }
     }
-    const int lim0 = g < live ? sq.keys_of_row(row0 + g, G) : 0;
-    const int lim1 = !kI8 && g + 8 < live ? sq.keys_of_row(row0 + g + 8, G) : 0;
+    // this lane's two rows of the softmax: 2 q4 and 2 q4 + 1 (kT), g and g + 8
+    const int ra = kT ? 2 * q4 : g, rb = kT ? 2 * q4 + 1 : g + 8;
+    const int lim0 = ra < live ? sq.keys_of_row(row0 + ra, G) : 0, lim1 = rb < live ? sq.keys_of_row(row0 + rb, G) : 0;
+    const int lim_all = sq.keys_of_row(row0, G);  // keys that all rows see
 
-    float acc[16][4];
+    constexpr int NO = kT ? 8 : 16;
+    float acc[NO][4];
 #pragma unroll
-    for (int n = 0; n < 16; ++n)
+    for (int n = 0; n < NO; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (int t = t0; t < t1; ++t) {
       const Place ahead = place_of(t + kStages);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t st = ring + (t % kStages) * kStageBytes;
-      constexpr int NT = S::Keys / 8;
-      float sc[NT][4];
+      // ---- scores: sc[n] has (kT) keys 16 n + g, + 8 for rows ra, rb, or keys 8 n + 2 q4, + 1 for row ra, then for rb
+      constexpr int NS = kT ? S::Keys / 16 : S::Keys / 8;
+      float sc[NS][4], s2[NS][4];  // (two sets of sums: shorter chains)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
-      if constexpr (!kI8) {
-        const int r = (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
-        float s2[NT][4];  // (a second set of sums: shorter chains)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s2[n][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 12; ++k) {
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(k < 8 ? st + kv_at<S::CK>(r, 2 * k + cc) : st + kPeOff + kv_at<S::CP>(r, 2 * (k - 8) + cc), b0, b1, b2, b3);
-          mma16816<kBf16>(k & 1 ? s2[0] : sc[0], qf[k], b0, b1);
-          mma16816<kBf16>(k & 1 ? s2[1] : sc[1], qf[k], b2, b3);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[n][i] += s2[n][i];
-      } else {
+        for (int i = 0; i < 4; ++i) sc[n][i] = s2[n][i] = 0.f;
+      if constexpr (kI8) {
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
           uint32_t x[4];
           ldsm_x4(k < 8 ? st + kv_at<S::CK>(lane, k) : st + kPeOff + kv_at<S::CP>(lane, k - 8), x[0], x[1], x[2], x[3]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t u = x[n] ^ 0x80808080u;
-            mma16816<false>(sc[n], qf[k], kv_half2(u, 0x4140), kv_half2(u, 0x4342));
+          for (int n = 0; n < 4; ++n) x[n] ^= 0x80808080u;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t af[4] = {kv_half2(x[2 * n], 0x4140), kv_half2(x[2 * n + 1], 0x4140), kv_half2(x[2 * n], 0x4342),
+                                    kv_half2(x[2 * n + 1], 0x4342)};
+            mma16816<false>(sc[n], af, qf[k][0], qf[k][1]);
+            mma16816<false>(s2[n], af, qf[k][2], qf[k][3]);
           }
+        }
+      } else if constexpr (kT) {
+        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          uint32_t af[4];
+          ldsm_x4(k < 8 ? st + kv_at<S::CK>(r, 2 * k + cc) : st + kPeOff + kv_at<S::CP>(r, 2 * (k - 8) + cc), af[0], af[1], af[2], af[3]);
+          mma16816<E::kBf16>(k & 1 ? s2[0] : sc[0], af, qf[k][0], qf[k][1]);
+        }
+      } else {
+        const int r = (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(k < 8 ? st + kv_at<S::CK>(r, 2 * k + cc) : st + kPeOff + kv_at<S::CP>(r, 2 * (k - 8) + cc), b0, b1, b2, b3);
+          mma16816<E::kBf16>(k & 1 ? s2[0] : sc[0], qf[k], b0, b1);
+          mma16816<E::kBf16>(k & 1 ? s2[1] : sc[1], qf[k], b2, b3);
         }
       }
-      // ---- softmax: row g in sc[.][0..1], row g + 8 in sc[.][2..3]
-      const int k0 = t * S::Keys + 2 * q4;
+      // ---- softmax
       float x0m = -INFINITY, x1m = -INFINITY;
+      // (value i of sc[n]: its row is the lane's second, its key that far from the stage's first)
+      auto second = [](int i) { return kT ? (i & 1) : (i >> 1); };
+      auto key_of = [&](int n, int i) { return kT ? 16 * n + g + 8 * (i >> 1) : 8 * n + 2 * q4 + (i & 1); };
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = k0 + n * 8 + i;
-          const float u = kI8 ? sc[n][i] + sc[n][2 + i] : sc[n][i];
-          sc[n][i] = k < lim0 ? u * row_scale : -INFINITY;
-          x0m = fmaxf(x0m, sc[n][i]);
-          if (!kI8) {
-            sc[n][2 + i] = k < lim1 ? sc[n][2 + i] * row_scale : -INFINITY;
-            x1m = fmaxf(x1m, sc[n][2 + i]);
-          }
+        for (int i = 0; i < 4; ++i) sc[n][i] = (sc[n][i] + s2[n][i]) * row_scale[second(i)];
+      if ((t + 1) * S::Keys > lim_all) {  // (the same for all lanes)
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t * S::Keys + key_of(n, i) >= (second(i) ? lim1 : lim0)) sc[n][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (second(i)) x1m = fmaxf(x1m, sc[n][i]);
+          else x0m = fmaxf(x0m, sc[n][i]);
         }
 #pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {
+      for (int d = kT ? 4 : 1; d <= (kT ? 16 : 2); d <<= 1) {
         x0m = fmaxf(x0m, __shfl_xor_sync(~0u, x0m, d));
-        if (!kI8) x1m = fmaxf(x1m, __shfl_xor_sync(~0u, x1m, d));
+        x1m = fmaxf(x1m, __shfl_xor_sync(~0u, x1m, d));
       }
       const float n0 = fmaxf(m0, x0m), n1 = fmaxf(m1, x1m);
       const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;  // (a row with no key so far)
-      const float a0 = n0 == m0 ? 1.f : exp2f(m0 - u0), a1 = n1 == m1 ? 1.f : exp2f(m1 - u1);
-      m0 = n0;
-      m1 = n1;
-      if (__any_sync(~0u, a0 != 1.f || a1 != 1.f)) {
+      if (__any_sync(~0u, n0 != m0 || n1 != m1)) {
+        const float a0 = ex2(m0 - u0), a1 = ex2(m1 - u1);
         l0 *= a0;
         l1 *= a1;
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          acc[n][0] *= a0;
-          acc[n][1] *= a0;
-          acc[n][2] *= a1;
-          acc[n][3] *= a1;
-        }
-      }
-      uint32_t pf[NT / 2][4];
+        for (int n = 0; n < NO; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float e0 = exp2f(sc[n][0] - u0), e1 = exp2f(sc[n][1] - u0);
-        l0 += e0 + e1;
-        if constexpr (kI8) {
-          const __half2 h = __floats2half2_rn(e0, e1);
-          pf[n / 2][(n & 1) * 2] = *reinterpret_cast<const uint32_t*>(&h);
-          pf[n / 2][(n & 1) * 2 + 1] = 0;
-        } else {
-          const float e2 = exp2f(sc[n][2] - u1), e3 = exp2f(sc[n][3] - u1);
-          l1 += e2 + e3;
-          pf[n / 2][(n & 1) * 2] = E::pack(e0, e1);
-          pf[n / 2][(n & 1) * 2 + 1] = E::pack(e2, e3);
-        }
+          for (int i = 0; i < 4; ++i) acc[n][i] *= second(i) ? a1 : a0;
+        m0 = n0;
+        m1 = n1;
       }
-      // ---- output
-      if constexpr (!kI8) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[n][i] = ex2(sc[n][i] - (second(i) ? u1 : u0));
+          if (second(i)) l1 += sc[n][i];
+          else l0 += sc[n][i];
+        }
+      // ---- output: acc[n] has (kT) value columns 16 n + g, + 8 (int8: 16 n + 2 g, + 1) for rows ra, rb, or columns
+      // 8 n + 2 q4, + 1 for row ra, then for rb
+      if constexpr (kT) {
+        uint32_t pf[NS][2];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x;
+            if constexpr (kI8)
+              x = Elem<__half>::pack(sc[n][2 * i], sc[n][2 * i + 1]);
+            else
+              x = E::pack(sc[n][2 * i], sc[n][2 * i + 1]);
+            pf[n][i] = movmatrix(x);
+          }
+        if constexpr (kI8) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            uint32_t x[4];
+            ldsm_x4_trans(st + kVOff + kv_at<S::CK>(lane, n), x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] ^= 0x80808080u;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t af[4] = {kv_half2(x[2 * k], 0x4240), kv_half2(x[2 * k], 0x4341), kv_half2(x[2 * k + 1], 0x4240),
+                                      kv_half2(x[2 * k + 1], 0x4341)};
+              mma16816<false>(acc[n], af, pf[k][0], pf[k][1]);
+            }
+          }
+        } else {
+          const int r = (lane & 7) + (lane >> 4) * 8, cc = (lane >> 3) & 1;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            uint32_t af[4];
+            ldsm_x4_trans(st + kVOff + kv_at<S::CK>(r, 2 * n + cc), af[0], af[1], af[2], af[3]);
+            mma16816<E::kBf16>(acc[n], af, pf[0][0], pf[0][1]);
+          }
+        }
+      } else {
+        const uint32_t pf[4] = {E::pack(sc[0][0], sc[0][1]), E::pack(sc[0][2], sc[0][3]), E::pack(sc[1][0], sc[1][1]),
+                                E::pack(sc[1][2], sc[1][3])};
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
           uint32_t b0, b1, b2, b3;
           ldsm_x4_trans(st + kVOff + kv_at<S::CK>(lane & 15, 2 * n + (lane >> 4)), b0, b1, b2, b3);
-          mma16816<kBf16>(acc[2 * n], pf[0], b0, b1);
-          mma16816<kBf16>(acc[2 * n + 1], pf[0], b2, b3);
-        }
-      } else {
-        // chunk n: acc[2n] has its even columns, acc[2n + 1] its odd ones
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          uint32_t x[4];
-          ldsm_x4_trans(st + kVOff + kv_at<S::CK>(lane, n), x[0], x[1], x[2], x[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] ^= 0x80808080u;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mma16816<false>(acc[2 * n], pf[k], kv_half2(x[2 * k], 0x4240), kv_half2(x[2 * k + 1], 0x4240));
-            mma16816<false>(acc[2 * n + 1], pf[k], kv_half2(x[2 * k], 0x4341), kv_half2(x[2 * k + 1], 0x4341));
-          }
+          mma16816<E::kBf16>(acc[2 * n], pf, b0, b1);
+          mma16816<E::kBf16>(acc[2 * n + 1], pf, b2, b3);
         }
       }
       __syncwarp();  // the stage is free
@@ -401,55 +447,49 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
     cp_async_wait<0>();
     __syncwarp();
 
-    // ---- results
+    // ---- results, through the ring's place, so that a warp stores whole rows
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
+    for (int d = kT ? 4 : 1; d <= (kT ? 16 : 2); d <<= 1) {
       l0 += __shfl_xor_sync(~0u, l0, d);
       l1 += __shfl_xor_sync(~0u, l1, d);
     }
-    const size_t slot = (size_t)w * 2 + (c.lo < x0 ? 0 : 1);
+    float* place = reinterpret_cast<float*>(smem + warp * kWarpBytes);
 #pragma unroll
-    for (int hf = 0; hf < (kI8 ? 1 : 2); ++hf) {
-      const int r = g + hf * 8;
-      if (r >= live) continue;
-      const float l = hf ? l1 : l0, m = hf ? m1 : m0;
-      const int tok = (row0 + r) / G, hd = c.head * G + (row0 + r) - tok * G;
-      const size_t orow = (size_t)(sq.begin + tok) * H + hd;
-      const float iv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      T* out = static_cast<T*>(p.plan.out) + orow * kV;
-      float* po = p.plan.part_o + (slot * R + r) * kV;
-      if (q4 == 0) {
-        if (!whole) {
-          float* ml = p.plan.part_ml + (slot * R + r) * 2;
-          ml[0] = m;
-          ml[1] = l;
-        } else if (p.plan.lse) {
-          p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
-      }
-      if constexpr (!kI8) {
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const float y0 = acc[n][2 * hf] * iv, y1 = acc[n][2 * hf + 1] * iv;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(out + n * 8 + 2 * q4) = E::pack(y0, y1);
-          else
-            *reinterpret_cast<float2*>(po + n * 8 + 2 * q4) = make_float2(y0, y1);
-        }
+    for (int n = 0; n < NO; ++n) {
+      if constexpr (!kT) {
+        *reinterpret_cast<float2*>(place + ra * kV + n * 8 + 2 * q4) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(place + rb * kV + n * 8 + 2 * q4) = make_float2(acc[n][2], acc[n][3]);
       } else {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int col = n * 16 + 4 * q4;
-          const float4 vs = *reinterpret_cast<const float4*>(p.v_scale + c.head * kV + col);
-          const float4 y = make_float4(acc[2 * n][0] * iv * vs.x, acc[2 * n + 1][0] * iv * vs.y, acc[2 * n][1] * iv * vs.z,
-                                       acc[2 * n + 1][1] * iv * vs.w);
-          if (whole)
-            *reinterpret_cast<uint2*>(out + col) = make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));
-          else
-            *reinterpret_cast<float4*>(po + col) = y;
-        }
+        const int c0 = n * 16 + (kI8 ? 2 * g : g), c1 = c0 + (kI8 ? 1 : 8);
+        place[ra * kV + c0] = acc[n][0];
+        place[rb * kV + c0] = acc[n][1];
+        place[ra * kV + c1] = acc[n][2];
+        place[rb * kV + c1] = acc[n][3];
       }
     }
+    __syncwarp();
+    const size_t slot = (size_t)w * 2 + (c.lo < x0 ? 0 : 1);
+    float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (kI8) vs = reinterpret_cast<const float4*>(p.v_scale + c.head * kV)[lane];
+    for (int r = 0; r < live; ++r) {
+      // (lane r / 2 holds row r in its first or second place, or lanes 4 r and 4 (r - 8))
+      const int from = kT ? r >> 1 : (r & 7) * 4;
+      const bool sec = kT ? r & 1 : r >= 8;
+      const float l = __shfl_sync(~0u, sec ? l1 : l0, from), m = __shfl_sync(~0u, sec ? m1 : m0, from);
+      const int tok = (row0 + r) / G;
+      const size_t orow = (size_t)(sq.begin + tok) * H + c.head * G + (row0 + r) - tok * G;
+      float4 y = reinterpret_cast<const float4*>(place + r * kV)[lane];
+      const float iv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      y = make_float4(y.x * iv * vs.x, y.y * iv * vs.y, y.z * iv * vs.z, y.w * iv * vs.w);
+      if (whole) {
+        reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] = make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));
+        if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        reinterpret_cast<float4*>(p.plan.part_o + (slot * R + r) * kV)[lane] = y;
+        if (lane == 0) reinterpret_cast<float2*>(p.plan.part_ml)[slot * R + r] = make_float2(m, l);
+      }
+    }
+    __syncwarp();  // (the ring is filled again by the next item)
   }
 }
 
@@ -533,20 +573,25 @@ __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constan
   }
 }
 
-template <typename T, bool kI8>
-cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
-  const bool whole = p.plan.page % 16 == 0;
-  if (whole)
-    paged_kv_kernel<T, kI8, true><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
+// Query rows per KV head and sequence (with ragged chunks the average, which
+// is all the host knows).
+long long kv_rows(const PagedKvParams& p) {
+  return (long long)(p.plan.T / p.plan.nseq > 0 ? p.plan.T / p.plan.nseq : 1) * p.plan.heads;
+}
+
+template <typename T, bool kI8, bool kT>
+cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
+  using S = KvCfg<kI8, kT>;
+  p.plan.workers = paged_kv_workers(num_sms);
+  if (p.plan.page % 16 == 0)
+    paged_kv_kernel<T, kI8, kT, true><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   else
-    paged_kv_kernel<T, kI8, false><<<p.plan.workers / kKvWarps, kKvThreads, kKvSmem, stream>>>(p);
+    paged_kv_kernel<T, kI8, kT, false><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  constexpr int R = KvCfg<kI8>::R;
-  // rows of an item (with ragged chunks the average, which is all the host knows)
-  const long long rows = (long long)(p.plan.T / p.plan.nseq > 0 ? p.plan.T / p.plan.nseq : 1) * p.plan.heads;
-  const int per = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 || R == 8 ? 8 : 16;
-  const int blocks = (p.plan.workers * per + 15) / 8, most = p.plan.workers / kKvWarps * 2;
+  const long long rows = kv_rows(p);
+  const int per = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 || S::R == 8 ? 8 : 16;
+  const int blocks = (p.plan.workers * per + 15) / 8, most = num_sms * 2;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((blocks < most ? blocks : most) & ~1);  // (16 warps are two blocks)
   c.blockDim = dim3(256);
@@ -556,27 +601,33 @@ cudaError_t launch(const PagedKvParams& p, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_kv_join_kernel<T>, p, per, R);
+  return cudaLaunchKernelEx(&c, paged_kv_join_kernel<T>, p, per, S::R);
 }
 
+template <typename T, bool kI8, bool kT>
+cudaError_t prepare_one() {
+  const cudaError_t e = cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+  return e == cudaSuccess ? cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem) : e;
+}
 template <typename T>
 cudaError_t prepare() {
-  const void* k[4] = {(const void*)paged_kv_kernel<T, false, false>, (const void*)paged_kv_kernel<T, false, true>,
-                      (const void*)paged_kv_kernel<T, true, false>, (const void*)paged_kv_kernel<T, true, true>};
-  for (const void* f : k) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  cudaError_t e = prepare_one<T, false, false>();
+  if (e == cudaSuccess) e = prepare_one<T, false, true>();
+  if (e == cudaSuccess) e = prepare_one<T, true, true>();
+  return e;
+}
+template <typename T>
+cudaError_t launch_any(bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream) {
+  if (i8) return launch<T, true, true>(p, num_sms, stream);
+  return kv_rows(p) <= kKvRowsT ? launch<T, false, true>(p, num_sms, stream) : launch<T, false, false>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t paged_kv_prepare(bool bf16) { return bf16 ? prepare<__nv_bfloat16>() : prepare<__half>(); }
 
-cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, cudaStream_t stream) {
-  if (i8) return bf16 ? launch<__nv_bfloat16, true>(p, stream) : launch<__half, true>(p, stream);
-  return bf16 ? launch<__nv_bfloat16, false>(p, stream) : launch<__half, false>(p, stream);
+cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream) {
+  return bf16 ? launch_any<__nv_bfloat16>(i8, p, num_sms, stream) : launch_any<__half>(i8, p, num_sms, stream);
 }
 
 }  // namespace mla
