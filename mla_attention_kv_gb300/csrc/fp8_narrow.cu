@@ -25,6 +25,7 @@ namespace mla {
 namespace {
 
 constexpr uint32_t kWTile = 128 * 128;
+constexpr int kNwSplit = 8;  // most CTAs of a cluster
 
 template <int TN>
 struct NwCfg {
@@ -216,18 +217,23 @@ __global__ void __launch_bounds__(NwCfg<TN>::kThreads, 2) fp8_narrow_kernel(cons
     const int n = nt * 128 + lane * 4;
     for (int j = live * rank / split + warp - 2; j < live * (rank + 1) / split; j += S::kEpi) {
       const uint32_t at = sbase + (j * 128 + lane * 4) * 4;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r = 0; r < split; ++r) {
-        float4 v;
+      // (all parts are requested before the first is waited for)
+      float4 v[kNwSplit];
+#pragma unroll
+      for (int r = 0; r < kNwSplit; ++r)
         asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(tc::mapa(at, r))
+                     : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                     : "r"(tc::mapa(at, r < split ? r : rank))
                      : "memory");
-        y.x += v.x;
-        y.y += v.y;
-        y.z += v.z;
-        y.w += v.w;
-      }
+      float4 y = v[0];
+#pragma unroll
+      for (int r = 1; r < kNwSplit; ++r)
+        if (r < split) {
+          y.x += v[r].x;
+          y.y += v[r].y;
+          y.z += v[r].z;
+          y.w += v[r].w;
+        }
       if (n < p.N)  // (N is a multiple of 8)
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (size_t)(t0 + j) * p.out_stride + n) =
             make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));

@@ -13,8 +13,8 @@
 // block of 128 columns belongs to 16 lanes, 8 values (16 bytes) each, so its
 // maximum takes four shuffles.  Without a norm a lane has kUnroll blocks of
 // one row in flight; with one, a row stays in registers between the sum of
-// squares and the scaling: in a warp's up to 2048 columns, in a CTA's up to
-// 8192, and longer ones are read again (from L2).
+// squares and the scaling: a warp's (up to 2048 columns, many rows) or a CTA's
+// (up to 8192; what is beyond is read again, from L2).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -57,12 +57,13 @@ __device__ __forceinline__ void emit_block(const float* f, bool live, uint8_t* q
 }
 
 // No norm: half-warp i of a CTA takes row blockIdx.y * 16 + i, kUnroll blocks
-// of columns.
+// of columns.  (Neighbouring CTAs take neighbouring columns: 8192 x 7168 30.7
+// us, 32.4 the other way round; scales gathered in shared memory first 31.5.)
 template <typename T, int kUnroll>
 __global__ void __launch_bounds__(kRowThreads) fp8_rows_kernel(const Fp8RowsParams p) {
   grid_dep_launch_dependents();
-  const int t = blockIdx.x * (kRowThreads / 16) + (threadIdx.x >> 4);
-  const int kb0 = blockIdx.y * kUnroll, c0 = kb0 * kFp8Block + (threadIdx.x & 15) * 8;
+  const int t = blockIdx.y * (kRowThreads / 16) + (threadIdx.x >> 4);
+  const int kb0 = blockIdx.x * kUnroll, c0 = kb0 * kFp8Block + (threadIdx.x & 15) * 8;
   const T* x = static_cast<const T*>(p.x) + (long long)(t < p.T ? t : 0) * p.x_stride;
   uint4 v[kUnroll];
 #pragma unroll
@@ -73,34 +74,32 @@ __global__ void __launch_bounds__(kRowThreads) fp8_rows_kernel(const Fp8RowsPara
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int c = c0 + u * kFp8Block;
-    const bool live = t < p.T && c < p.K;
     float f[8];
     to_floats<T>(v[u], f);
-    emit_block(f, live, p.q + (long long)t * p.q_stride + c, p.scale + (long long)(kb0 + u) * p.T + t);
+    emit_block(f, t < p.T && c < p.K, p.q + (long long)t * p.q_stride + c, p.scale + (long long)(kb0 + u) * p.T + t);
   }
 }
 
 // Norm, a group of kLanes threads (a warp or the CTA) per row; the first
 // kKeep vectors of a thread stay in registers.
 template <typename T, int kLanes, int kKeep>
-__global__ void __launch_bounds__(kRowThreads) fp8_norm_rows_kernel(const Fp8RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, kLanes == 32 ? 3 : 4) fp8_norm_rows_kernel(const Fp8RowsParams p) {
   grid_dep_launch_dependents();
+  constexpr int kRows = kRowThreads / kLanes;
   __shared__ float part[kRowThreads / 32];
+  __shared__ float scales[kRows > 1 ? kKeep * kLanes / 16 : 1][kRows];  // (a warp's rows: written together at the end)
   const int i = threadIdx.x % kLanes;
-  const int t = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
+  const int t0 = blockIdx.x * kRows, t = t0 + threadIdx.x / kLanes;
   const bool row = t < p.T;  // (the same for a whole warp)
   const T* x = static_cast<const T*>(p.x) + (long long)(row ? t : 0) * p.x_stride;
   const T* gamma = static_cast<const T*>(p.gamma);
   constexpr int kStep = kLanes * 8;
-  uint4 v[kKeep], g[kKeep];
+  uint4 v[kKeep];
 #pragma unroll
   for (int u = 0; u < kKeep; ++u) {
     const int c = u * kStep + i * 8;
-    v[u] = g[u] = make_uint4(0, 0, 0, 0);
-    if (row && c < p.K) {
-      v[u] = *reinterpret_cast<const uint4*>(x + c);
-      g[u] = __ldg(reinterpret_cast<const uint4*>(gamma + c));
-    }
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (row && c < p.K) v[u] = *reinterpret_cast<const uint4*>(x + c);
   }
   float ss = 0.f;
 #pragma unroll
@@ -126,25 +125,29 @@ __global__ void __launch_bounds__(kRowThreads) fp8_norm_rows_kernel(const Fp8Row
     for (int w = 0; w < kRowThreads / 32; ++w) ss += part[w];
   }
   const float r = 1.0f / sqrtf(ss / (float)p.K + p.eps);
-  auto block = [&](int c, const uint4& xv, const uint4& gv) {
+  auto block = [&](int c, const uint4& xv) {
+    const uint4 gv = row && c < p.K ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
     float f[8], gf[8];
     to_floats<T>(xv, f);
     to_floats<T>(gv, gf);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = f[k] * r * gf[k];
-    emit_block(f, row && c < p.K, p.q + (long long)t * p.q_stride + c, p.scale + (long long)(c / kFp8Block) * p.T + t);
+    emit_block(f, row && c < p.K, p.q + (long long)t * p.q_stride + c,
+               kRows > 1 ? &scales[kRows > 1 ? c / kFp8Block : 0][t - t0] : p.scale + (long long)(c / kFp8Block) * p.T + t);
   };
 #pragma unroll
   for (int u = 0; u < kKeep; ++u)
-    if (u * kStep < p.K) block(u * kStep + i * 8, v[u], g[u]);  // (the same for a whole warp)
+    if (u * kStep < p.K) block(u * kStep + i * 8, v[u]);  // (the same for a whole warp)
   for (int c0 = kKeep * kStep; c0 < p.K; c0 += kStep) {
     const int c = c0 + i * 8;
-    uint4 xv = make_uint4(0, 0, 0, 0), gv = xv;
-    if (row && c < p.K) {
-      xv = *reinterpret_cast<const uint4*>(x + c);
-      gv = __ldg(reinterpret_cast<const uint4*>(gamma + c));
+    block(c, row && c < p.K ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0));
+  }
+  if constexpr (kRows > 1) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < kKeep * kLanes / 16 * kRows; x += kRowThreads) {
+      const int b = x / kRows, r = x % kRows;
+      if (b * kFp8Block < p.K && t0 + r < p.T) p.scale[(long long)b * p.T + t0 + r] = scales[b][r];
     }
-    block(c, xv, gv);
   }
 }
 
@@ -154,11 +157,21 @@ cudaError_t launch(const Fp8RowsParams& p, cudaStream_t stream) {
   if (!p.gamma) {
     const int rows = (p.T + 15) / 16;
     constexpr int kU = 4;
-    fp8_rows_kernel<T, kU><<<dim3(rows, (blocks + kU - 1) / kU), kRowThreads, 0, stream>>>(p);
-  } else if (p.K <= 2048) {
-    fp8_norm_rows_kernel<T, 32, 8><<<(p.T + 7) / 8, kRowThreads, 0, stream>>>(p);
-  } else {
+    fp8_rows_kernel<T, kU><<<dim3((blocks + kU - 1) / kU, rows), kRowThreads, 0, stream>>>(p);
+  } else if (p.K > 2048) {
     fp8_norm_rows_kernel<T, 256, 4><<<p.T, kRowThreads, 0, stream>>>(p);
+  } else if (p.T <= 1024) {  // (a CTA per row: 64 x 1536 2.1 us, 4.0 with a warp; 8192 x 1536 25.5 and 14.2)
+    fp8_norm_rows_kernel<T, 256, 1><<<p.T, kRowThreads, 0, stream>>>(p);
+  } else {
+    const int grid = (p.T + 7) / 8;
+    if (p.K <= 512)
+      fp8_norm_rows_kernel<T, 32, 2><<<grid, kRowThreads, 0, stream>>>(p);
+    else if (p.K <= 1024)
+      fp8_norm_rows_kernel<T, 32, 4><<<grid, kRowThreads, 0, stream>>>(p);
+    else if (p.K <= 1536)
+      fp8_norm_rows_kernel<T, 32, 6><<<grid, kRowThreads, 0, stream>>>(p);
+    else
+      fp8_norm_rows_kernel<T, 32, 8><<<grid, kRowThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

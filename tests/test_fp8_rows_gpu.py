@@ -97,6 +97,11 @@ def test_norm_rows(T, K, dtype):
     assert ((q.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T,K", [(1025, 512), (1500, 976), (1030, 1536), (1025, 2048), (2000, 16)])
+def test_norm_many_rows(T, K):
+    test_norm_rows(T, K, "bf16")
+
+
 def test_many_rows_and_another_stream():
     x = torch.randn(20000, 384, generator=gen(1), device="cuda").to(torch.bfloat16)
     _, q, s = outputs(20000, 384)
