@@ -585,8 +585,8 @@ typedef struct mla_attn_paged_kv_args {
  * are rounded to fp16, the scaled queries enter with 22 bits); results do not
  * depend on timing.  A block index outside [0, num_blocks) reads as zeros
  * and is reported (MLA_ERR_BAD_SLOT); lengths and offsets out of range are
- * clamped and reported (MLA_ERR_BAD_LENGTH).  Two launches.  Made for few
- * query rows per KV head (n * H / KH up to 16; more rows read the cache once
+ * clamped and reported (MLA_ERR_BAD_LENGTH); lengths, offsets and tables must
+ * not change while a call runs.  One launch, or two.  Made for few query rows per KV head (n * H / KH up to 16; more rows read the cache once
  * for each 16 of them, 8 with int8).  Errors: MLA_ERR_INVALID_ARG (also T %
  * num_seqs != 0 without cu_q, bad strides, some of the scales only),
  * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */

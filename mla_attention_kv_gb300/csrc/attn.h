@@ -105,6 +105,7 @@ cudaError_t paged_combine_launch(bool bf16, const PagedParams& p, int rows, cuda
 // ---------------------------------------------------------------- paged K/V attention
 struct PagedKvParams {
   PagedParams plan;  // sequences, lengths, table, workspace, out and lse; heads: query heads per KV head
+  unsigned* arrived;  // [workers] pieces of the item that a worker began, 0 between calls
   const void* q_nope;
   const void* q_pe;
   const void* k;  // [block, KV head, row, 128] by strides (elements)
@@ -117,7 +118,14 @@ struct PagedKvParams {
   int k_rs, v_rs, kpe_rs;
   int qn_ts, qn_hs, qp_ts, qp_hs;
   int kv_heads;
+  int join_here;  // pieces of an item are joined by the worker that finishes last, else by a second kernel
 };
+// Query rows per KV head and sequence (with ragged chunks the average, which
+// is all the host knows).
+inline long long paged_kv_rows(const PagedKvParams& p) {
+  return (long long)(p.plan.T / p.plan.nseq > 0 ? p.plan.T / p.plan.nseq : 1) * p.plan.heads;
+}
+inline bool paged_kv_joins_here(long long rows) { return rows <= 2; }
 constexpr int kKvWarps = 8;                 // workers per CTA
 constexpr int kKvRows = 16, kKvRowsT = 8;   // query rows of an item, and in the kernel for few rows
 inline int paged_kv_workers(int num_sms) { return num_sms * kKvWarps; }

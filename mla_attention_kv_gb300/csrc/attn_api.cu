@@ -26,6 +26,7 @@ struct mla_attn_s {
   float* part_o;
   float* part_ml;
   PagedJoin* joins;
+  unsigned* arrived;
   PagedMaps paged_maps;
   PromptMaps prompt_maps;
 };
@@ -64,21 +65,22 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
     delete h;
     return fail(e, "device query");
   }
-  // workspace: [status, 256 bytes] | a join record per worker | two partial results per worker (512 columns wide for the
+  // workspace: [status, 256 bytes] | a join record and a counter per worker | two partial results per worker (512 columns wide for the
   // latent cache, 128 for the K/V caches, whose workers are more)
   const size_t rows_mma = (size_t)h->num_sms * 2 * kPagedMmaRows, rows_tc = (size_t)(h->num_sms / 2) * 2 * kPagedPairRows;
   const size_t rows_lat = rows_mma > rows_tc ? rows_mma : rows_tc, rows_kv = (size_t)paged_kv_workers(h->num_sms) * 2 * kKvRows;
   const size_t rows = rows_lat > rows_kv ? rows_lat : rows_kv;
   const size_t values = rows_lat * kRank > rows_kv * kV ? rows_lat * kRank : rows_kv * kV;
   const size_t workers = (size_t)(paged_kv_workers(h->num_sms) > h->num_sms * 2 ? paged_kv_workers(h->num_sms) : h->num_sms * 2);
-  const size_t join_off = 256, ml_off = join_off + ((workers * sizeof(PagedJoin) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+  const size_t join_off = 256, count_off = join_off + ((workers * sizeof(PagedJoin) + 255) & ~(size_t)255);
+  const size_t ml_off = count_off + ((workers * sizeof(unsigned) + 255) & ~(size_t)255), o_off = ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
   e = cudaMalloc(&h->ws, o_off + values * sizeof(float));
   if (e != cudaSuccess) {
     delete h;
     fail(e, "cudaMalloc workspace");
     return MLA_ERR_NO_MEMORY;
   }
-  e = cudaMemset(h->ws, 0, ml_off);  // (status and records)
+  e = cudaMemset(h->ws, 0, ml_off);  // (status, records and counters)
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // a first call may come on a stream that does not wait for this one
   if (e != cudaSuccess) {
     cudaFree(h->ws);
@@ -88,6 +90,7 @@ mla_status mla_attn_create(const mla_attn_config* cfg, mla_attn** out) {
   unsigned char* base = static_cast<unsigned char*>(h->ws);
   h->status = reinterpret_cast<unsigned*>(base);
   h->joins = reinterpret_cast<PagedJoin*>(base + join_off);
+  h->arrived = reinterpret_cast<unsigned*>(base + count_off);
   h->part_ml = reinterpret_cast<float*>(base + ml_off);
   h->part_o = reinterpret_cast<float*>(base + o_off);
   // (shared memory beyond the default is asked for once, not per call)
@@ -252,14 +255,14 @@ mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args
   s.part_ml = h->part_ml; s.joins = h->joins; s.status = h->status; s.table_stride = a.table_stride; s.page = a.page_size;
   s.nblocks = a.num_blocks; s.nseq = a.num_seqs; s.T = a.T; s.heads = H / KH; s.n_uniform = a.cu_q ? 0 : a.T / a.num_seqs;
   s.scale_log2 = h->scale_log2;
-  p.q_nope = a.q_nope; p.q_pe = a.q_pe; p.k = a.k_cache; p.v = a.v_cache; p.kpe = a.kpe_cache; p.k_scale = a.k_scale;
+  p.arrived = h->arrived; p.q_nope = a.q_nope; p.q_pe = a.q_pe; p.k = a.k_cache; p.v = a.v_cache; p.kpe = a.kpe_cache; p.k_scale = a.k_scale;
   p.v_scale = a.v_scale; p.kpe_scale = a.kpe_scale; p.k_bs = a.k_block_stride; p.k_hs = a.k_head_stride;
   p.v_bs = a.v_block_stride; p.v_hs = a.v_head_stride; p.kpe_bs = a.kpe_block_stride; p.k_rs = a.k_row_stride;
   p.v_rs = a.v_row_stride; p.kpe_rs = a.kpe_row_stride; p.qn_ts = a.q_nope_token_stride; p.qn_hs = a.q_nope_head_stride;
   p.qp_ts = a.q_pe_token_stride; p.qp_hs = a.q_pe_head_stride; p.kv_heads = KH;
   cudaError_t e = paged_kv_launch(h->cfg.dtype == MLA_BF16, i8, p, h->num_sms, stream);
   if (e != cudaSuccess) return fail(e, "paged K/V attention launch");
-  h->last_launches = 2;
+  h->last_launches = paged_kv_joins_here(paged_kv_rows(p)) ? 1 : 2;
   return MLA_OK;
 }
 

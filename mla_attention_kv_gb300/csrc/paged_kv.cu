@@ -1,6 +1,6 @@
 // paged_kv.cu -- attention of new tokens over the paged k_nope / value / k_pe
 // caches that the prolog writes, in 16 bits or as int8 codes with a scale per
-// channel; and the kernel that joins partial results.
+// channel; and the kernel that joins partial results of many rows.
 //
 // Per query row r (a token and a head; q = [q_nope | q_pe], 192 wide) of KV
 // head h and cached token j:
@@ -17,7 +17,12 @@
 // own: the kernel is bound by the cache's bytes.  So each warp is a worker
 // with its own share of the keys, its own ring of stages filled by 16-byte
 // cp.async (any page size; a page may end anywhere in a stage) and its own
-// running softmax: nothing in the loop waits for another warp.  The products
+// running softmax: nothing in the loop waits for another warp.  Pieces of
+// an item that several workers share are joined in their order.  Few rows: by
+// the worker that finishes last (its being last changes nothing in the result).
+// More: by a second kernel, which spreads them over the GPU.  64 sequences of
+// up to 4096 keys, 16 heads, one row each: 177 us, 182 with the second kernel;
+// 12 rows per head in 20 pieces: 45 us with it, 69 without; 4 rows 37 and 42.  The products
 // run on mma.sync, in one of two forms:
 //   up to 8 rows: S^T = K Q^T and O^T = V^T P^T, keys and value columns being
 //     the 16 rows of an operand and the query rows its 8 columns.  P^T turns
@@ -42,6 +47,7 @@ namespace mla {
 namespace {
 
 constexpr int kStages = 2;
+constexpr int kJoinFlight = 16;  // pieces in flight when they are joined
 constexpr int kStageBytes = 10240;  // keys 4 KB, rotated parts 2 KB, values 4 KB
 constexpr int kPeOff = 4096, kVOff = 6144;
 constexpr int kWarpBytes = kStages * kStageBytes;
@@ -100,11 +106,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
   const uint32_t ring = smem_u32(smem) + warp * kWarpBytes;
   const int G = p.plan.heads, H = G * p.kv_heads;
 
-  grid_dep_launch_dependents();  // (the joining kernel may take its place)
+  grid_dep_launch_dependents();  // (a joining kernel may take its place)
   const long long total = kv_total(p, plan, R, blockIdx.x == 0);
   const int W = total > 0 ? kv_workers(total, p.plan.workers) : 0;
   const int w = warp * gridDim.x + blockIdx.x;  // (few workers: spread over the SMs)
-  if (lane == 0) plan_open_join(p.plan, w);
+  if (!p.join_here && lane == 0) plan_open_join(p.plan, w);
   if (w >= W) return;
   const long long x0 = plan_worker_begin(total, w, W), x1 = plan_worker_begin(total, w + 1, W);
 
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
     constexpr int kSub = kKvTile / S::Keys;
     const int t0 = c.tile_at(a, tiles) * kSub, t1 = min(c.tile_at(b, tiles) * kSub, (keys + S::Keys - 1) / S::Keys);
     const bool whole = c.lo >= x0 && c.hi <= x1;
-    if (lane == 0 && c.hi >= x1) kv_post_join(p, c, R, w, x0, x1, total, W);
+    if (!p.join_here && lane == 0 && c.hi >= x1) kv_post_join(p, c, R, w, x0, x1, total, W);
 
     // ---- stages.  A place is looked up two stages ahead of its use.
     constexpr int kParts = kWhole ? S::Keys / 16 : 1;  // of a stage that lie in one page each
@@ -468,28 +474,87 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       }
     }
     __syncwarp();
-    const size_t slot = (size_t)w * 2 + (c.lo < x0 ? 0 : 1);
     float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
     if (kI8) vs = reinterpret_cast<const float4*>(p.v_scale + c.head * kV)[lane];
+    auto store = [&](int r, float4 y, float m, float l) {  // row r's result, four columns a lane
+      const int tok = (row0 + r) / G;
+      const size_t orow = (size_t)(sq.begin + tok) * H + c.head * G + (row0 + r) - tok * G;
+      const float iv = l == 0.f ? 0.f : 1.f / l;
+      reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
+          make_uint2(E::pack(y.x * iv * vs.x, y.y * iv * vs.y), E::pack(y.z * iv * vs.z, y.w * iv * vs.w));
+      if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    };
+    // (slot of worker v: its first place for an item that others began, its second for one that it begins)
+    auto part = [&](int v, bool begins) { return (size_t)v * 2 + (begins ? 1 : 0); };
+    float4* part_o = reinterpret_cast<float4*>(p.plan.part_o);
+    float2* part_ml = reinterpret_cast<float2*>(p.plan.part_ml);
     for (int r = 0; r < live; ++r) {
       // (lane r / 2 holds row r in its first or second place, or lanes 4 r and 4 (r - 8))
       const int from = kT ? r >> 1 : (r & 7) * 4;
       const bool sec = kT ? r & 1 : r >= 8;
       const float l = __shfl_sync(~0u, sec ? l1 : l0, from), m = __shfl_sync(~0u, sec ? m1 : m0, from);
-      const int tok = (row0 + r) / G;
-      const size_t orow = (size_t)(sq.begin + tok) * H + c.head * G + (row0 + r) - tok * G;
-      float4 y = reinterpret_cast<const float4*>(place + r * kV)[lane];
-      const float iv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      y = make_float4(y.x * iv * vs.x, y.y * iv * vs.y, y.z * iv * vs.z, y.w * iv * vs.w);
+      const float4 y = reinterpret_cast<const float4*>(place + r * kV)[lane];
       if (whole) {
-        reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] = make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));
-        if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        store(r, y, m, l);
       } else {
-        reinterpret_cast<float4*>(p.plan.part_o + (slot * R + r) * kV)[lane] = y;
-        if (lane == 0) reinterpret_cast<float2*>(p.plan.part_ml)[slot * R + r] = make_float2(m, l);
+        const size_t at = part(w, c.lo >= x0) * R + r;
+        part_o[at * (kV / 4) + lane] = y;
+        if (lane == 0) part_ml[at] = make_float2(m, l);
       }
     }
     __syncwarp();  // (the ring is filled again by the next item)
+    if (whole || !p.join_here) continue;
+    // ---- the last piece to arrive joins them all: with weights u_i = 2^(m_i - m),
+    //   l = sum u_i l_i,  out = sum u_i o_i / l
+    int w1, w2;
+    kv_sharers(c, w, x0, x1, total, W, &w1, &w2);
+    __threadfence();
+    __syncwarp();
+    unsigned before = 0;
+    if (lane == 0) before = atomicInc(p.arrived + w1, w2 - w1);  // (0 again after the last)
+    if (__shfl_sync(~0u, before, 0) != (unsigned)(w2 - w1)) continue;
+    __threadfence();
+    const int n = w2 - w1 + 1;
+    for (int r = 0; r < live; ++r) {
+      auto piece = [&](int i) { return part(w1 + i, i == 0) * R + r; };
+      // (all loads of a group are made, those past the end of the last piece, and before the weights are there)
+      float4 y[kJoinFlight];
+      auto request = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < kJoinFlight; ++k) y[k] = __ldcg(part_o + piece(min(j0 + k, n - 1)) * (kV / 4) + lane);
+      };
+      request(0);
+      auto ml = [&](int i) { return i < n ? __ldcg(part_ml + piece(i)) : make_float2(-INFINITY, 0.f); };
+      const float2 a0 = ml(lane);
+      float m = a0.x;
+      for (int i = 32 + lane; i < n; i += 32) m = fmaxf(m, ml(i).x);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      const float mu = m == -INFINITY ? 0.f : m;
+      float l = 0.f, f = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j0 = 0; j0 < n; j0 += kJoinFlight) {
+        if (j0 % 32 == 0) {
+          const float2 a = j0 == 0 ? a0 : ml(j0 + lane);
+          f = ex2(a.x - mu);
+          l += f * a.y;
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinFlight; ++k) {
+          const float u = __shfl_sync(~0u, f, (j0 + k) & 31);
+          if (j0 + k < n) {
+            o.x += u * y[k].x;
+            o.y += u * y[k].y;
+            o.z += u * y[k].z;
+            o.w += u * y[k].w;
+          }
+        }
+        if (j0 + kJoinFlight < n) request(j0 + kJoinFlight);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+      store(r, o, m, l);
+    }
   }
 }
 
@@ -501,7 +566,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
 // time with 16 pieces in flight.  Bound by latency, so the grid is what fits
 // on the GPU at once: with a block for each eight possible rows 12 sequences
 // with 12 rows per head took 47 us instead of 39.
-constexpr int kJoinFlight = 16;
 template <typename T>
 __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constant__ PagedKvParams p, int per, int R) {
   using E = Elem<T>;
@@ -565,31 +629,27 @@ __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constan
 #pragma unroll
       for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
       const float iv = l == 0.f ? 0.f : 1.f / l;
+      const float4 vs = p.v_scale ? reinterpret_cast<const float4*>(p.v_scale + j.pad * kV)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
       reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
-          make_uint2(E::pack(o.x * iv, o.y * iv), E::pack(o.z * iv, o.w * iv));
+          make_uint2(E::pack(o.x * iv * vs.x, o.y * iv * vs.y), E::pack(o.z * iv * vs.z, o.w * iv * vs.w));
       if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
    }
   }
 }
 
-// Query rows per KV head and sequence (with ragged chunks the average, which
-// is all the host knows).
-long long kv_rows(const PagedKvParams& p) {
-  return (long long)(p.plan.T / p.plan.nseq > 0 ? p.plan.T / p.plan.nseq : 1) * p.plan.heads;
-}
-
 template <typename T, bool kI8, bool kT>
 cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
   using S = KvCfg<kI8, kT>;
   p.plan.workers = paged_kv_workers(num_sms);
+  const long long rows = paged_kv_rows(p);
+  p.join_here = paged_kv_joins_here(rows);
   if (p.plan.page % 16 == 0)
     paged_kv_kernel<T, kI8, kT, true><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   else
     paged_kv_kernel<T, kI8, kT, false><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const long long rows = kv_rows(p);
+  if (e != cudaSuccess || p.join_here) return e;
   const int per = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 || S::R == 8 ? 8 : 16;
   const int blocks = (p.plan.workers * per + 15) / 8, most = num_sms * 2;
   cudaLaunchConfig_t c = {};
@@ -619,7 +679,7 @@ cudaError_t prepare() {
 template <typename T>
 cudaError_t launch_any(bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream) {
   if (i8) return launch<T, true, true>(p, num_sms, stream);
-  return kv_rows(p) <= kKvRowsT ? launch<T, false, true>(p, num_sms, stream) : launch<T, false, false>(p, num_sms, stream);
+  return paged_kv_rows(p) <= kKvRowsT ? launch<T, false, true>(p, num_sms, stream) : launch<T, false, false>(p, num_sms, stream);
 }
 
 }  // namespace

@@ -60,7 +60,7 @@ __device__ __forceinline__ long long kv_total(const PagedKvParams& p, PlanShared
 }
 
 // Workers that take part, at least kKvMinRange of cost each.
-constexpr int kKvMinRange = 2;
+constexpr int kKvMinRange = 1;
 __host__ __device__ __forceinline__ int kv_workers(long long total, int W) {
   const long long w = total / kKvMinRange;
   return w < 1 ? 1 : (w < W ? (int)w : W);
@@ -151,6 +151,14 @@ __host__ __device__ __forceinline__ void kv_post_join(const PagedKvParams& p, co
     j.pad = c.head;
   }
   p.plan.joins[w] = j;
+}
+
+// The workers that an item is split over, seen from worker w with the range
+// [x0, x1): the first and the last.
+__host__ __device__ __forceinline__ void kv_sharers(const KvCursor& c, int w, long long x0, long long x1, long long total, int W,
+                                                    int* first, int* last) {
+  *first = c.lo >= x0 ? w : plan_worker_of(c.lo, total, W);
+  *last = c.hi <= x1 ? w : plan_worker_of(c.hi - 1, total, W);
 }
 
 }  // namespace mla

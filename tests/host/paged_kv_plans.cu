@@ -1,7 +1,8 @@
 // paged_kv_plans.cu -- host check of the paged K/V attention's work split
 // (paged_kv_plan.cuh): the workers' pieces cover every key tile of every item
 // (sequence, KV head, row block) once, partial results have a slot of their
-// own, and the records of the joining kernel fit the pieces.
+// own, all workers of an item agree on the first and the last of them, and the
+// records of the joining kernel fit the pieces.
 #include <cstdio>
 #include <cstdlib>
 #include <map>
@@ -22,7 +23,7 @@ static int failed = 0, checks = 0;
     }                                                                          \
   } while (0)
 
-struct Piece { int t0, t1, worker, slot; bool whole; };
+struct Piece { int t0, t1, worker, slot; bool whole; int first, last; };
 using Key = std::tuple<int, int, int>;
 
 static void run(const std::vector<int>& n, const std::vector<int>& L, int G, int KH, int R, int W, int nt, int lead, bool uniform) {
@@ -70,12 +71,13 @@ static void run(const std::vector<int>& n, const std::vector<int>& L, int G, int
         CHECK(c.s >= 0 && c.s < p.plan.nseq && c.head >= 0 && c.head < KH && c.j >= 0 && c.j < c.q.items && c.hi > c.lo);
         const int keys = c.q.keys_of_item(c.j, R, G), tiles = (keys + kKvTile - 1) / kKvTile;
         const long long a = x0 > c.lo ? x0 : c.lo, b = x1 < c.hi ? x1 : c.hi;
-        Piece pc = {c.tile_at(a, tiles), c.tile_at(b, tiles), w, -1, c.lo >= x0 && c.hi <= x1};
+        Piece pc = {c.tile_at(a, tiles), c.tile_at(b, tiles), w, -1, c.lo >= x0 && c.hi <= x1, -1, -1};
         CHECK(pc.t0 >= 0 && pc.t0 <= pc.t1 && pc.t1 <= tiles);
         if (!pc.whole) {
           pc.slot = w * 2 + (c.lo < x0 ? 0 : 1);
           CHECK(++slots[pc.slot] == 1);
         }
+        kv_sharers(c, w, x0, x1, total, We, &pc.first, &pc.last);
         got[Key(c.s, c.head, c.j)].push_back(pc);
         if (c.hi >= x1) {
           kv_post_join(p, c, R, w, x0, x1, total, We);
@@ -88,12 +90,14 @@ static void run(const std::vector<int>& n, const std::vector<int>& L, int G, int
       }
       CHECK(joins[w].rows >= 0);
     }
+    std::map<int, int> begun;  // split items that a worker begins
     for (auto& kv : got) {
       const auto& v = kv.second;
       CHECK((v.size() > 1) == (joined.count(kv.first) == 1));
-      if (v.size() > 1) {
-        CHECK(joins[v[0].worker].last_worker - v[0].worker + 1 == (int)v.size());
-        for (size_t i = 0; i < v.size(); ++i) CHECK(v[i].worker == v[0].worker + (int)i && v[i].slot == v[i].worker * 2 + (i == 0 ? 1 : 0));
+      if (v.size() > 1) CHECK(++begun[v[0].worker] == 1 && joins[v[0].worker].last_worker == v.back().worker);
+      for (size_t i = 0; i < v.size(); ++i) {
+        CHECK(v[i].first == v[0].worker && v[i].last == v.back().worker && v[i].worker == v[0].worker + (int)i);
+        if (v.size() > 1) CHECK(v[i].slot == v[i].worker * 2 + (i == 0 ? 1 : 0));
       }
     }
   }

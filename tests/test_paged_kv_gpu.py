@@ -129,7 +129,7 @@ def run_case(*args, cu=True, kv_heads=None, **kw):
     c = Case(*args, **kw)
     a = B.MLAAttention(config(c.H, "fp16" if c.dt is torch.float16 else "bf16"), max(1, c.T), num_kv_heads=c.KH)
     c.run(a, cu=cu)
-    assert a.status() == 0 and a.last_launches == 2
+    assert a.status() == 0 and a.last_launches == (1 if c.T // len(c.n) * (c.H // c.KH) <= 2 else 2)
     c.check()
     a.close()
     return c
