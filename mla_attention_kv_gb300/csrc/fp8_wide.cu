@@ -7,13 +7,16 @@
 // warps take them from there, scale them and add them to fp32 registers while
 // the next block's MMAs run.  A block of a tile is two MMA groups of 128
 // weight rows (one weight scale each, 256 cycles); tensor memory holds four
-// such results.  Eight epilogue warps: a thread holds one token row and 64
-// columns of either weight block, 128 registers of sums.
+// such results.  Sixteen epilogue warps: a thread holds one token row and 64
+// columns of one weight block.  With eight, which hold twice as much, the way
+// of a warp through a block (wait, load, scale, release) is the bound: 1024 x
+// 16384 -> 7168 takes 152 us instead of 123.
 //
-// What bounds it is the way of a result: MMA, commit, wait, load from tensor
-// memory, release, wait, next MMA.  That is why the CTAs do not pair up for
-// the 2-SM MMA, which would halve the weight traffic but sends commits and
-// releases across the pair, about 1000 cycles each way.
+// 8192 x 1536 -> 24576: 241 us (2560 TFLOP/s); without the epilogue, loads and
+// MMAs alone take 231 on a ring of three stages (209 on four, whose room the
+// results' staging takes).  The CTAs do not pair up for the 2-SM MMA, which
+// halves the weight traffic (loads and MMAs alone 151 us) but sends commits
+// and releases across the pair, about 1000 cycles a way: 296 us.
 //
 // Warps: 0 TMA, 1 tensor memory, 1 and 2 MMA, 4-19 epilogue (3 only gives its
 // registers).

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
   const uint32_t ring = smem_u32(smem) + warp * kWarpBytes;
   const int G = p.plan.heads, H = G * p.kv_heads;
 
-  grid_dep_launch_dependents();  // (a joining kernel may take its place)
+  if (!p.join_here) grid_dep_launch_dependents();  // (the joining kernel may take its place)
   const long long total = kv_total(p, plan, R, blockIdx.x == 0);
   const int W = total > 0 ? kv_workers(total, p.plan.workers) : 0;
   const int w = warp * gridDim.x + blockIdx.x;  // (few workers: spread over the SMs)
