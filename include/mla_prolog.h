@@ -586,9 +586,10 @@ typedef struct mla_attn_paged_kv_args {
  * depend on timing.  A block index outside [0, num_blocks) reads as zeros
  * and is reported (MLA_ERR_BAD_SLOT); lengths and offsets out of range are
  * clamped and reported (MLA_ERR_BAD_LENGTH); lengths, offsets and tables must
- * not change while a call runs.  One launch, or two.  Made for few query rows per KV head (n * H / KH up to 16; more rows read the cache once
- * for each 16 of them, 8 with int8).  Errors: MLA_ERR_INVALID_ARG (also T %
- * num_seqs != 0 without cu_q, bad strides, some of the scales only),
+ * not change while a call runs.  One launch, or two.  Made for few query rows
+ * per KV head (n * H / KH up to 16; more rows read the cache once for each 16
+ * of them, 8 with int8).  Errors: MLA_ERR_INVALID_ARG (also T % num_seqs != 0
+ * without cu_q, num_seqs > 2^30, bad strides, some of the scales only),
  * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args, cudaStream_t stream);
 
@@ -637,10 +638,10 @@ typedef struct mla_page_plan_args {
  * range are clamped, and pages past the stack's end dropped
  * (MLA_ERR_BAD_LENGTH); a row whose block is not in [0, num_blocks) gets
  * slot -1 (MLA_ERR_BAD_SLOT).  T may be smaller than max_tokens; of the
- * handle only its status word is used.  One launch.  Other than as stated the arrays
- * must not overlap.  Errors: MLA_ERR_INVALID_ARG (also num_blocks *
- * page_size > INT_MAX, num_seqs > 2^30), MLA_ERR_TOO_MANY_TOKENS,
- * MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+ * handle only its status word is used.  One launch.  Other than as stated the
+ * arrays must not overlap.  Errors: MLA_ERR_INVALID_ARG (also num_blocks *
+ * page_size > INT_MAX, num_seqs > 2^30, T or num_blocks > 2^31 - 65536),
+ * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
@@ -668,12 +669,12 @@ typedef struct mla_fp8_quant_args {
  * a NaN code and does not enter its block's scale; an infinity makes the
  * scale infinite).  Runs on the current device, one launch.  Errors:
  * MLA_ERR_INVALID_ARG (also bad strides), MLA_ERR_UNSUPPORTED (K not a
- * multiple of 16), MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
+ * multiple of 16; T or K > 2^31 - 65536), MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_fp8_quant_rows(const mla_fp8_quant_args* args, cudaStream_t stream);
 
 typedef struct mla_fp8_linear_config {
   int in_features;  /* K, multiple of 16                               */
-  int out_features; /* N, multiple of 8                                */
+  int out_features; /* N, multiple of 8, at most 65535 * 128           */
   int dtype;        /* mla_dtype of x, gamma and out                   */
   int max_tokens;   /* largest T of any run (sizes the workspace)      */
   unsigned long long spin_budget_ns; /* device wait limit; 0 selects 1 s */
@@ -688,8 +689,8 @@ typedef struct mla_fp8_linear_s mla_fp8_linear;
  * workspace of quantised rows and a status word.  One handle serves one
  * stream at a time, and one host thread (runs given codes use only its
  * status word and may overlap on the device).  Errors:
- * MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (K or N), MLA_ERR_MISALIGNED,
- * MLA_ERR_NO_MEMORY, MLA_ERR_CUDA. */
+ * MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (K or N; K or max_tokens > 2^31 -
+ * 65536), MLA_ERR_MISALIGNED, MLA_ERR_NO_MEMORY, MLA_ERR_CUDA. */
 mla_status mla_fp8_linear_create(const mla_fp8_linear_config* cfg, const void* weight,
                                  const float* weight_scale, mla_fp8_linear** out);
 mla_status mla_fp8_linear_destroy(mla_fp8_linear* h);

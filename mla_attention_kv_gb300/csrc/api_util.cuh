@@ -19,6 +19,10 @@ mla_status fail(cudaError_t e, const char* what) {
   return MLA_ERR_CUDA;
 }
 
+// Most rows, columns or blocks: from here on the kernels' sums of a count and a
+// step could leave 32 bits.
+constexpr int kMostCount = 0x7fff0000;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Reads and clears the status word in one step (the second word keeps what was

@@ -222,7 +222,7 @@ mla_status mla_attn_paged_run(mla_attn* h, const mla_attn_paged_args* args, cuda
 mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args, cudaStream_t stream) {
   if (!h || !args) return MLA_ERR_INVALID_ARG;
   const mla_attn_paged_kv_args& a = *args;
-  if (a.num_seqs < 0 || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
+  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
       (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
     return MLA_ERR_INVALID_ARG;
   h->last_launches = 0;
@@ -309,8 +309,8 @@ mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cu
 mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream) {
   if (!h || !args) return MLA_ERR_INVALID_ARG;
   const mla_page_plan_args& a = *args;
-  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.page_size <= 0 || a.num_blocks <= 0 || a.table_stride < 0 ||
-      (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
+  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.T > kMostCount || a.page_size <= 0 || a.num_blocks <= 0 ||
+      a.num_blocks > kMostCount || a.table_stride < 0 || (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
     return MLA_ERR_INVALID_ARG;
   h->last_launches = 0;
   if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;

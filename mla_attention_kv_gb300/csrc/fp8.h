@@ -33,27 +33,12 @@ struct Fp8LinearParams {
   int dependent;  // launched while the kernel that makes the rows runs
   unsigned long long budget_ns;
 };
-// Tensor maps of the weight (boxes of 128 rows), and of the last call's rows and results.
-struct Fp8Maps {
-  CUtensorMap w;
-  struct Key {
-    const void* x;
-    int T, stride, box;
-  } key;
-  bool valid;
-  CUtensorMap x;
-  struct OutKey {
-    const void* out;
-    int T, stride;
-  } out_key;
-  bool out_valid;
-  CUtensorMap out;
-};
 // Few rows: weights as the 128-row operand, the K blocks split over a cluster.
 // `cost` (where not null) gets what the kernel would take, in K blocks of time.
 int fp8_narrow_split(const Fp8LinearParams& p, int num_sms, int* cost);
 cudaError_t fp8_narrow_prepare();
-cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+// w: the weight's tensor map, in boxes of 128 rows.
+cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                               cudaStream_t stream);
 // Many rows: persistent CTAs on tiles of 128 rows x 256 weight rows.
 inline int fp8_wide_cost(const Fp8LinearParams& p, int num_sms) {
@@ -62,9 +47,9 @@ inline int fp8_wide_cost(const Fp8LinearParams& p, int num_sms) {
   return c < 0x7fffffff ? (int)c : 0x7fffffff;
 }
 cudaError_t fp8_wide_prepare();
-cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                             cudaStream_t stream);
-// The map of rows xq [T, K] with boxes of `box` rows, made anew if it is another than the last one.
-bool fp8_row_map(Fp8Maps* maps, const void* xq, int T, int K, int stride, int box);
+// The map of rows xq [T, K] with boxes of `box` rows.
+bool fp8_row_map(CUtensorMap* map, const void* xq, int T, int K, int stride, int box);
 
 }  // namespace mla

@@ -24,7 +24,7 @@ struct mla_fp8_linear_s {
   uint8_t* xq;    // [max_tokens, K]
   float* xscale;  // [blocks of K, max_tokens]
   const float* w_scale;
-  Fp8Maps maps;
+  CUtensorMap w;
 };
 
 namespace {
@@ -41,7 +41,7 @@ mla_status mla_fp8_quant_rows(const mla_fp8_quant_args* args, cudaStream_t strea
   if (!args) return MLA_ERR_INVALID_ARG;
   const mla_fp8_quant_args& a = *args;
   if (a.T < 0 || a.K <= 0 || (a.dtype != MLA_F16 && a.dtype != MLA_BF16) || !(a.eps >= 0.0f)) return MLA_ERR_INVALID_ARG;
-  if (a.K % 16 != 0) return MLA_ERR_UNSUPPORTED;
+  if (a.K % 16 != 0 || a.K > kMostCount || a.T > kMostCount) return MLA_ERR_UNSUPPORTED;
   if (a.T == 0) return MLA_OK;
   if (!a.x || !a.q || !a.scale) return MLA_ERR_INVALID_ARG;
   if (!stride_ok(a.x_stride, a.K, 8, a.T) || !stride_ok(a.q_stride, a.K, 16, a.T)) return MLA_ERR_INVALID_ARG;
@@ -62,7 +62,10 @@ mla_status mla_fp8_linear_create(const mla_fp8_linear_config* cfg, const void* w
   if (c.in_features <= 0 || c.out_features <= 0 || c.max_tokens <= 0 || (c.dtype != MLA_F16 && c.dtype != MLA_BF16) || !weight ||
       !weight_scale)
     return MLA_ERR_INVALID_ARG;
-  if (c.in_features % 16 != 0 || c.out_features % 8 != 0) return MLA_ERR_UNSUPPORTED;
+  // (a grid has 65535 CTAs along the weight's 128-row tiles)
+  if (c.in_features % 16 != 0 || c.in_features > kMostCount || c.out_features % 8 != 0 || c.out_features > 65535 * kFp8Block ||
+      c.max_tokens > kMostCount)
+    return MLA_ERR_UNSUPPORTED;
   if (!aligned16(weight) || !aligned16(weight_scale)) return MLA_ERR_MISALIGNED;
   mla_fp8_linear_s* h = new (std::nothrow) mla_fp8_linear_s();
   if (!h) return MLA_ERR_NO_MEMORY;
@@ -76,7 +79,7 @@ mla_status mla_fp8_linear_create(const mla_fp8_linear_config* cfg, const void* w
     delete h;
     return fail(e, "device query");
   }
-  if (!encode_tmap_2d(&h->maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, weight, (uint64_t)c.in_features, (uint64_t)c.out_features,
+  if (!encode_tmap_2d(&h->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, weight, (uint64_t)c.in_features, (uint64_t)c.out_features,
                       (uint64_t)c.in_features, kFp8Block, kFp8Block, CU_TENSOR_MAP_SWIZZLE_128B)) {
     delete h;
     return fail(cudaErrorInvalidValue, "weight tensor map");
@@ -166,8 +169,8 @@ mla_status mla_fp8_linear_run(mla_fp8_linear* h, const mla_fp8_linear_args* args
   p.out_stride = a.T > 1 ? a.out_stride : N; p.budget_ns = h->budget_ns;
   int narrow_cost = 0;
   fp8_narrow_split(p, h->num_sms, &narrow_cost);
-  e = narrow_cost <= fp8_wide_cost(p, h->num_sms) ? fp8_narrow_launch(bf16, p, xq, xq_stride, &h->maps, h->num_sms, stream)
-                                                  : fp8_wide_launch(bf16, p, xq, xq_stride, &h->maps, h->num_sms, stream);
+  e = narrow_cost <= fp8_wide_cost(p, h->num_sms) ? fp8_narrow_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream)
+                                                  : fp8_wide_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream);
   if (e != cudaSuccess) return fail(e, "fp8 linear launch");
   ++h->last_launches;
   return MLA_OK;

@@ -15,8 +15,6 @@
 // Warps: 0 TMA, 1 tensor memory and MMA, 2-5 (or 2-9) epilogue.  Behind the row
 // quantisation the kernel is launched early: its first weight tiles are under
 // way while that one still runs.
-#include <string.h>
-
 #include "attn_tc.cuh"
 #include "fp8.h"
 #include "tma.h"
@@ -247,9 +245,10 @@ __global__ void __launch_bounds__(NwCfg<TN>::kThreads, 2) fp8_narrow_kernel(cons
 }
 
 template <typename T, int TN>
-cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms, cudaStream_t stream) {
   NwArgs a;
-  a.w = maps.w; a.x = maps.x; a.p = p;
+  a.w = w; a.p = p;
+  if (!fp8_row_map(&a.x, xq, p.T, p.K, xq_stride, TN)) return cudaErrorInvalidValue;
   const int nt = (p.N + 127) / 128, tt = (p.T + TN - 1) / TN, split = fp8_narrow_split(p, num_sms, nullptr);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(split, nt, tt);
@@ -270,13 +269,11 @@ cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, c
 int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 template <typename T>
-cudaError_t launch_tn(const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms, cudaStream_t stream) {
-  const int tn = tile_tokens(p.T);
-  if (!fp8_row_map(maps, xq, p.T, p.K, xq_stride, tn)) return cudaErrorInvalidValue;
-  switch (tn) {
-    case 16: return launch<T, 16>(p, *maps, num_sms, stream);
-    case 32: return launch<T, 32>(p, *maps, num_sms, stream);
-    default: return launch<T, 64>(p, *maps, num_sms, stream);
+cudaError_t launch_tn(const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms, cudaStream_t stream) {
+  switch (tile_tokens(p.T)) {
+    case 16: return launch<T, 16>(p, w, xq, xq_stride, num_sms, stream);
+    case 32: return launch<T, 32>(p, w, xq, xq_stride, num_sms, stream);
+    default: return launch<T, 64>(p, w, xq, xq_stride, num_sms, stream);
   }
 }
 
@@ -299,9 +296,10 @@ cudaError_t prepare() {
 // sums are larger (64 x 7168 -> 2112: 10.0 us on 4, 11.3 on 8; one row 8.2 on 4,
 // 7.4 on 8).  Cost: the blocks that an SM takes in turn, in units of about 0.15
 // us: one for a block of up to 32 tokens, two for 64, three for a block of the
-// other kernel's tile (1 x 1536 -> 24576: 9.5 us here, 12.6 there, cost 24, 36).  256 x 7168 -> 2112: 14.2 us here, 29.4 there (cost 56, 168);
-// 128 x 1536 -> 24576: 19.6 and 12.4 (72, 36); 256 x 16384 -> 7168: 72 and 63
-// (512, 384); 512 x 2048 -> 576: 7.8 and 10.1 (16, 48).
+// other kernel's tile.  1 x 1536 -> 24576: 9.5 us here, 12.6 there (cost 24 and
+// 36); 256 x 7168 -> 2112: 14.2 and 29.4 (56, 168); 128 x 1536 -> 24576: 19.6
+// and 12.4 (72, 36); 256 x 16384 -> 7168: 72 and 63 (512, 384); 512 x 2048 ->
+// 576: 7.8 and 10.1 (16, 48).
 int fp8_narrow_split(const Fp8LinearParams& p, int num_sms, int* cost) {
   const int tn = tile_tokens(p.T), most = tn == 64 ? 4 : 8;
   const long long blocks = (p.K + kFp8Block - 1) / kFp8Block, tiles = (long long)((p.N + 127) / 128) * ((p.T + tn - 1) / tn);
@@ -314,18 +312,9 @@ int fp8_narrow_split(const Fp8LinearParams& p, int num_sms, int* cost) {
   return split;
 }
 
-bool fp8_row_map(Fp8Maps* maps, const void* xq, int T, int K, int stride, int box) {
-  Fp8Maps::Key key;
-  memset(&key, 0, sizeof(key));
-  key.x = xq; key.T = T; key.stride = stride; key.box = box;
-  if (maps->valid && memcmp(&key, &maps->key, sizeof(key)) == 0) return true;
-  maps->valid = false;
-  if (!encode_tmap_2d(&maps->x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K, (uint64_t)T, (uint64_t)stride, kFp8Block, (uint32_t)box,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
-    return false;
-  maps->key = key;
-  maps->valid = true;
-  return true;
+bool fp8_row_map(CUtensorMap* map, const void* xq, int T, int K, int stride, int box) {
+  return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K, (uint64_t)T, (uint64_t)stride, kFp8Block, (uint32_t)box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 cudaError_t fp8_narrow_prepare() {
@@ -333,10 +322,10 @@ cudaError_t fp8_narrow_prepare() {
   return e == cudaSuccess ? prepare<__nv_bfloat16>() : e;
 }
 
-cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                               cudaStream_t stream) {
-  return bf16 ? launch_tn<__nv_bfloat16>(p, xq, xq_stride, maps, num_sms, stream)
-              : launch_tn<__half>(p, xq, xq_stride, maps, num_sms, stream);
+  return bf16 ? launch_tn<__nv_bfloat16>(p, w, xq, xq_stride, num_sms, stream)
+              : launch_tn<__half>(p, w, xq, xq_stride, num_sms, stream);
 }
 
 }  // namespace mla

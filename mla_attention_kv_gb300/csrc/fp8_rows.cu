@@ -56,14 +56,15 @@ __device__ __forceinline__ void emit_block(const float* f, bool live, uint8_t* q
   if ((threadIdx.x & 15) == 0) *scale = s;
 }
 
-// No norm: half-warp i of a CTA takes row blockIdx.y * 16 + i, kUnroll blocks
-// of columns.  (Neighbouring CTAs take neighbouring columns: 8192 x 7168 30.7
+// No norm: half-warp i of a CTA takes row 16 y + i and kUnroll blocks of
+// columns, CTA = y * across + x.  (Neighbouring CTAs take neighbouring columns: 8192 x 7168 30.7
 // us, 32.4 the other way round; scales gathered in shared memory first 31.5.)
 template <typename T, int kUnroll>
-__global__ void __launch_bounds__(kRowThreads) fp8_rows_kernel(const Fp8RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads) fp8_rows_kernel(const Fp8RowsParams p, unsigned across) {
   grid_dep_launch_dependents();
-  const int t = blockIdx.y * (kRowThreads / 16) + (threadIdx.x >> 4);
-  const int kb0 = blockIdx.x * kUnroll, c0 = kb0 * kFp8Block + (threadIdx.x & 15) * 8;
+  const unsigned y = blockIdx.x / across;
+  const int t = y * (kRowThreads / 16) + (threadIdx.x >> 4);
+  const int kb0 = (blockIdx.x - y * across) * kUnroll, c0 = kb0 * kFp8Block + (threadIdx.x & 15) * 8;
   const T* x = static_cast<const T*>(p.x) + (long long)(t < p.T ? t : 0) * p.x_stride;
   uint4 v[kUnroll];
 #pragma unroll
@@ -155,9 +156,9 @@ template <typename T>
 cudaError_t launch(const Fp8RowsParams& p, cudaStream_t stream) {
   const int blocks = (p.K + kFp8Block - 1) / kFp8Block;
   if (!p.gamma) {
-    const int rows = (p.T + 15) / 16;
     constexpr int kU = 4;
-    fp8_rows_kernel<T, kU><<<dim3((blocks + kU - 1) / kU, rows), kRowThreads, 0, stream>>>(p);
+    const unsigned across = (blocks + kU - 1) / kU;
+    fp8_rows_kernel<T, kU><<<(unsigned)((p.T + 15) / 16) * across, kRowThreads, 0, stream>>>(p, across);
   } else if (p.K > 2048) {
     fp8_norm_rows_kernel<T, 256, 4><<<p.T, kRowThreads, 0, stream>>>(p);
   } else if (p.T <= 1024) {  // (a CTA per row: 64 x 1536 2.1 us, 4.0 with a warp; 8192 x 1536 25.5 and 14.2)

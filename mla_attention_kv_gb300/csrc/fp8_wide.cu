@@ -20,8 +20,6 @@
 //
 // Warps: 0 TMA, 1 tensor memory, 1 and 2 MMA, 4-19 epilogue (3 only gives its
 // registers).
-#include <string.h>
-
 #include "attn_tc.cuh"
 #include "fp8.h"
 #include "tma.h"
@@ -236,9 +234,14 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
 }
 
 template <typename T>
-cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms, cudaStream_t stream) {
   WdArgs a;
-  a.w = maps.w; a.x = maps.x; a.out = maps.out; a.p = p;
+  a.w = w; a.p = p;
+  // (results in boxes of 32 rows x 64 columns)
+  if (!fp8_row_map(&a.x, xq, p.T, p.K, xq_stride, 128) ||
+      !encode_tmap_2d(&a.out, Elem<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out, (uint64_t)p.N,
+                      (uint64_t)p.T, (uint64_t)p.out_stride * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   a.nm = (p.T + 127) / 128;
   a.nn = (p.N + 255) / 256;
   // A group's rows (16 MB at most) stay in L2 while the weights stream past them; more than 64 tiles leave too few weight
@@ -260,21 +263,6 @@ cudaError_t launch(const Fp8LinearParams& p, const Fp8Maps& maps, int num_sms, c
   return cudaLaunchKernelEx(&c, fp8_wide_kernel<T>, a);
 }
 
-// The map of the results in boxes of 32 rows x 64 columns, made anew if it is another than the last one.
-bool out_map(Fp8Maps* maps, const Fp8LinearParams& p, bool bf16) {
-  Fp8Maps::OutKey key;
-  memset(&key, 0, sizeof(key));
-  key.out = p.out; key.T = p.T; key.stride = p.out_stride;
-  if (maps->out_valid && memcmp(&key, &maps->out_key, sizeof(key)) == 0) return true;
-  maps->out_valid = false;
-  if (!encode_tmap_2d(&maps->out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out, (uint64_t)p.N,
-                      (uint64_t)p.T, (uint64_t)p.out_stride * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
-    return false;
-  maps->out_key = key;
-  maps->out_valid = true;
-  return true;
-}
-
 }  // namespace
 
 cudaError_t fp8_wide_prepare() {
@@ -291,10 +279,9 @@ cudaError_t fp8_wide_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const void* xq, int xq_stride, Fp8Maps* maps, int num_sms,
+cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                             cudaStream_t stream) {
-  if (!fp8_row_map(maps, xq, p.T, p.K, xq_stride, 128) || !out_map(maps, p, bf16)) return cudaErrorInvalidValue;
-  return bf16 ? launch<__nv_bfloat16>(p, *maps, num_sms, stream) : launch<__half>(p, *maps, num_sms, stream);
+  return bf16 ? launch<__nv_bfloat16>(p, w, xq, xq_stride, num_sms, stream) : launch<__half>(p, w, xq, xq_stride, num_sms, stream);
 }
 
 }  // namespace mla

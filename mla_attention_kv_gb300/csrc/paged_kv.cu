@@ -22,8 +22,8 @@
 // the worker that finishes last (its being last changes nothing in the result).
 // More: by a second kernel, which spreads them over the GPU.  64 sequences of
 // up to 4096 keys, 16 heads, one row each: 177 us, 182 with the second kernel;
-// 12 rows per head in 20 pieces: 45 us with it, 69 without; 4 rows 37 and 42.  The products
-// run on mma.sync, in one of two forms:
+// 12 rows per head in 20 pieces: 45 us with it, 69 without; 4 rows 37 and 42.
+// The products run on mma.sync, in one of two forms:
 //   up to 8 rows: S^T = K Q^T and O^T = V^T P^T, keys and value columns being
 //     the 16 rows of an operand and the query rows its 8 columns.  P^T turns
 //     from result to operand by a transposing move.  Half the products of the
@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
 //   l = sum u_i l_i,  out = sum u_i o_i / l,  lse = (m + log2 l) * ln 2.
 // `per` warps (1, 2, 4, 8 or 16) share a record's rows, a warp taking one row at a
 // time with 16 pieces in flight.  Bound by latency, so the grid is what fits
-// on the GPU at once: with a block for each eight possible rows 12 sequences
-// with 12 rows per head took 47 us instead of 39.
+// on the GPU at once: a block for each eight possible rows costs 12 sequences
+// with 12 rows per head 8 us more.
 template <typename T>
 __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constant__ PagedKvParams p, int per, int R) {
   using E = Elem<T>;
@@ -575,66 +575,66 @@ __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constan
   // (neighbouring records to a group: a long item leaves one record in many, at even distances)
   const int groups = gridDim.x * 8 / per, each = (p.plan.workers + groups - 1) / groups, first = (blockIdx.x * 8 + warp) / per * each;
   for (int c0 = 0; c0 < each; c0 += 32) {
-   // (a lane looks at a record: most of them are empty)
-   const int mine = first + c0 + lane;
-   PagedJoin rec = {0, 0, 0, 0};
-   if (c0 + lane < each && mine < p.plan.workers) rec = p.plan.joins[mine];
-   const bool fits = rec.rows > 0 && rec.rows <= R && rec.row >= 0 && (long long)rec.row + rec.rows <= (long long)p.plan.T * G &&
+    // (a lane looks at a record: most of them are empty)
+    const int mine = first + c0 + lane;
+    PagedJoin rec = {0, 0, 0, 0};
+    if (c0 + lane < each && mine < p.plan.workers) rec = p.plan.joins[mine];
+    const bool fits = rec.rows > 0 && rec.rows <= R && rec.row >= 0 && (long long)rec.row + rec.rows <= (long long)p.plan.T * G &&
                      rec.pad >= 0 && rec.pad < p.kv_heads && rec.last_worker >= mine && rec.last_worker < p.plan.workers;
-   for (uint32_t left = __ballot_sync(~0u, fits); left; left &= left - 1) {
-    const int from = __ffs(left) - 1, w1 = first + c0 + from;
-    const PagedJoin j = {__shfl_sync(~0u, rec.row, from), __shfl_sync(~0u, rec.rows, from), __shfl_sync(~0u, rec.last_worker, from),
-                         __shfl_sync(~0u, rec.pad, from)};
-    const int n = j.last_worker - w1 + 1;
-    auto slot = [&](int i) { return (size_t)(w1 + i) * 2 + (i == 0 ? 1 : 0); };
-    for (int r = (blockIdx.x * 8 + warp) % per; r < j.rows; r += per) {
-      const int tok = (j.row + r) / G;
-      const size_t orow = (size_t)tok * H + j.pad * G + (j.row + r) - tok * G;
-      auto ml = [&](int i) { return i < n ? reinterpret_cast<const float2*>(p.plan.part_ml)[slot(i) * R + r] : make_float2(-INFINITY, 0.f); };
-      float m = -INFINITY;
-      for (int i = lane; i < n; i += 32) {
-        const float2 a = ml(i);
-        if (a.y != 0.f) m = fmaxf(m, a.x);
-      }
+    for (uint32_t left = __ballot_sync(~0u, fits); left; left &= left - 1) {
+      const int from = __ffs(left) - 1, w1 = first + c0 + from;
+      const PagedJoin j = {__shfl_sync(~0u, rec.row, from), __shfl_sync(~0u, rec.rows, from), __shfl_sync(~0u, rec.last_worker, from),
+                           __shfl_sync(~0u, rec.pad, from)};
+      const int n = j.last_worker - w1 + 1;
+      auto slot = [&](int i) { return (size_t)(w1 + i) * 2 + (i == 0 ? 1 : 0); };
+      for (int r = (blockIdx.x * 8 + warp) % per; r < j.rows; r += per) {
+        const int tok = (j.row + r) / G;
+        const size_t orow = (size_t)tok * H + j.pad * G + (j.row + r) - tok * G;
+        auto ml = [&](int i) { return i < n ? reinterpret_cast<const float2*>(p.plan.part_ml)[slot(i) * R + r] : make_float2(-INFINITY, 0.f); };
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) {
+          const float2 a = ml(i);
+          if (a.y != 0.f) m = fmaxf(m, a.x);
+        }
 #pragma unroll
-      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const float2 a = ml(i0 + lane);
-        const float f = a.y == 0.f ? 0.f : exp2f(a.x - m);
-        l += f * a.y;
-        const int end = min(32, n - i0);
-        for (int j0 = 0; j0 < end; j0 += kJoinFlight) {
-          float4 y[kJoinFlight];
-          float u[kJoinFlight];
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          const float2 a = ml(i0 + lane);
+          const float f = a.y == 0.f ? 0.f : exp2f(a.x - m);
+          l += f * a.y;
+          const int end = min(32, n - i0);
+          for (int j0 = 0; j0 < end; j0 += kJoinFlight) {
+            float4 y[kJoinFlight];
+            float u[kJoinFlight];
 #pragma unroll
-          for (int k = 0; k < kJoinFlight; ++k) {
-            // (all loads are made, those past the end of the last piece: under a condition each would wait for the one
-            // before.  A piece without keys has zeros.)
-            const int i = min(j0 + k, end - 1);
-            u[k] = __shfl_sync(~0u, f, i);
-            if (j0 + k >= end) u[k] = 0.f;
-            y[k] = reinterpret_cast<const float4*>(p.plan.part_o + (slot(i0 + i) * R + r) * kV)[lane];
-          }
+            for (int k = 0; k < kJoinFlight; ++k) {
+              // (all loads are made, those past the end of the last piece: under a condition each would wait for the one
+              // before.  A piece without keys has zeros.)
+              const int i = min(j0 + k, end - 1);
+              u[k] = __shfl_sync(~0u, f, i);
+              if (j0 + k >= end) u[k] = 0.f;
+              y[k] = reinterpret_cast<const float4*>(p.plan.part_o + (slot(i0 + i) * R + r) * kV)[lane];
+            }
 #pragma unroll
-          for (int k = 0; k < kJoinFlight; ++k) {
-            o.x += u[k] * y[k].x;
-            o.y += u[k] * y[k].y;
-            o.z += u[k] * y[k].z;
-            o.w += u[k] * y[k].w;
+            for (int k = 0; k < kJoinFlight; ++k) {
+              o.x += u[k] * y[k].x;
+              o.y += u[k] * y[k].y;
+              o.z += u[k] * y[k].z;
+              o.w += u[k] * y[k].w;
+            }
           }
         }
-      }
 #pragma unroll
-      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-      const float iv = l == 0.f ? 0.f : 1.f / l;
-      const float4 vs = p.v_scale ? reinterpret_cast<const float4*>(p.v_scale + j.pad * kV)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
-      reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
-          make_uint2(E::pack(o.x * iv * vs.x, o.y * iv * vs.y), E::pack(o.z * iv * vs.z, o.w * iv * vs.w));
-      if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+        const float iv = l == 0.f ? 0.f : 1.f / l;
+        const float4 vs = p.v_scale ? reinterpret_cast<const float4*>(p.v_scale + j.pad * kV)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
+        reinterpret_cast<uint2*>(static_cast<T*>(p.plan.out) + orow * kV)[lane] =
+            make_uint2(E::pack(o.x * iv * vs.x, o.y * iv * vs.y), E::pack(o.z * iv * vs.z, o.w * iv * vs.w));
+        if (p.plan.lse && lane == 0) p.plan.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
     }
-   }
   }
 }
 

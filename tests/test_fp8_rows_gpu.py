@@ -113,6 +113,15 @@ def test_many_rows_and_another_stream():
     assert torch.equal(s, rs.t()) and torch.equal(q.float(), ref.to(E4).float())
 
 
+def test_more_rows_than_a_grid_has_in_its_second_dimension():
+    T, K = 65535 * 16 + 21, 32
+    x = torch.randn(T, K, generator=gen(2), device="cuda").to(torch.bfloat16)
+    _, q, s = outputs(T, K)
+    B.mla_fp8_quant_rows(x, q, s)
+    ref, rs = quantise(x.float())
+    assert torch.equal(s, rs.t()) and torch.equal(q.float(), ref.to(E4).float())
+
+
 def test_no_rows():
     B.mla_fp8_quant_rows(torch.empty(0, 128, dtype=torch.float16, device="cuda"), torch.empty(0, 128, device="cuda").to(E4),
                          torch.empty(1, 0, device="cuda"))

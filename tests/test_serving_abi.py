@@ -55,6 +55,7 @@ def packed(struct, base, **over):
     (dict(n=-1), 1), (dict(n=(1 << 30) + 1), 1), (dict(T=-1), 1), (dict(T=17), 3), (dict(page=0), 1), (dict(nb=0), 1), (dict(ts=-1), 1),
     (dict(page=1 << 16, nb=1 << 16), 1), (dict(new=0), 1), (dict(lens=0), 1), (dict(table=0), 1), (dict(free=0), 1),
     (dict(count=0), 1), (dict(lens_out=0), 1), (dict(count_out=0), 1), (dict(cu=0), 1), (dict(slots=0), 1), (dict(pos=0), 1),
+    (dict(page=1, nb=(1 << 31) - 65535), 1), (dict(T=(1 << 31) - 65535), 1),
     (dict(new=0x5000008), 4), (dict(ended=0x5000004), 4), (dict(cu=0x5000004), 4), (dict(slots=0x5000008), 4),
 ])
 def test_plan_refusals(L, over, code):
@@ -62,7 +63,7 @@ def test_plan_refusals(L, over, code):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(n=-1), 1), (dict(T=-2), 1), (dict(T=17, n=17), 3), (dict(T=3), 1), (dict(page=0), 1), (dict(nb=-1), 1), (dict(ts=-1), 1),
+    (dict(n=-1), 1), (dict(n=(1 << 30) + 1, cu=fake()), 1), (dict(T=-2), 1), (dict(T=17, n=17), 3), (dict(T=3), 1), (dict(page=0), 1), (dict(nb=-1), 1), (dict(ts=-1), 1),
     (dict(page=1 << 16, nb=1 << 15), 1), (dict(qn=0), 1), (dict(qp=0), 1), (dict(lens=0), 1), (dict(table=0), 1), (dict(k=0), 1),
     (dict(v=0), 1), (dict(e=0), 1), (dict(out=0), 1), (dict(ks=fake()), 1), (dict(vs=fake()), 1), (dict(ks=fake(), es=fake()), 1),
     (dict(qn_t=120), 1), (dict(qn_h=100), 1), (dict(qp_t=63), 1), (dict(qp_h=0), 1), (dict(k_bs=0), 1), (dict(k_hs=130), 1),
@@ -79,7 +80,7 @@ def test_paged_kv_refusals(L, over, code):
     (dict(T=-1), 1), (dict(K=0), 1), (dict(K=-16), 1), (dict(K=264), 2), (dict(dtype=2), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
     (dict(x=0), 1), (dict(q=0), 1), (dict(scale=0), 1), (dict(xs=255), 1), (dict(xs=248), 1), (dict(xs=260), 1), (dict(qs=264), 1),
     (dict(qs=240), 1), (dict(x=0x5000008), 4), (dict(gamma=0x5000002), 4), (dict(q=0x5000004), 4), (dict(scale=0x5000008), 4),
-    (dict(T=0, x=0), 0),
+    (dict(T=0, x=0), 0), (dict(T=(1 << 31) - 65535), 2), (dict(K=(1 << 31) - 65520, xs=(1 << 31) - 65520, qs=(1 << 31) - 65520), 2),
 ])
 def test_fp8_rows_refusals(L, over, code):
     assert L.mla_fp8_quant_rows(packed(B._FP8_ROWS_ARGS, ROWS, **over), None) == code, over
@@ -94,6 +95,8 @@ def linear_cfg(**over):
 @pytest.mark.parametrize("over,w,s,code", [
     (dict(in_features=0), 16, 16, 1), (dict(out_features=-8), 16, 16, 1), (dict(max_tokens=0), 16, 16, 1), (dict(dtype=2), 16, 16, 1),
     (dict(), 0, 16, 1), (dict(), 16, 0, 1), (dict(in_features=264), 16, 16, 2), (dict(out_features=260), 16, 16, 2),
+    (dict(in_features=(1 << 31) - 65520), 16, 16, 2), (dict(out_features=65535 * 128 + 8), 16, 16, 2),
+    (dict(max_tokens=(1 << 31) - 65535), 16, 16, 2),
     (dict(), 24, 16, 4), (dict(), 16, 20, 4),
 ])
 def test_linear_create_refusals(L, over, w, s, code):
