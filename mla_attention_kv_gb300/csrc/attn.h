@@ -118,6 +118,7 @@ struct PagedKvParams {
   int k_rs, v_rs, kpe_rs;
   int qn_ts, qn_hs, qp_ts, qp_hs;
   int kv_heads;
+  int item_cost;  // width of an item beyond its key tiles (its queries, its result)
   int join_here;  // pieces of an item are joined by the worker that finishes last, else by a second kernel
 };
 // Query rows per KV head and sequence (with ragged chunks the average, which

@@ -11,12 +11,10 @@
 namespace mla {
 
 constexpr int kKvTile = 32;
-// Width of an item beyond its key tiles (its queries, its result).
-constexpr int kKvItemCost = 1;
 
 __host__ __device__ __forceinline__ Seq kv_seq(const PagedKvParams& p, int s, int R, bool report) {
   Seq q = plan_seq(p.plan, s, R, report);
-  q.first = q.last = kKvItemCost;
+  q.first = q.last = p.item_cost;
   if (q.items > 0) {
     q.first += (q.keys_of_item(0, R, p.plan.heads) + kKvTile - 1) / kKvTile;
     q.last += (q.keys_of_item(q.items - 1, R, p.plan.heads) + kKvTile - 1) / kKvTile;
@@ -68,7 +66,7 @@ __host__ __device__ __forceinline__ int kv_workers(long long total, int W) {
 
 // A place in the list of items: sequence, KV head, item, and the item's cost range.
 struct KvCursor {
-  int s, head, j;
+  int s, head, j, own;  // (own: item_cost)
   Seq q;
   long long seq_base, head_cost;
   long long lo, hi;
@@ -82,6 +80,7 @@ struct KvCursor {
   }
   __host__ __device__ __forceinline__ void open(const PagedKvParams& p, int ss, int R) {
     s = ss;
+    own = p.item_cost;
     q = kv_seq(p, ss, R, false);
     head_cost = q.cum(q.items);
   }
@@ -129,9 +128,9 @@ struct KvCursor {
   }
   // Key tile that position x of this item (lo <= x <= hi) stands for.
   __host__ __device__ __forceinline__ int tile_at(long long x, int tiles) const {
-    const long long d = hi - lo - kKvItemCost;
+    const long long d = hi - lo - own;
     if (d < 1) return x < hi ? 0 : tiles;
-    const long long y = x - lo - kKvItemCost;
+    const long long y = x - lo - own;
     if (y <= 0) return 0;
     const long long n = y * tiles;
     return n < (1ll << 31) ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
