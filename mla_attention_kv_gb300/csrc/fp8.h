@@ -34,18 +34,12 @@ struct Fp8LinearParams {
   unsigned long long budget_ns;
 };
 // Few rows: weights as the 128-row operand, the K blocks split over a cluster.
-// `cost` (where not null) gets what the kernel would take, in K blocks of time.
-int fp8_narrow_split(const Fp8LinearParams& p, int num_sms, int* cost);
+bool fp8_narrow_is_faster(const Fp8LinearParams& p, int num_sms);
 cudaError_t fp8_narrow_prepare();
 // w: the weight's tensor map, in boxes of 128 rows.
 cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                               cudaStream_t stream);
 // Many rows: persistent CTAs on tiles of 128 rows x 256 weight rows.
-inline int fp8_wide_cost(const Fp8LinearParams& p, int num_sms) {
-  const long long tiles = (long long)((p.T + 127) / 128) * ((p.N + 255) / 256), blocks = (p.K + kFp8Block - 1) / kFp8Block;
-  const long long c = (tiles + num_sms - 1) / num_sms * blocks * 3;
-  return c < 0x7fffffff ? (int)c : 0x7fffffff;
-}
 cudaError_t fp8_wide_prepare();
 cudaError_t fp8_wide_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,
                             cudaStream_t stream);

@@ -167,10 +167,8 @@ mla_status mla_fp8_linear_run(mla_fp8_linear* h, const mla_fp8_linear_args* args
   }
   p.w_scale = h->w_scale; p.out = a.out; p.status = h->status; p.T = a.T; p.K = K; p.N = N;
   p.out_stride = a.T > 1 ? a.out_stride : N; p.budget_ns = h->budget_ns;
-  int narrow_cost = 0;
-  fp8_narrow_split(p, h->num_sms, &narrow_cost);
-  e = narrow_cost <= fp8_wide_cost(p, h->num_sms) ? fp8_narrow_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream)
-                                                  : fp8_wide_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream);
+  e = fp8_narrow_is_faster(p, h->num_sms) ? fp8_narrow_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream)
+                                          : fp8_wide_launch(bf16, p, h->w, xq, xq_stride, h->num_sms, stream);
   if (e != cudaSuccess) return fail(e, "fp8 linear launch");
   ++h->last_launches;
   return MLA_OK;
