@@ -128,7 +128,7 @@ inline long long paged_kv_rows(const PagedKvParams& p) {
 }
 inline bool paged_kv_joins_here(long long rows) { return rows <= 2; }
 constexpr int kKvWarps = 8;                 // workers per CTA
-constexpr int kKvRows = 16, kKvRowsT = 8;   // query rows of an item, and in the kernel for few rows
+constexpr int kKvRows = 16, kKvRowsT = 8, kKvRowsSplit = 4;  // query rows of an item, and in the kernels for few rows
 inline int paged_kv_workers(int num_sms) { return num_sms * kKvWarps; }
 cudaError_t paged_kv_prepare(bool bf16);
 cudaError_t paged_kv_launch(bool bf16, bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream);

@@ -23,22 +23,29 @@
 // More: by a second kernel, which spreads them over the GPU.  64 sequences of
 // up to 4096 keys, 16 heads, one row each: 177 us, 182 with the second kernel;
 // 12 rows per head in 20 pieces: 45 us with it, 69 without; 4 rows 37 and 42.
-// The products run on mma.sync, in one of two forms:
+// The products run on mma.sync, in one of three forms:
 //   up to 8 rows: S^T = K Q^T and O^T = V^T P^T, keys and value columns being
 //     the 16 rows of an operand and the query rows its 8 columns.  P^T turns
 //     from result to operand by a transposing move.  Half the products of the
-//     other form, and 32 registers of output instead of 64;
+//     last form, and 32 registers of output instead of 64;
+//   int8, up to 4 rows: the same with the queries' high parts in columns 0-3 and
+//     their low parts in columns 4-7, so that a key is multiplied once for
+//     both (16 sequences of up to 4096 keys, 128 heads: 182 us, 186 without);
 //   up to 16 rows (16-bit caches): S = Q K^T and O = P V.
 // Eight warps per SM: eleven, which the first form has room for, bring more
 // pieces to join and no more bandwidth (64 sequences of up to 4096 keys, 16
 // heads: 182 us and 181).
 //
-// int8: codes become fp16 exactly (byte ^ 0x80 as the low byte of 1024 + u,
-// minus 1152).  The scaled queries are split in two fp16 parts, high and low,
-// multiplied one after the other into the same sums, so the products see them
-// to about 2^-22.  A thread's four consecutive codes of a key are four columns
-// of one k-step in an order of its own, and the queries are laid out in the
-// same order.
+// int8: the scaled queries are split in two fp16 parts, high and low, so the
+// products see them to about 2^-22.  Codes become fp16 exactly and at the cost
+// of the integer pipe alone, which bounds this form beside the bytes: in the
+// scores as (code + 128) 2^-24, the low byte of an fp16 without exponent, and
+// 128 times the queries' sum comes off a score at its end (a sum's
+// intermediate values are at most 255 / 127 times as large for it); for the
+// values, whose sums are long, byte ^ 0x80 as the low byte of 1024 + u, minus
+// 1152.  A thread's four consecutive codes of a key are four columns of one
+// k-step in an order of its own, and the queries are laid out in the same
+// order.
 #include "attn.h"
 #include "attn_tc.cuh"
 #include "paged_kv_plan.cuh"
@@ -55,10 +62,15 @@ constexpr int kKvThreads = kKvWarps * 32;
 constexpr int kKvSmem = kKvWarps * kWarpBytes + (int)sizeof(PlanShared);
 static_assert(kKvSmem <= 227 * 1024, "shared memory");
 
-// kT: up to 8 query rows per item.
-template <bool kI8, bool kT>
+// kForm: how the products are made.
+enum KvForm {
+  kWide,   // up to 16 query rows per item
+  kTrans,  // up to 8, transposed
+  kSplit,  // int8, up to 4: columns 0-3 are the queries' high parts, columns 4-7 their low parts
+};
+template <bool kI8, KvForm kForm>
 struct KvCfg {
-  static constexpr int R = kT ? kKvRowsT : kKvRows;
+  static constexpr int R = kForm == kWide ? kKvRows : kForm == kTrans ? kKvRowsT : kKvRowsSplit;
   static constexpr int E = kI8 ? 1 : 2;        // bytes per value
   static constexpr int Keys = kI8 ? 32 : 16;   // per stage
   static constexpr int CK = kNope * E / 16;    // 16-byte chunks of a key (and value) row
@@ -82,6 +94,11 @@ __device__ __forceinline__ uint32_t kv_half2(uint32_t biased, uint32_t selector)
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Two of them as (code + 128) 2^-24: the low byte of an fp16 without exponent,
+// which the matrix pipe multiplies exactly.  (A byte move: under a mask and a
+// second constant 16 sequences of up to 4096 keys, 128 heads take 193 us, so 182.)
+__device__ __forceinline__ uint32_t kv_tiny2(uint32_t biased, uint32_t selector) { return __byte_perm(biased, 0, selector); }
 
 // The 8 x 8 matrix of 16-bit values that a warp holds (lane = row * 4 + pair), transposed.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -143,11 +160,12 @@ __device__ __forceinline__ float4 kv_join_row(const PagedParams& p, int n, Piece
 
 // kWhole: pages are multiples of 16 rows, so that each 16 rows of a stage lie
 // in one page.
-template <typename T, bool kI8, bool kT, bool kWhole>
+template <typename T, bool kI8, KvForm kForm, bool kWhole>
 __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_constant__ PagedKvParams p) {
   using E = Elem<T>;
-  using S = KvCfg<kI8, kT>;
-  static_assert(kT || !kI8, "int8: 8 rows");
+  using S = KvCfg<kI8, kForm>;
+  constexpr bool kT = kForm != kWide, kTwo = kForm == kSplit;
+  static_assert(kI8 ? kT : !kTwo, "int8 is transposed");
   constexpr int R = S::R;
   constexpr bool kBf16 = !kI8 && E::kBf16;  // (codes are multiplied as fp16)
   extern __shared__ __align__(128) unsigned char smem[];
@@ -288,8 +306,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       qn = static_cast<const T*>(p.q_nope) + (long long)(sq.begin + tok) * p.qn_ts + (long long)hd * p.qn_hs;
       qp = static_cast<const T*>(p.q_pe) + (long long)(sq.begin + tok) * p.qp_ts + (long long)hd * p.qp_hs;
     };
-    uint32_t qf[12][kT && !kI8 ? 2 : 4];
-    float row_scale[2] = {p.plan.scale_log2, p.plan.scale_log2};
+    uint32_t qf[12][(kT && !kI8) || kTwo ? 2 : 4];
+    float row_scale[2] = {p.plan.scale_log2, p.plan.scale_log2}, row_shift[2] = {0.f, 0.f};
     if constexpr (!kI8) {
 #pragma unroll
       for (int hf = 0; hf < (kT ? 1 : 2); ++hf) {
@@ -306,10 +324,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       }
     } else {
       // q * scale, brought to a largest magnitude of 2^13 .. 2^14 by a power of two, as high + low fp16 parts
-      float x[48], mx = 0.f;
-      const bool ok = g < live;
+      float x[48], mx = 0.f, sum = 0.f;
+      const int r = kTwo ? g & 3 : g;
+      const bool ok = r < live;
       const T *qn = nullptr, *qp = nullptr;
-      if (ok) q_row(g, qn, qp);
+      if (ok) q_row(r, qn, qp);
 #pragma unroll
       for (int k = 0; k < 12; ++k) {
         const T* src = (k < 8 ? qn + k * 16 : qp + (k - 8) * 16) + 4 * q4;
@@ -326,23 +345,36 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
       const int up = mx > 0.f && mx < INFINITY ? min(13 - ilogbf(mx), 100) : 0;
-      const float f = scalbnf(1.f, up), down = p.plan.scale_log2 * scalbnf(1.f, -up);
-      row_scale[0] = __shfl_sync(~0u, down, 8 * q4);  // rows 2 q4 and 2 q4 + 1 (lane 4 r holds row r)
-      row_scale[1] = __shfl_sync(~0u, down, 8 * q4 + 4);
+      const float f = scalbnf(1.f, up);
 #pragma unroll
       for (int k = 0; k < 12; ++k)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float y0 = x[4 * k + 2 * i] * f, y1 = x[4 * k + 2 * i + 1] * f;
+        for (int i = 0; i < 2; ++i) {  // (codes 0 and 2 of the four, then 1 and 3)
+          const float y0 = x[4 * k + i] * f, y1 = x[4 * k + i + 2] * f;
           const __half2 hi = __floats2half2_rn(y0, y1);
           const float2 hf = __half22float2(hi);
           const __half2 lo = __floats2half2_rn(y0 - hf.x, y1 - hf.y);
-          qf[k][i] = *reinterpret_cast<const uint32_t*>(&hi);
-          qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&lo);
+          const float2 lf = __half22float2(lo);
+          sum += (hf.x + lf.x) + (hf.y + lf.y);
+          if constexpr (kTwo) {
+            qf[k][i] = *reinterpret_cast<const uint32_t*>(g < 4 ? &hi : &lo);
+          } else {
+            qf[k][i] = *reinterpret_cast<const uint32_t*>(&hi);
+            qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&lo);
+          }
         }
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      const float down = p.plan.scale_log2 * scalbnf(1.f, -up);
+      const int ra = kTwo ? 2 * (q4 & 1) : 2 * q4;  // this lane's rows of the softmax (lane 4 r holds row r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row_scale[i] = __shfl_sync(~0u, down, 4 * (ra + i));
+        row_shift[i] = __shfl_sync(~0u, -128.f * sum, 4 * (ra + i));
+      }
     }
     // this lane's two rows of the softmax: 2 q4 and 2 q4 + 1 (kT), g and g + 8
-    const int ra = kT ? 2 * q4 : g, rb = kT ? 2 * q4 + 1 : g + 8;
+    const int ra = kTwo ? 2 * (q4 & 1) : kT ? 2 * q4 : g, rb = kT ? ra + 1 : g + 8;
     const int lim0 = ra < live ? sq.keys_of_row(row0 + ra, G) : 0, lim1 = rb < live ? sq.keys_of_row(row0 + rb, G) : 0;
     const int lim_all = sq.keys_of_row(row0, G);  // keys that all rows see
 
@@ -375,10 +407,14 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
           for (int n = 0; n < 4; ++n) x[n] ^= 0x80808080u;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const uint32_t af[4] = {kv_half2(x[2 * n], 0x4140), kv_half2(x[2 * n + 1], 0x4140), kv_half2(x[2 * n], 0x4342),
-                                    kv_half2(x[2 * n + 1], 0x4342)};
-            mma16816<false>(sc[n], af, qf[k][0], qf[k][1]);
-            mma16816<false>(s2[n], af, qf[k][2], qf[k][3]);
+            const uint32_t af[4] = {kv_tiny2(x[2 * n], 0x4240), kv_tiny2(x[2 * n + 1], 0x4240), kv_tiny2(x[2 * n], 0x4341),
+                                    kv_tiny2(x[2 * n + 1], 0x4341)};
+            if constexpr (kTwo) {
+              mma16816<false>(k & 1 ? s2[n] : sc[n], af, qf[k][0], qf[k][1]);
+            } else {
+              mma16816<false>(sc[n], af, qf[k][0], qf[k][1]);
+              mma16816<false>(s2[n], af, qf[k][2], qf[k][3]);
+            }
           }
         }
       } else if constexpr (kT) {
@@ -407,7 +443,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = (sc[n][i] + s2[n][i]) * row_scale[second(i)];
+        for (int i = 0; i < 4; ++i) {
+          float x = sc[n][i] + s2[n][i];
+          if (kTwo) x += __shfl_xor_sync(~0u, x, 2);  // (high and low parts; both lanes go on with the row)
+          if (kI8) x = fmaf(x, 16777216.f, row_shift[second(i)]);  // (codes entered as (code + 128) 2^-24)
+          sc[n][i] = x * row_scale[second(i)];
+        }
       if ((t + 1) * S::Keys > lim_all) {  // (the same for all lanes)
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -518,6 +559,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
         *reinterpret_cast<float2*>(place + rb * kV + n * 8 + 2 * q4) = make_float2(acc[n][2], acc[n][3]);
       } else {
         const int c0 = n * 16 + (kI8 ? 2 * g : g), c1 = c0 + (kI8 ? 1 : 8);
+        if (kTwo && q4 >= 2) continue;
         place[ra * kV + c0] = acc[n][0];
         place[rb * kV + c0] = acc[n][1];
         place[ra * kV + c1] = acc[n][2];
@@ -615,9 +657,9 @@ __global__ void __launch_bounds__(256) paged_kv_join_kernel(const __grid_constan
   }
 }
 
-template <typename T, bool kI8, bool kT>
+template <typename T, bool kI8, KvForm kForm>
 cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
-  using S = KvCfg<kI8, kT>;
+  using S = KvCfg<kI8, kForm>;
   p.plan.workers = paged_kv_workers(num_sms);
   const long long rows = paged_kv_rows(p);
   p.join_here = paged_kv_joins_here(rows);
@@ -626,9 +668,9 @@ cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
   // sequences of up to 512 keys, 16 heads, one row: 31.9, 31.4, 33.7, 34.9.  16 bits, up to 256 keys: 22.6, 24.2, 25.0.
   p.item_cost = !kI8 ? 1 : p.join_here ? 2 : 3;
   if (p.plan.page % 16 == 0)
-    paged_kv_kernel<T, kI8, kT, true><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
+    paged_kv_kernel<T, kI8, kForm, true><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   else
-    paged_kv_kernel<T, kI8, kT, false><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
+    paged_kv_kernel<T, kI8, kForm, false><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.join_here) return e;
   const int per = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 || S::R == 8 ? 8 : 16;
@@ -645,22 +687,24 @@ cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&c, paged_kv_join_kernel<T>, p, per, S::R);
 }
 
-template <typename T, bool kI8, bool kT>
+template <typename T, bool kI8, KvForm kForm>
 cudaError_t prepare_one() {
-  const cudaError_t e = cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
-  return e == cudaSuccess ? cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem) : e;
+  const cudaError_t e = cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kForm, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+  return e == cudaSuccess ? cudaFuncSetAttribute(paged_kv_kernel<T, kI8, kForm, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem) : e;
 }
 template <typename T>
 cudaError_t prepare() {
-  cudaError_t e = prepare_one<T, false, false>();
-  if (e == cudaSuccess) e = prepare_one<T, false, true>();
-  if (e == cudaSuccess) e = prepare_one<T, true, true>();
+  cudaError_t e = prepare_one<T, false, kWide>();
+  if (e == cudaSuccess) e = prepare_one<T, false, kTrans>();
+  if (e == cudaSuccess) e = prepare_one<T, true, kTrans>();
+  if (e == cudaSuccess) e = prepare_one<T, true, kSplit>();
   return e;
 }
 template <typename T>
 cudaError_t launch_any(bool i8, const PagedKvParams& p, int num_sms, cudaStream_t stream) {
-  if (i8) return launch<T, true, true>(p, num_sms, stream);
-  return paged_kv_rows(p) <= kKvRowsT ? launch<T, false, true>(p, num_sms, stream) : launch<T, false, false>(p, num_sms, stream);
+  const long long rows = paged_kv_rows(p);
+  if (i8) return rows <= kKvRowsSplit ? launch<T, true, kSplit>(p, num_sms, stream) : launch<T, true, kTrans>(p, num_sms, stream);
+  return rows <= kKvRowsT ? launch<T, false, kTrans>(p, num_sms, stream) : launch<T, false, kWide>(p, num_sms, stream);
 }
 
 }  // namespace

@@ -162,6 +162,19 @@ def test_ragged_chunks(layout, i8):
 
 
 @pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("H,KH", [(4, 4), (8, 4), (9, 3)])
+def test_ragged_steps(H, KH, i8):
+    """Few rows per head on average, single sequences with more of them than an item of the kernels for few rows has."""
+    run_case([1, 0, 1, 13, 1, 1, 2, 1], [900, 7, 33, 250, 1, 4000, 65, 18], H, KH, 16, "bf16", seed=H, i8=i8)
+
+
+def test_huge_queries():
+    """int8: no intermediate value leaves the range of fp32 before a score does."""
+    c = run_case([1, 1], [1, 1], 4, 4, 16, "bf16", seed=15, i8=True, qstd=2.0 ** 124)
+    assert torch.isfinite(c.out).all() and torch.isfinite(c.lse).all()
+
+
+@pytest.mark.parametrize("i8", [False, True])
 def test_long_sequences_are_split(i8):
     run_case([1], [40000], 2, 2, 64, "fp16", seed=3, i8=i8)
     run_case([2, 2], [9001, 30000], 16, 4, 32, "bf16", seed=4, i8=i8, cu=False)
