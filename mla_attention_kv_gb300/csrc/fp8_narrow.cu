@@ -52,7 +52,8 @@ struct NwArgs {
   Fp8LinearParams p;
 };
 
-__device__ __forceinline__ float ld_scale(const float* p) {  // (volatile: requested where it stands)
+// A weight scale, which nothing writes during the kernel (volatile: requested where it stands).
+__device__ __forceinline__ float ld_w_scale(const float* p) {
   float v;
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
@@ -159,10 +160,10 @@ __global__ void __launch_bounds__(NwCfg<TN>::kThreads, 2) fp8_narrow_kernel(cons
     const bool mine = lane < kCols && t < p.T;
     const float* xs = p.x_scale + (size_t)b0 * p.T + (mine ? t : 0);
     const float* ws = p.w_scale + (size_t)nt * blocks + b0;
-    float x1 = mine ? ld_scale(xs) : 0.f, w1 = ld_scale(ws), x2 = 0.f, w2 = 0.f;
+    float x1 = mine ? ld_behind_dep(xs) : 0.f, w1 = ld_w_scale(ws), x2 = 0.f, w2 = 0.f;
     if (nb > 1) {
-      x2 = mine ? ld_scale(xs + p.T) : 0.f;
-      w2 = ld_scale(ws + 1);
+      x2 = mine ? ld_behind_dep(xs + p.T) : 0.f;
+      w2 = ld_w_scale(ws + 1);
     }
     for (int i = 0; i < nb; ++i) {
       const int buf = i & 1;
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(NwCfg<TN>::kThreads, 2) fp8_narrow_kernel(cons
       x1 = x2;
       w1 = w2;
       if (i + 2 < nb) {
-        x2 = mine ? ld_scale(xs + (size_t)(i + 2) * p.T) : 0.f;
-        w2 = ld_scale(ws + i + 2);
+        x2 = mine ? ld_behind_dep(xs + (size_t)(i + 2) * p.T) : 0.f;
+        w2 = ld_w_scale(ws + i + 2);
       }
       __syncwarp();
       if (!__all_sync(~0u, mbar_try_wait(bar(&sh->tfull[buf]), (i >> 1) & 1)) &&

@@ -169,13 +169,13 @@ __global__ void __launch_bounds__(kWdThreads, 1) fp8_wide_kernel(const __grid_co
       uint64_t acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = 0;
-      float fx = __ldg(xs), fw = __ldg(ws);
+      float fx = ld_behind_dep(xs), fw = __ldg(ws);
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b, ++s) {
         const float f = fx * fw;
         if (b + 1 < blocks) {
           xs += p.T;
-          fx = __ldg(xs);
+          fx = ld_behind_dep(xs);
           fw = __ldg(ws + b + 1);
         }
         const uint64_t f2 = f2_pack(f, f);
