@@ -30,22 +30,23 @@
 //     last form, and 32 registers of output instead of 64;
 //   int8, up to 4 rows: the same with the queries' high parts in columns 0-3 and
 //     their low parts in columns 4-7, so that a key is multiplied once for
-//     both (16 sequences of up to 4096 keys, 128 heads: 182 us, 186 without);
+//     both (16 sequences of up to 4096 keys, 128 heads: 194 us, 205 without);
 //   up to 16 rows (16-bit caches): S = Q K^T and O = P V.
 // Eight warps per SM: eleven, which the first form has room for, bring more
 // pieces to join and no more bandwidth (64 sequences of up to 4096 keys, 16
 // heads: 182 us and 181).
 //
 // int8: the scaled queries are split in two fp16 parts, high and low, so the
-// products see them to about 2^-22.  Codes become fp16 exactly and at the cost
-// of the integer pipe alone, which bounds this form beside the bytes: in the
-// scores as (code + 128) 2^-24, the low byte of an fp16 without exponent, and
-// 128 times the queries' sum comes off a score at its end (a sum's
-// intermediate values are at most 255 / 127 times as large for it); for the
-// values, whose sums are long, byte ^ 0x80 as the low byte of 1024 + u, minus
-// 1152.  A thread's four consecutive codes of a key are four columns of one
-// k-step in an order of its own, and the queries are laid out in the same
-// order.
+// products see them to about 2^-22.  Codes become fp16 exactly (byte ^ 0x80 as
+// the low byte of 1024 + u, minus 1152), so a sum is never larger than the
+// products in it, whatever part of their range the codes use.  Scores of codes
+// that keep an offset, code + 128, with 128 times the queries' sum taken off at
+// the end, are 12 us faster (16 sequences of up to 4096 keys, 128 heads: 182 us,
+// 194 so), but their sums are (|code| + 128) / |code| times as large, and with codes
+// of 0 and 1 a score is off by several hundred 2^-23 of sum |q k|.  The integer
+// pipe and these moves bound this form beside the bytes.  A thread's four
+// consecutive codes of a key are four columns of one k-step in an order of its
+// own, and the queries are laid out in the same order.
 #include "attn.h"
 #include "attn_tc.cuh"
 #include "paged_kv_plan.cuh"
@@ -94,11 +95,6 @@ __device__ __forceinline__ uint32_t kv_half2(uint32_t biased, uint32_t selector)
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// Two of them as (code + 128) 2^-24: the low byte of an fp16 without exponent,
-// which the matrix pipe multiplies exactly.  (A byte move: under a mask and a
-// second constant 16 sequences of up to 4096 keys, 128 heads take 193 us, so 182.)
-__device__ __forceinline__ uint32_t kv_tiny2(uint32_t biased, uint32_t selector) { return __byte_perm(biased, 0, selector); }
 
 // The 8 x 8 matrix of 16-bit values that a warp holds (lane = row * 4 + pair), transposed.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -307,7 +303,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       qp = static_cast<const T*>(p.q_pe) + (long long)(sq.begin + tok) * p.qp_ts + (long long)hd * p.qp_hs;
     };
     uint32_t qf[12][(kT && !kI8) || kTwo ? 2 : 4];
-    float row_scale[2] = {p.plan.scale_log2, p.plan.scale_log2}, row_shift[2] = {0.f, 0.f};
+    float row_scale[2] = {p.plan.scale_log2, p.plan.scale_log2};
     if constexpr (!kI8) {
 #pragma unroll
       for (int hf = 0; hf < (kT ? 1 : 2); ++hf) {
@@ -324,7 +320,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
       }
     } else {
       // q * scale, brought to a largest magnitude of 2^13 .. 2^14 by a power of two, as high + low fp16 parts
-      float x[48], mx = 0.f, sum = 0.f;
+      float x[48], mx = 0.f;
       const int r = kTwo ? g & 3 : g;
       const bool ok = r < live;
       const T *qn = nullptr, *qp = nullptr;
@@ -354,8 +350,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
           const __half2 hi = __floats2half2_rn(y0, y1);
           const float2 hf = __half22float2(hi);
           const __half2 lo = __floats2half2_rn(y0 - hf.x, y1 - hf.y);
-          const float2 lf = __half22float2(lo);
-          sum += (hf.x + lf.x) + (hf.y + lf.y);
           if constexpr (kTwo) {
             qf[k][i] = *reinterpret_cast<const uint32_t*>(g < 4 ? &hi : &lo);
           } else {
@@ -363,15 +357,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
             qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&lo);
           }
         }
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
       const float down = p.plan.scale_log2 * scalbnf(1.f, -up);
       const int ra = kTwo ? 2 * (q4 & 1) : 2 * q4;  // this lane's rows of the softmax (lane 4 r holds row r)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        row_scale[i] = __shfl_sync(~0u, down, 4 * (ra + i));
-        row_shift[i] = __shfl_sync(~0u, -128.f * sum, 4 * (ra + i));
-      }
+      for (int i = 0; i < 2; ++i) row_scale[i] = __shfl_sync(~0u, down, 4 * (ra + i));
     }
     // this lane's two rows of the softmax: 2 q4 and 2 q4 + 1 (kT), g and g + 8
     const int ra = kTwo ? 2 * (q4 & 1) : kT ? 2 * q4 : g, rb = kT ? ra + 1 : g + 8;
@@ -407,8 +396,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
           for (int n = 0; n < 4; ++n) x[n] ^= 0x80808080u;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const uint32_t af[4] = {kv_tiny2(x[2 * n], 0x4240), kv_tiny2(x[2 * n + 1], 0x4240), kv_tiny2(x[2 * n], 0x4341),
-                                    kv_tiny2(x[2 * n + 1], 0x4341)};
+            const uint32_t af[4] = {kv_half2(x[2 * n], 0x4240), kv_half2(x[2 * n + 1], 0x4240), kv_half2(x[2 * n], 0x4341),
+                                    kv_half2(x[2 * n + 1], 0x4341)};
             if constexpr (kTwo) {
               mma16816<false>(k & 1 ? s2[n] : sc[n], af, qf[k][0], qf[k][1]);
             } else {
@@ -446,7 +435,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
         for (int i = 0; i < 4; ++i) {
           float x = sc[n][i] + s2[n][i];
           if (kTwo) x += __shfl_xor_sync(~0u, x, 2);  // (high and low parts; both lanes go on with the row)
-          if (kI8) x = fmaf(x, 16777216.f, row_shift[second(i)]);  // (codes entered as (code + 128) 2^-24)
           sc[n][i] = x * row_scale[second(i)];
         }
       if ((t + 1) * S::Keys > lim_all) {  // (the same for all lanes)
@@ -664,8 +652,8 @@ cudaError_t launch(PagedKvParams p, int num_sms, cudaStream_t stream) {
   const long long rows = paged_kv_rows(p);
   p.join_here = paged_kv_joins_here(rows);
   // What beginning and ending an item takes, in tiles of 32 keys, which a warp goes through in 3.3 us with 16 bits and 1.5
-  // with int8.  int8, 16 sequences of up to 8192 keys, 8 heads: 8 rows 57.6, 46.7, 42.2, 41.6 us with 1, 2, 3, 4; 64
-  // sequences of up to 512 keys, 16 heads, one row: 31.9, 31.4, 33.7, 34.9.  16 bits, up to 256 keys: 22.6, 24.2, 25.0.
+  // with int8.  int8, 16 sequences of up to 8192 keys, 8 heads: 8 rows 58.6, 47.3, 42.3, 41.8 us with 1, 2, 3, 4; 64
+  // sequences of up to 512 keys, 16 heads, one row: 33.0, 31.7, 33.3, 34.4.  16 bits, up to 256 keys: 22.6, 24.2, 25.0.
   p.item_cost = !kI8 ? 1 : p.join_here ? 2 : 3;
   if (p.plan.page % 16 == 0)
     paged_kv_kernel<T, kI8, kForm, true><<<num_sms, kKvThreads, kKvSmem, stream>>>(p);
