@@ -617,6 +617,8 @@ typedef struct mla_page_plan_args {
  * packed in sequence order.
  *   free_blocks [num_blocks] int32: a stack, entries 0 .. free_count - 1 are
  *            blocks that no sequence holds, the next one handed out last
+ *   kv_lens  what the last plan gave as kv_lens_out: lengths that become
+ *            shorter over a page's end need mla_page_plan_held
  *   ended    [num_seqs] int32: where not 0, the sequence's
  *            ceil(kv_lens / page_size) pages go back to the stack first (in
  *            sequence and page order) and its length becomes 0; with new
@@ -643,6 +645,21 @@ typedef struct mla_page_plan_args {
  * page_size > INT_MAX, num_seqs > 2^30, T or num_blocks > 2^31 - 65536),
  * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream);
+
+/* The same for sequences that may become shorter between steps (drafted tokens
+ * that are rejected: the caller lowers kv_lens by them).  A sequence keeps its
+ * pages until it ends, and new ones are taken only past those:
+ *   held     [num_seqs] int32: pages that sequence i holds, the first ones of
+ *            its table row; 0 for one that has not begun
+ *   held_out [num_seqs]: pages it holds after the step (may be held)
+ * An ended sequence gives back held[i] pages.  A count below ceil(kv_lens /
+ * page_size) or above table_stride is clamped (MLA_ERR_BAD_LENGTH).  All else as
+ * for mla_page_plan, which takes a sequence to hold ceil(kv_lens / page_size)
+ * pages: after a length that was lowered over a page's end it hands out
+ * new blocks for those that the table names already, and these are lost.
+ * Errors: as there, and MLA_ERR_INVALID_ARG without held or held_out. */
+mla_status mla_page_plan_held(mla_attn* h, const mla_page_plan_args* args, const int32_t* held,
+                              int32_t* held_out, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * 8-bit floating point next to the int8 building blocks: rows and weights in

@@ -35,7 +35,7 @@ EXPORTED = ["mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
             "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold", "mla_prolog_w8a8_capture",
             "mla_kv_prolog_last_cluster_launches", "mla_attn_create", "mla_attn_destroy", "mla_attn_status",
             "mla_attn_last_launches", "mla_latent_append", "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan",
-            "mla_fp8_quant_rows", "mla_attn_paged_kv_run",
+            "mla_page_plan_held", "mla_fp8_quant_rows", "mla_attn_paged_kv_run",
             "mla_fp8_linear_create", "mla_fp8_linear_destroy", "mla_fp8_linear_status", "mla_fp8_linear_last_launches",
             "mla_fp8_linear_run"]
 
@@ -115,6 +115,7 @@ def load(path: str | None = None):
     L.mla_fp8_linear_status.argtypes = [H, P]
     L.mla_fp8_linear_last_launches.argtypes = [H]
     L.mla_fp8_linear_run.argtypes = [H, P, P]
+    L.mla_page_plan_held.argtypes = [H, P, P, P, P]
     for fn in (L.mla_latent_append, L.mla_attn_paged_run, L.mla_attn_prompt_run, L.mla_page_plan, L.mla_attn_paged_kv_run):
         fn.argtypes = [H, P, P]
     for fn in ("mla_kv_prolog_create", "mla_kv_prolog_run", "mla_prolog_w8a8_run",
@@ -125,7 +126,7 @@ def load(path: str | None = None):
                "mla_kv_prolog_run_paged", "mla_kv_prolog_run_c8", "mla_kv_prolog_auto_threshold",
                "mla_prolog_w8a8_capture", "mla_kv_prolog_last_cluster_launches", "mla_attn_create",
                "mla_attn_destroy", "mla_attn_status", "mla_attn_last_launches", "mla_latent_append",
-               "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan", "mla_fp8_quant_rows",
+               "mla_attn_paged_run", "mla_attn_prompt_run", "mla_page_plan", "mla_page_plan_held", "mla_fp8_quant_rows",
                "mla_attn_paged_kv_run", "mla_fp8_linear_create", "mla_fp8_linear_destroy", "mla_fp8_linear_status",
                "mla_fp8_linear_last_launches", "mla_fp8_linear_run"):
         getattr(L, fn).restype = ctypes.c_int
@@ -683,25 +684,34 @@ class MLAAttention:
         return out
 
     def plan_pages(self, new_lens, kv_lens, block_table, free_blocks, free_count, page_size, cu_q, slot_mapping, positions,
-                   kv_lens_out=None, free_count_out=None, ended=None, stream=None):
+                   kv_lens_out=None, free_count_out=None, ended=None, held=None, held_out=None, stream=None):
         """One step's plan of a paged cache, all int32: new_lens and kv_lens [n], block_table [n, blocks] and the stack
         free_blocks [num_blocks] (both updated), free_count [1], ended [n] or None -> cu_q [n + 1], slot_mapping [T],
-        positions [T], kv_lens_out [n] and free_count_out [1] (None: in place)."""
+        positions [T], kv_lens_out [n] and free_count_out [1] (None: in place).  held [n], updated (or held_out [n] written): pages
+        of each sequence, for lengths that may become shorter between steps; None: ceil(kv_lens / page_size)."""
         i32 = torch.int32
         n, T, nb = new_lens.shape[0], slot_mapping.shape[0], free_blocks.shape[0]
         if block_table.dim() != 2:
             raise ValueError("block_table must have shape [num_seqs, blocks]")
         width = block_table.shape[1]
+        if held is None and held_out is not None:
+            raise ValueError("held_out needs held")
         lens, count = self._flat(kv_lens, i32, n, "kv_lens"), self._flat(free_count, i32, 1, "free_count")
-        code = self._lib.mla_page_plan(self.h, _PLAN_ARGS.pack(
+        args = _PLAN_ARGS.pack(
             self._flat(new_lens, i32, n, "new_lens"), 0 if ended is None else self._flat(ended, i32, n, "ended"), lens,
             self._flat(block_table, i32, n * width, "block_table"), self._flat(free_blocks, i32, nb, "free_blocks"), count,
             lens if kv_lens_out is None else self._flat(kv_lens_out, i32, n, "kv_lens_out"),
             count if free_count_out is None else self._flat(free_count_out, i32, 1, "free_count_out"),
             self._flat(cu_q, i32, n + 1, "cu_q"), self._flat(slot_mapping, i32, T, "slot_mapping"),
-            self._flat(positions, i32, T, "positions"), n, T, width, page_size, nb), self._stream(stream))
+            self._flat(positions, i32, T, "positions"), n, T, width, page_size, nb)
+        if held is None:
+            code = self._lib.mla_page_plan(self.h, args, self._stream(stream))
+        else:
+            hp = self._flat(held, i32, n, "held")
+            code = self._lib.mla_page_plan_held(self.h, args, hp, hp if held_out is None else self._flat(held_out, i32, n, "held_out"),
+                                                self._stream(stream))
         if code:
-            _check(code, "mla_page_plan")
+            _check(code, "mla_page_plan" if held is None else "mla_page_plan_held")
         return slot_mapping
 
 

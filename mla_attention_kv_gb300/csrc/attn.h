@@ -48,6 +48,8 @@ struct PagePlanParams {
   int32_t* cu_q;
   int32_t* slots;
   int32_t* positions;
+  const int32_t* held;  // null: ceil(kv_lens / page)
+  int32_t* held_out;    // may be held; null without held
   unsigned* status;
   int nseq, T, table_stride, page, nblocks;
 };

@@ -37,6 +37,35 @@ namespace {
 // overlapping (the stride of a dimension of size 1 is not read).
 bool stride_ok(int stride, int width, bool used) { return !used || (stride >= width && stride % 8 == 0); }
 
+// A step's plan; held: pages per sequence, where the caller keeps them.
+mla_status plan_pages(mla_attn* h, const mla_page_plan_args* args, const int32_t* held, int32_t* held_out, cudaStream_t stream) {
+  if (!h || !args) return MLA_ERR_INVALID_ARG;
+  const mla_page_plan_args& a = *args;
+  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.T > kMostCount || a.page_size <= 0 || a.num_blocks <= 0 ||
+      a.num_blocks > kMostCount || a.table_stride < 0 || (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
+    return MLA_ERR_INVALID_ARG;
+  h->last_launches = 0;
+  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
+  if (!a.free_blocks || !a.free_count || !a.free_count_out || !a.cu_q || (a.T > 0 && (!a.slot_mapping || !a.positions)) ||
+      (a.num_seqs > 0 && (!a.new_lens || !a.kv_lens || !a.kv_lens_out || (a.table_stride > 0 && !a.block_table))))
+    return MLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.new_lens, a.ended, a.kv_lens, a.block_table, a.free_blocks, a.free_count, a.kv_lens_out,
+                        a.free_count_out, a.cu_q, a.slot_mapping, a.positions, held, held_out};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
+  DeviceGuard g(h->device);
+  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
+  PagePlanParams p = {};
+  p.new_lens = a.new_lens; p.ended = a.ended; p.kv_lens = a.kv_lens; p.table = a.block_table; p.free_blocks = a.free_blocks;
+  p.free_count = a.free_count; p.kv_lens_out = a.kv_lens_out; p.free_count_out = a.free_count_out; p.cu_q = a.cu_q;
+  p.slots = a.slot_mapping; p.positions = a.positions; p.held = held; p.held_out = held_out;
+  p.status = h->status; p.nseq = a.num_seqs; p.T = a.T; p.table_stride = a.table_stride; p.page = a.page_size; p.nblocks = a.num_blocks;
+  cudaError_t e = page_plan_launch(p, stream);
+  if (e != cudaSuccess) return fail(e, "page plan launch");
+  h->last_launches = 1;
+  return MLA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -307,31 +336,12 @@ mla_status mla_attn_prompt_run(mla_attn* h, const mla_attn_prompt_args* args, cu
 }
 
 mla_status mla_page_plan(mla_attn* h, const mla_page_plan_args* args, cudaStream_t stream) {
-  if (!h || !args) return MLA_ERR_INVALID_ARG;
-  const mla_page_plan_args& a = *args;
-  if (a.num_seqs < 0 || a.num_seqs > (1 << 30) || a.T < 0 || a.T > kMostCount || a.page_size <= 0 || a.num_blocks <= 0 ||
-      a.num_blocks > kMostCount || a.table_stride < 0 || (long long)a.page_size * a.num_blocks > 0x7fffffffLL)
-    return MLA_ERR_INVALID_ARG;
-  h->last_launches = 0;
-  if (a.T > h->cfg.max_tokens) return MLA_ERR_TOO_MANY_TOKENS;
-  if (!a.free_blocks || !a.free_count || !a.free_count_out || !a.cu_q || (a.T > 0 && (!a.slot_mapping || !a.positions)) ||
-      (a.num_seqs > 0 && (!a.new_lens || !a.kv_lens || !a.kv_lens_out || (a.table_stride > 0 && !a.block_table))))
-    return MLA_ERR_INVALID_ARG;
-  const void* ptrs[] = {a.new_lens, a.ended, a.kv_lens, a.block_table, a.free_blocks, a.free_count, a.kv_lens_out,
-                        a.free_count_out, a.cu_q, a.slot_mapping, a.positions};
-  for (const void* q : ptrs)
-    if (!aligned16(q)) return MLA_ERR_MISALIGNED;
-  DeviceGuard g(h->device);
-  if (g.err != cudaSuccess) return fail(g.err, "cudaSetDevice");
-  PagePlanParams p = {};
-  p.new_lens = a.new_lens; p.ended = a.ended; p.kv_lens = a.kv_lens; p.table = a.block_table; p.free_blocks = a.free_blocks;
-  p.free_count = a.free_count; p.kv_lens_out = a.kv_lens_out; p.free_count_out = a.free_count_out; p.cu_q = a.cu_q;
-  p.slots = a.slot_mapping; p.positions = a.positions; p.status = h->status; p.nseq = a.num_seqs; p.T = a.T;
-  p.table_stride = a.table_stride; p.page = a.page_size; p.nblocks = a.num_blocks;
-  cudaError_t e = page_plan_launch(p, stream);
-  if (e != cudaSuccess) return fail(e, "page plan launch");
-  h->last_launches = 1;
-  return MLA_OK;
+  return plan_pages(h, args, nullptr, nullptr, stream);
+}
+
+mla_status mla_page_plan_held(mla_attn* h, const mla_page_plan_args* args, const int32_t* held, int32_t* held_out, cudaStream_t stream) {
+  if (args && args->num_seqs > 0 && (!held || !held_out)) return MLA_ERR_INVALID_ARG;
+  return plan_pages(h, args, held, held_out, stream);
 }
 
 }  // extern "C"

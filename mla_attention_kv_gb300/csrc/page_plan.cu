@@ -4,8 +4,10 @@
 // its cache slot and its position.
 //
 // Sequence i with L cached and n new tokens (an ended one: L = 0):
-//   need_i = ceil((L + n) / page) - ceil(L / page),  k_i = sum_{j<i} need_j
+//   need_i = max(0, ceil((L + n) / page) - h),  k_i = sum_{j<i} need_j
 //   its m-th new page is free[count - 1 - (k_i + m)]
+// h being the pages it holds: ceil(L / page), or where the caller keeps counts
+// (sequences that become shorter when drafted tokens are rejected) its count.
 //   row cu_q[i] + j: position L + j, slot = block * page + position % page
 // Two prefix sums over the sequences, then one thread per row and per page
 // that finds its sequence by bisection.  Every order is fixed, so the result
@@ -31,7 +33,7 @@ struct PlShared {
   int begin[kPlThreads + 1];  // first token row of each sequence of the strip
   int k[kPlThreads + 1];      // pages handed out before it (or, in the first pass, taken back)
   int old[kPlThreads];        // cached tokens
-  int first[kPlThreads];      // pages it had
+  int first[kPlThreads];      // pages it held
   int ok[kPlThreads];
   int used;
 };
@@ -90,13 +92,23 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PagePlanPar
     return L;
   };
   auto pages = [&](int L) { return (int)(((unsigned)L + p.page - 1) / (unsigned)p.page); };
+  auto holds = [&](int i, int L) {  // pages of sequence i with L cached tokens
+    const int own = pages(L);
+    if (!p.held) return own;
+    int h = p.held[i];
+    if (h < own || h > p.table_stride) {
+      bad |= kStatusBadLength;
+      h = h < own ? own : p.table_stride;
+    }
+    return h;
+  };
 
   // ---- pages of the sequences that end, in (sequence, page) order onto the stack
   if (p.ended) {
     long long back = 0;
     for (int s0 = 0; s0 < p.nseq; s0 += nt) {
       const int i = s0 + tid;
-      const int give = i < p.nseq && p.ended[i] ? pages(cached(i)) : 0;
+      const int give = i < p.nseq && p.ended[i] ? holds(i, cached(i)) : 0;
       long long total;
       const long long at = pl_scan(sh, 0, give, &total);
       if (total > 0) {  // (the same for all threads)
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PagePlanPar
   for (int s0 = 0; s0 < p.nseq || s0 == 0; s0 += nt) {
     const int i = s0 + tid;
     const int live = min(nt, p.nseq - s0);
-    int n = 0, L = 0;
+    int n = 0, L = 0, first = 0;
     bool ok = false;
     if (i < p.nseq) {
       n = p.new_lens[i];
@@ -143,7 +155,10 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PagePlanPar
         bad |= kStatusBadLength;
         n = 0;
       }
-      L = p.ended && p.ended[i] ? 0 : cached(i);
+      if (!p.ended || !p.ended[i]) {
+        L = cached(i);
+        first = holds(i, L);
+      }
     }
     long long rows, need_all;
     const long long at = row0 + pl_scan(sh, 0, n, &rows);
@@ -152,8 +167,7 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PagePlanPar
       ok = end <= p.T && (long long)L + n <= cap;
       if (!ok) bad |= kStatusBadLength;
     }
-    const int first = pages(L);
-    const int need = ok ? pages(L + n) - first : 0;
+    const int need = ok ? max(0, pages(L + n) - first) : 0;
     const long long k = page0 + pl_scan(sh, 1, need, &need_all);
     if (ok && need > 0 && k + need > count) {
       ok = false;
@@ -170,6 +184,7 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PagePlanPar
     if (ok && need > 0) atomicMax(&sh.used, (int)(k + need));
     if (rank == 0 && i < p.nseq) {
       p.kv_lens_out[i] = ok ? L + n : L;
+      if (p.held) p.held_out[i] = ok ? first + need : first;
       if (i == 0) p.cu_q[0] = 0;
       p.cu_q[i + 1] = (int)(end < p.T ? end : p.T);
     }
