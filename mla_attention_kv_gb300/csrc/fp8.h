@@ -34,7 +34,6 @@ struct Fp8LinearParams {
   unsigned long long budget_ns;
 };
 // Few rows: weights as the 128-row operand, the K blocks split over a cluster.
-bool fp8_narrow_is_faster(const Fp8LinearParams& p, int num_sms);
 cudaError_t fp8_narrow_prepare();
 // w: the weight's tensor map, in boxes of 128 rows.
 cudaError_t fp8_narrow_launch(bool bf16, const Fp8LinearParams& p, const CUtensorMap& w, const void* xq, int xq_stride, int num_sms,

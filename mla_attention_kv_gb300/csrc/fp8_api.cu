@@ -9,6 +9,7 @@
 #include "../../include/mla_prolog.h"
 #include "api_util.cuh"
 #include "fp8.h"
+#include "fp8_plan.h"
 #include "tma.h"
 
 using namespace mla;
