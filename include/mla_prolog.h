@@ -566,8 +566,9 @@ typedef struct mla_attn_paged_kv_args {
 
 /* Attention of the newest tokens of num_seqs sequences over the paged
  * up-projected caches that mla_kv_prolog_run_paged writes, or over int8 codes
- * as mla_kv_prolog_run_c8 makes them (its dense [b, H, s, 128] outputs are a
- * cache of b blocks with pages of s rows):
+ * as mla_kv_prolog_run_c8 makes them (a prompt's dense [b, H, s, 128] outputs
+ * are a cache of b blocks with pages of s rows; a later token's codes, its
+ * outputs with s = 1, are the caller's to copy to their row of the cache):
  *   q_nope [T, H, 128], q_pe [T, H, 64]  dtype (strided; q_pe rotated)
  *   k_cache, v_cache  a block's rows per KV head, KH = num_kv_heads; query
  *            head h reads KV head h / (H / KH).  dtype; with scales int8
