@@ -101,7 +101,10 @@ static const CUtensorMap* wkvb_map(mla_prolog_s* h, const void* W_kvb) {
 
 static thread_local char g_last_cuda_error[256] = "no error";
 
+// Reports an error and takes it from the runtime, so that the next launch that
+// asks does not find it.
 static mla_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s (%d)", what,
            cudaGetErrorString(e), (int)e);
   return MLA_ERR_CUDA;

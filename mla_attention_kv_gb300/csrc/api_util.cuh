@@ -12,7 +12,10 @@ namespace {
 
 using mla::set_error_text;
 
+// Reports an error and takes it from the runtime, so that the next launch that
+// asks does not find it.
 mla_status fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   char text[256];
   snprintf(text, sizeof(text), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
   set_error_text(text);
