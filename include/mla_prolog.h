@@ -588,8 +588,10 @@ typedef struct mla_attn_paged_kv_args {
  * and is reported (MLA_ERR_BAD_SLOT); lengths and offsets out of range are
  * clamped and reported (MLA_ERR_BAD_LENGTH); lengths, offsets and tables must
  * not change while a call runs.  One launch, or two.  Made for few query rows
- * per KV head (n * H / KH up to 16; more rows read the cache once for each 16
- * of them, 8 with int8).  Errors: MLA_ERR_INVALID_ARG (also T % num_seqs != 0
+ * per KV head, which share one read of the cache: 16 of them, or 8 where the
+ * average T / num_seqs * H / KH is at most 8, rows of no sequence counted (int8:
+ * 8, or 4 where it is at most 4).  A sequence with more rows reads the cache
+ * once for each so many of them.  Errors: MLA_ERR_INVALID_ARG (also T % num_seqs != 0
  * without cu_q, num_seqs > 2^30, bad strides, some of the scales only),
  * MLA_ERR_TOO_MANY_TOKENS, MLA_ERR_MISALIGNED, MLA_ERR_CUDA. */
 mla_status mla_attn_paged_kv_run(mla_attn* h, const mla_attn_paged_kv_args* args, cudaStream_t stream);
@@ -704,7 +706,8 @@ typedef struct mla_fp8_linear_s mla_fp8_linear;
  *   weight        [N, K] e4m3, dense ([out, in], as checkpoints store it)
  *   weight_scale  [ceil(N / 128), ceil(K / 128)] f32, dense
  * Both stay the caller's and are read by every run; the handle owns the
- * workspace of quantised rows and a status word.  One handle serves one
+ * workspace of quantised rows (max_tokens * K bytes and a float for each 128
+ * of them, also where every run is given codes) and a status word.  One handle serves one
  * stream at a time, and one host thread (runs given codes use only its
  * status word and may overlap on the device).  Errors:
  * MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (K or N; K or max_tokens > 2^31 -

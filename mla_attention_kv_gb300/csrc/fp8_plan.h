@@ -13,8 +13,10 @@ struct NwPlan {
 // CTAs of a cluster that share a tile's K blocks: as many as leave a block
 // each and two CTAs per SM in all, up to 8, or 4 for tiles of 64 tokens, whose
 // sums are larger (64 x 7168 -> 2112 on tiles of 64: 10.0 us on 4, 11.3 on 8;
-// one row 8.2 on 4, 7.4 on 8).  Cost: the blocks that an SM takes in turn, in
-// units of about 0.15 us: one for a block of up to 32 tokens, two for 64.
+// one row 8.2 on 4, 7.4 on 8).  Cost: the blocks that the busiest SM takes in
+// turn, in units of about 0.15 us: one for a block of up to 32 tokens, two for 64.
+// (Splits are powers of two, so the last doubling may leave some SMs with two
+// CTAs and others with one: 64 x 16384 -> 7168 has 224 on 152 SMs.)
 inline NwPlan plan_for(const Fp8LinearParams& p, int num_sms, int tokens) {
   const int most = tokens == 64 ? 4 : 8;
   const long long blocks = (p.K + kFp8Block - 1) / kFp8Block, tiles = (long long)((p.N + 127) / 128) * ((p.T + tokens - 1) / tokens);

@@ -16,7 +16,9 @@
 // MMAs alone take 231 on a ring of three stages (209 on four, whose room the
 // results' staging takes).  The CTAs do not pair up for the 2-SM MMA, which
 // halves the weight traffic (loads and MMAs alone 151 us) but sends commits
-// and releases across the pair, about 1000 cycles a way: 296 us.
+// and releases across the pair, about 1000 cycles a way.  Pairs took 296 us with
+// eight epilogue warps that store their results themselves; single CTAs took 288 with
+// sixteen such warps.  Pairs with sixteen and results by TMA were not measured.
 //
 // Warps: 0 TMA, 1 tensor memory, 1 and 2 MMA, 4-19 epilogue (3 only gives its
 // registers).
@@ -244,9 +246,10 @@ cudaError_t launch(const Fp8LinearParams& p, const CUtensorMap& w, const void* x
     return cudaErrorInvalidValue;
   a.nm = (p.T + 127) / 128;
   a.nn = (p.N + 255) / 256;
-  // A group's rows (16 MB at most) stay in L2 while the weights stream past them; more than 64 tiles leave too few weight
-  // tiles at work at a time.  8192 x 1536 -> 24576: 241 us in one group of 64, 254 in groups of 24; 16384 x 7168 -> 2112:
-  // 211 in groups of 24, 261 in one of 128; 16384 x 512 -> 32768: 281 in groups of 64, 323 in one of 128.
+  // A group's rows (16 MB, or eight tiles where these are more: K > 16384) stay in L2 while the weights stream past them; more
+  // than 64 tiles leave too few weight tiles at work at a time.  8192 x 1536 -> 24576: 238 us in one group of 64, as here,
+  // 253 in groups of 18; 16384 x 7168 -> 2112: 222 in groups of 18, as here, 199 of 24, 247 of 64, 265 in one of 128; 16384 x
+  // 512 -> 32768: 280-291 in groups of 64, as here, 290-299 of 24, 311-314 in one of 128.
   const long long fit = (1ll << 24) / (128ll * p.K);
   a.group = fit < 8 ? 8 : fit > 64 ? 64 : (int)fit;
   const long long tiles = (long long)a.nm * a.nn;

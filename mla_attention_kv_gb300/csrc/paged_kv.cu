@@ -36,6 +36,13 @@
 // pieces to join and no more bandwidth (64 sequences of up to 4096 keys, 16
 // heads: 182 us and 181).
 //
+// The softmax weights enter the second product in 16 bits (the type of the
+// caches, fp16 with int8), which is the one rounding on the way; sums, maxima
+// and results in progress have 32.  With a second part for what the rounding
+// leaves, that product would be made twice; so the results' error against 64
+// bits is 0.00024 with fp16 and 0.0021 with bf16, where 32-bit weights have 0.0002 and
+// 0.0017, the rounding of the result itself.
+//
 // int8: the scaled queries are split in two fp16 parts, high and low, so the
 // products see them to about 2^-22.  Codes become fp16 exactly (byte ^ 0x80 as
 // the low byte of 1024 + u, minus 1152), so a sum is never larger than the
@@ -163,7 +170,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) paged_kv_kernel(const __grid_co
   constexpr bool kT = kForm != kWide, kTwo = kForm == kSplit;
   static_assert(kI8 ? kT : !kTwo, "int8 is transposed");
   constexpr int R = S::R;
-  constexpr bool kBf16 = !kI8 && E::kBf16;  // (codes are multiplied as fp16)
   extern __shared__ __align__(128) unsigned char smem[];
   PlanShared* plan = reinterpret_cast<PlanShared*>(smem + kKvWarps * kWarpBytes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
